@@ -9,8 +9,21 @@ kernels.  PyTorch provides device memory and streams.
     logprob, entropy, lse = lmhead_fwd(hidden, weight, targets, mask, spans, num_spans)
     dhidden, dweight = lmhead_bwd(g_logprob, g_entropy, hidden, weight, targets, mask,
                                   spans, num_spans, lse, entropy)
+
+Around the LM head: the embedding lookup and its gradient, the residual RMS
+norm (bf16 or fp32, with e4m3 codes for lmhead_fwd_fp8) and its backward, and
+the clipping of all gradients by their global norm.
+
+    x = embed_fwd(ids, table, scale)
+    y, y_e4m3, y_scale, s = rmsnorm_fwd(x, norm_weight, eps, residual=r, mask=mask,
+                                        want_e4m3=True)
+    ds, dnorm_weight = rmsnorm_bwd(dhidden, s, norm_weight, eps, mask=mask)
+    embed_bwd(ids, ds, V, scale, accumulate=True, dweight=dweight)   # tied weights
+    norm = clip_grad_norm([dweight, dnorm_weight], max_norm)
 """
 from __future__ import annotations
+
+import ctypes
 
 import torch
 
@@ -26,6 +39,9 @@ __all__ = [
     "fused_logprob_entropy", "trace_enable", "trace_read", "lmhead_fwd_shard",
     "lmhead_combine_shards", "lmhead_bwd_shard", "cp_local_layout", "quantize_rows_e4m3",
     "lmhead_fwd_fp8", "lmhead_bwd_fp8", "lmhead_bwd_fp8_workspace_size",
+    "rmsnorm_fwd", "rmsnorm_bwd", "rmsnorm_bwd_workspace_size", "FusedRMSNorm", "fused_rmsnorm",
+    "embed_fwd", "embed_bwd", "embed_bwd_workspace_size", "FusedEmbedding", "fused_embedding",
+    "clip_grad_norm", "clip_grad_norm_workspace_size",
 ]
 
 
@@ -363,7 +379,6 @@ def trace_enable(on: bool = True) -> None:
 
 def trace_read() -> list[tuple[str, float]]:
     """(kernel name, milliseconds) of every launch recorded since trace_enable(True)."""
-    import ctypes
     lib = _lib.load()
     n = lib.eas_trace_read(None, None, 0)
     kinds = (ctypes.c_int32 * max(n, 1))()
@@ -412,3 +427,281 @@ def fused_logprob_entropy(hidden, weight, targets, mask, spans=None, num_spans=N
         return lp, ent
     return FusedLMHeadLogprob.apply(hidden, weight, targets, mask, spans, num_spans, flags,
                                     vocab_chunk)
+
+
+# ------------------------------------------------- operators around the LM head
+
+def _row_code(t: torch.Tensor, name: str) -> int:
+    """dtype code of a row operator's tensor; refuses what no kernel can read."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on a CUDA device, got {t.device}")
+    if t.dtype == torch.bfloat16:
+        return EAS_BF16
+    if t.dtype == torch.float32:
+        return EAS_FP32
+    raise TypeError(f"{name} must be bfloat16 or float32, got {t.dtype}")
+
+
+def _need_shape(t: torch.Tensor, name: str, dtype: torch.dtype, device, shape) -> None:
+    _need(t, name, dtype, device)
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def rmsnorm_fwd(x, weight, eps: float = 1e-6, residual=None, mask=None, want_y: bool = True,
+                want_e4m3: bool = False, want_sum: bool = True, out=None):
+    """RMS norm of x + residual ([R, H], bf16 or fp32) times weight [H].
+
+    Returns (y, y_e4m3, y_scale, s): y in x's dtype (None without want_y), its
+    e4m3 codes and row scales as lmhead_fwd_fp8 takes them (None without
+    want_e4m3), and s = x + residual, which rmsnorm_bwd takes (x itself without
+    a residual; None without want_sum).  Rows whose mask byte is 0 get y = 0,
+    zero codes and scale 1.  out: buffers for the four, None where one is to be
+    allocated; s may be x or residual itself."""
+    code = _row_code(x, "x")
+    dev, dt = x.device, x.dtype
+    if x.dim() != 2:
+        raise ValueError("x must be [R, H]")
+    R, H = x.shape
+    _need(x, "x", dt, dev)
+    _need_shape(weight, "weight", dt, dev, (H,))
+    if residual is not None:
+        _need_shape(residual, "residual", dt, dev, x.shape)
+    if mask is not None:
+        _need_shape(mask, "mask", torch.uint8, dev, (R,))
+    y, q, scale, s = out if out is not None else (None, None, None, None)
+    if not want_y:
+        y = None
+    elif y is None:
+        y = torch.empty_like(x)
+    else:
+        _need_shape(y, "y", dt, dev, x.shape)
+    if not want_e4m3:
+        q = scale = None
+    else:
+        if q is None:
+            q = torch.empty((R, H), dtype=torch.uint8, device=dev)
+        else:
+            q = _as_codes(q)
+            _need_shape(q, "y_e4m3", torch.uint8, dev, x.shape)
+        if scale is None:
+            scale = torch.empty(R, dtype=torch.float32, device=dev)
+        else:
+            _need_shape(scale, "y_scale", torch.float32, dev, (R,))
+    if residual is None or not want_sum:
+        s = None
+    elif s is None:
+        s = torch.empty_like(x)
+    else:
+        _need_shape(s, "s", dt, dev, x.shape)
+    _lib.check(_lib.load().eas_rmsnorm_fwd(
+        _ptr(x), _ptr(residual), _ptr(weight), _ptr(mask), R, H, code, eps, _ptr(s), _ptr(y),
+        _ptr(q), _ptr(scale), _stream(dev)))
+    return y, q, scale, (x if residual is None and want_sum else s)
+
+
+def rmsnorm_bwd_workspace_size(R: int, H: int) -> int:
+    return int(_lib.load().eas_rmsnorm_bwd_workspace_size(R, H))
+
+
+def rmsnorm_bwd(dy, s, weight, eps: float = 1e-6, ds=None, mask=None, ws=None, dx=None,
+                dweight=None):
+    """Gradients of rmsnorm_fwd's y: (dx in s's dtype, dweight fp32).
+
+    s is the forward's sum; dx is the gradient of x and of the residual alike.
+    ds, the gradient arriving at s from elsewhere, is added to dx (and may be
+    the dx buffer).  Inactive rows' dx is ds or 0."""
+    code = _row_code(s, "s")
+    dev, dt = s.device, s.dtype
+    if s.dim() != 2:
+        raise ValueError("s must be [R, H]")
+    R, H = s.shape
+    _need(s, "s", dt, dev)
+    _need_shape(dy, "dy", dt, dev, s.shape)
+    _need_shape(weight, "weight", dt, dev, (H,))
+    if ds is not None:
+        _need_shape(ds, "ds", dt, dev, s.shape)
+    if mask is not None:
+        _need_shape(mask, "mask", torch.uint8, dev, (R,))
+    if dx is None:
+        dx = torch.empty_like(s)
+    else:
+        _need_shape(dx, "dx", dt, dev, s.shape)
+    if dweight is None:
+        dweight = torch.empty(H, dtype=torch.float32, device=dev)
+    else:
+        _need_shape(dweight, "dweight", torch.float32, dev, (H,))
+    if ws is None:
+        ws = workspace(rmsnorm_bwd_workspace_size(R, H), dev)
+    _lib.check(_lib.load().eas_rmsnorm_bwd(
+        _ptr(dy), _ptr(s), _ptr(weight), _ptr(ds), _ptr(mask), R, H, code, eps, _ptr(dx),
+        _ptr(dweight), _ptr(ws), ws.numel(), _stream(dev)))
+    return dx, dweight
+
+
+def embed_fwd(ids, table, scale: float = 1.0, ws=None, out=None):
+    """scale * table[ids] ([T, H] in table's dtype); id -1 is padding (a zero row).
+
+    Other ids outside the table give zero rows and, where ws (16 bytes or
+    more) is passed, EAS_ERR_INVALID_ARG in its status word."""
+    code = _row_code(table, "table")
+    dev, dt = table.device, table.dtype
+    if table.dim() != 2:
+        raise ValueError("table must be [V, H]")
+    V, H = table.shape
+    _need(table, "table", dt, dev)
+    _need(ids, "ids", torch.int32, dev)
+    T = ids.numel()
+    if out is None:
+        out = torch.empty((T, H), dtype=dt, device=dev)
+    else:
+        _need_shape(out, "out", dt, dev, (T, H))
+    _lib.check(_lib.load().eas_embed_fwd(
+        _ptr(ids), _ptr(table), T, H, V, code, scale, _ptr(out), _ptr(ws),
+        0 if ws is None else ws.numel(), _stream(dev)))
+    return out
+
+
+def embed_bwd_workspace_size(T: int, H: int, V: int) -> int:
+    return int(_lib.load().eas_embed_bwd_workspace_size(T, H, V))
+
+
+def embed_bwd(ids, dout, V: int, scale: float = 1.0, accumulate: bool = False, ws=None,
+              dweight=None):
+    """Gradient of embed_fwd's table: fp32 [V, H], summed in a fixed order.
+
+    With accumulate the sums are added to dweight (tied weights: lmhead_bwd's),
+    else every row of it is written."""
+    code = _row_code(dout, "dout")
+    dev, dt = dout.device, dout.dtype
+    if dout.dim() != 2:
+        raise ValueError("dout must be [T, H]")
+    T, H = dout.shape
+    _need(dout, "dout", dt, dev)
+    _need(ids, "ids", torch.int32, dev)
+    if ids.numel() != T:
+        raise ValueError("ids must have T entries")
+    if dweight is None:
+        if accumulate:
+            raise ValueError("accumulate needs dweight")
+        dweight = torch.empty((V, H), dtype=torch.float32, device=dev)
+    else:
+        _need_shape(dweight, "dweight", torch.float32, dev, (V, H))
+    if ws is None:
+        ws = workspace(embed_bwd_workspace_size(T, H, V), dev)
+    _lib.check(_lib.load().eas_embed_bwd(
+        _ptr(ids), _ptr(dout), T, H, V, code, scale, 1 if accumulate else 0, _ptr(dweight),
+        _ptr(ws), ws.numel(), _stream(dev)))
+    return dweight
+
+
+def clip_grad_norm_workspace_size(n: int) -> int:
+    return int(_lib.load().eas_clip_grad_norm_workspace_size(n))
+
+
+def clip_grad_norm(grads, max_norm: float | None, out=None, ws=None, norm=None):
+    """Scales gradients by min(1, max_norm / (norm + 1e-6)), norm being the
+    2-norm over all of them, and returns norm (fp32 [1], on the device).
+
+    grads: contiguous bf16 or fp32 tensors.  out: None scales in place; else one
+    tensor for each gradient, of its shape, bf16 or fp32 (an fp32 gradient
+    clipped into the bf16 one that an optimiser reads).  max_norm None computes
+    the norm alone.  Where the norm is not finite nothing is scaled."""
+    grads = list(grads)
+    outs = grads if out is None else list(out)
+    if len(outs) != len(grads):
+        raise ValueError("out must have one tensor for each gradient")
+    if not grads:
+        raise ValueError("no gradients")
+    codes = [_row_code(g, "grads") for g in grads]
+    dev = grads[0].device
+    for g in grads:
+        if g.device != dev:
+            raise ValueError(f"gradient on {g.device}, expected {dev}")
+        if not g.is_contiguous():
+            raise ValueError("gradients must be contiguous")
+    out_codes = codes
+    if out is not None:
+        out_codes = [_row_code(o, "out") for o in outs]
+        for g, o in zip(grads, outs):
+            if o.device != dev or o.shape != g.shape or not o.is_contiguous():
+                raise ValueError("out must be contiguous and have the gradients' shapes and device")
+    n = len(grads)
+    ptrs, i32 = ctypes.c_void_p * n, ctypes.c_int32 * n
+    if norm is None:
+        norm = torch.empty(1, dtype=torch.float32, device=dev)
+    else:
+        _need_shape(norm, "norm", torch.float32, dev, (1,))
+    if ws is None:
+        ws = workspace(clip_grad_norm_workspace_size(n), dev)
+    clip = max_norm is not None
+    _lib.check(_lib.load().eas_clip_grad_norm(
+        ptrs(*[g.data_ptr() for g in grads]), ptrs(*[o.data_ptr() for o in outs]) if clip else None,
+        (ctypes.c_int64 * n)(*[g.numel() for g in grads]), i32(*codes), i32(*out_codes), n,
+        max_norm if clip else 0.0, _ptr(norm), _ptr(ws), ws.numel(), _stream(dev)))
+    return norm
+
+
+def _grad_rows(g: torch.Tensor) -> torch.Tensor:
+    """An upstream gradient as the kernels read it: dense, on a 16-byte boundary
+    (autograd hands over broadcast and offset views)."""
+    g = g.contiguous()
+    return g if g.data_ptr() % 16 == 0 else g.clone()
+
+
+class FusedRMSNorm(torch.autograd.Function):
+    """Autograd wrapper of rmsnorm_fwd / rmsnorm_bwd: (y, s, y_e4m3, y_scale).
+
+    The codes and scales carry no gradient: the LM head's e4m3 backward
+    projects with the unquantised rows."""
+
+    @staticmethod
+    def forward(ctx, x, residual, weight, mask, eps, want_e4m3):
+        y, q, scale, s = rmsnorm_fwd(x, weight, eps, residual, mask, want_e4m3=want_e4m3)
+        ctx.save_for_backward(s, weight, mask)
+        ctx.eps, ctx.has_residual = eps, residual is not None
+        ctx.set_materialize_grads(False)
+        if want_e4m3:
+            ctx.mark_non_differentiable(q, scale)
+        return y, (s if residual is not None else None), q, scale
+
+    @staticmethod
+    def backward(ctx, g_y, g_s, _q, _scale):
+        s, weight, mask = ctx.saved_tensors
+        if g_y is None:
+            dx, dw = g_s, None
+        else:
+            ds = None if g_s is None else _grad_rows(g_s)
+            dx, dw = rmsnorm_bwd(_grad_rows(g_y), s, weight, ctx.eps, ds, mask)
+            dw = dw.to(weight.dtype)
+        return dx, (dx if ctx.has_residual else None), dw, None, None, None
+
+
+def fused_rmsnorm(x, weight, residual=None, eps: float = 1e-6, mask=None,
+                  want_e4m3: bool = False):
+    """Differentiable RMS norm of x (+ residual): (y, s, y_e4m3, y_scale), s being
+    None without a residual, the codes and scales None without want_e4m3."""
+    return FusedRMSNorm.apply(x, residual, weight, mask, eps, want_e4m3)
+
+
+class FusedEmbedding(torch.autograd.Function):
+    """Autograd wrapper of embed_fwd / embed_bwd; the table's gradient is
+    returned in the table's dtype."""
+
+    @staticmethod
+    def forward(ctx, ids, table, scale):
+        ctx.save_for_backward(ids)
+        ctx.V, ctx.dtype, ctx.scale = table.shape[0], table.dtype, scale
+        return embed_fwd(ids, table, scale)
+
+    @staticmethod
+    def backward(ctx, g):
+        ids, = ctx.saved_tensors
+        return None, embed_bwd(ids, _grad_rows(g), ctx.V, ctx.scale).to(ctx.dtype), None
+
+
+def fused_embedding(ids, table, scale: float = 1.0):
+    """Differentiable scale * table[ids] ([T, H]); id -1 is padding."""
+    return FusedEmbedding.apply(ids, table, scale)

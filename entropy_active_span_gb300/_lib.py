@@ -30,6 +30,7 @@ EAS_STATIC_SCRATCH_BYTES = 64 << 20
 
 # name -> (restype, argtypes), in the order of include/eas.h
 _P, _I64, _I32, _U32, _SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_uint32, ctypes.c_size_t
+_F32 = ctypes.c_float
 SIGNATURES = {
     "eas_spans_workspace_size": (_SZ, [_I64]),
     "eas_build_active_spans": (ctypes.c_int, [_P, _I64, _I32, _P, _I64, _P, _P, _SZ, _P]),
@@ -55,6 +56,18 @@ SIGNATURES = {
                                             _P, _P, _P, _SZ, _P]),
     "eas_lmhead_fwd_noalloc": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I64,
                                               ctypes.c_int, _U32, _P, _P, _P, _P]),
+    "eas_rmsnorm_fwd": (ctypes.c_int, [_P, _P, _P, _P, _I64, _I64, ctypes.c_int, _F32, _P, _P, _P,
+                                       _P, _P]),
+    "eas_rmsnorm_bwd_workspace_size": (_SZ, [_I64, _I64]),
+    "eas_rmsnorm_bwd": (ctypes.c_int, [_P, _P, _P, _P, _P, _I64, _I64, ctypes.c_int, _F32, _P, _P,
+                                       _P, _SZ, _P]),
+    "eas_embed_fwd": (ctypes.c_int, [_P, _P, _I64, _I64, _I64, ctypes.c_int, _F32, _P, _P, _SZ,
+                                     _P]),
+    "eas_embed_bwd_workspace_size": (_SZ, [_I64, _I64, _I64]),
+    "eas_embed_bwd": (ctypes.c_int, [_P, _P, _I64, _I64, _I64, ctypes.c_int, _F32, _I32, _P, _P,
+                                     _SZ, _P]),
+    "eas_clip_grad_norm_workspace_size": (_SZ, [_I32]),
+    "eas_clip_grad_norm": (ctypes.c_int, [_P, _P, _P, _P, _P, _I32, _F32, _P, _P, _SZ, _P]),
     "eas_selftest_wait_timeout": (ctypes.c_int, [_I64, _P, _SZ, _P]),
     "eas_read_device_status": (ctypes.c_int, [_P, _P]),
     "eas_trace_enable": (None, [_I32]),

@@ -6,13 +6,11 @@
 
 #include "eas_device.cuh"
 #include "eas_kernels.h"
+#include "eas_vec.cuh"
 
 namespace eas {
 
 namespace {
-
-__device__ __forceinline__ float to_f32(float x) { return x; }
-__device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
 
 template <typename In>
 __global__ void __launch_bounds__(256)

@@ -1,0 +1,493 @@
+// Root-mean-square norm of rows with the residual's addition, and its backward.
+//
+//   s = x + r,  rstd = 1 / sqrt(mean(s^2) + eps),  y = (s w) rstd,
+//   q = e4m3(y inv), inv = 448 / amax, scale = amax / 448, amax = max |y|.
+// (s w) rstd is monotonic in |s w| for a row's rstd, so amax = max |s w| * rstd
+// is the largest |y| to the bit, and the row's two statistics, sum s^2 and
+// max |s w|, come from one pass and one block reduction.
+//
+// Backward, with g = dy w and n = s rstd:
+//   dx = ds + rstd (g - s rstd^2 / H sum(g s)),   dw = sum over rows of dy n.
+// rstd is recomputed from s (its row is read anyway), so the gradient is that
+// of the stored s and nothing but s is kept from the forward.
+//
+// All of it is bound by bytes: about 10 operations an element.
+#include <cuda_fp8.h>
+
+#include "eas_device.cuh"
+#include "eas_kernels.h"
+#include "eas_vec.cuh"
+
+namespace eas {
+
+namespace {
+
+// Rows below this amax are stored as zeros with scale 1: 448 / amax would
+// leave the fp32 range (2^-117 * 2^117 * 448 is still finite).
+constexpr float kTinyAmax = 6.0185e-36f;   // 2^-117
+
+struct RowScale {
+  float scale, inv;
+};
+
+__device__ __forceinline__ RowScale row_scale(float amax) {
+  if (!(amax >= kTinyAmax)) return {1.f, amax > 0.f ? 0.f : 1.f};
+  return {__fdiv_rn(amax, 448.f), __fdiv_rn(448.f, amax)};
+}
+
+template <int VEC>
+__device__ __forceinline__ void store_e4m3(uint8_t* p, const float (&y)[VEC], float inv) {
+  if constexpr (VEC == 1) {
+    *p = static_cast<uint8_t>(__nv_cvt_float_to_fp8(__fmul_rn(y[0], inv), __NV_SATFINITE, __NV_E4M3));
+  } else {
+    uint32_t w[VEC / 4];
+#pragma unroll
+    for (int i = 0; i < VEC / 4; ++i) {
+      const uint32_t lo = __nv_cvt_float2_to_fp8x2(
+          make_float2(__fmul_rn(y[4 * i], inv), __fmul_rn(y[4 * i + 1], inv)), __NV_SATFINITE, __NV_E4M3);
+      const uint32_t hi = __nv_cvt_float2_to_fp8x2(
+          make_float2(__fmul_rn(y[4 * i + 2], inv), __fmul_rn(y[4 * i + 3], inv)), __NV_SATFINITE, __NV_E4M3);
+      w[i] = lo | (hi << 16);
+    }
+    if constexpr (VEC == 8)
+      *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+    else
+      *reinterpret_cast<uint32_t*>(p) = w[0];
+  }
+}
+
+// Combines (a, b) over the G threads of a row: a by sum, b by sum or maximum.
+// A group is a warp (G = 32, no barrier) or the whole CTA; `red` alternates
+// with the row's parity, so one barrier a row is enough.
+template <bool kMaxB>
+__device__ __forceinline__ void reduce_pair(float& a, float& b, float2* red, int warps) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    a += __shfl_xor_sync(0xffffffffu, a, o);
+    const float t = __shfl_xor_sync(0xffffffffu, b, o);
+    b = kMaxB ? fmaxf(b, t) : b + t;
+  }
+  if (warps == 1) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (lane == 0) red[warp] = make_float2(a, b);
+  __syncthreads();
+  const float2 v = lane < warps ? red[lane] : make_float2(0.f, 0.f);
+  a = v.x;
+  b = v.y;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    a += __shfl_xor_sync(0xffffffffu, a, o);
+    const float t = __shfl_xor_sync(0xffffffffu, b, o);
+    b = kMaxB ? fmaxf(b, t) : b + t;
+  }
+}
+
+// ------------------------------------------------------------------ forward
+
+// One row by blockDim.x threads, blockDim.y rows a CTA (blockDim.y > 1 only
+// where a warp holds a row).  The row stays in registers: NV vectors of VEC
+// elements a thread, thread-contiguous so that every access is coalesced.
+template <typename T, int VEC, int NV>
+__global__ void __launch_bounds__(1024)
+rmsnorm_fwd_kernel(const RmsNormFwdArgs p) {
+  __shared__ float2 red[32];
+  const long long row = static_cast<long long>(blockIdx.x) * blockDim.y + threadIdx.y;
+  if (row >= p.R) return;   // whole warps: a group of several warps is the CTA
+  const T* x = static_cast<const T*>(p.x) + row * p.H;
+  const T* r = p.r ? static_cast<const T*>(p.r) + row * p.H : nullptr;
+  const T* w = static_cast<const T*>(p.w);
+  const bool active = !p.mask || p.mask[row] != 0;
+
+  float s[NV][VEC];
+  if (active || (r && p.s_out)) {
+    Raw<T, VEC> rx[NV], rr[NV];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = (j * blockDim.x + threadIdx.x) * VEC;
+      if (c < p.H) {
+        rx[j] = load_raw<T, VEC>(x + c);
+        if (r) rr[j] = load_raw<T, VEC>(r + c);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = (j * blockDim.x + threadIdx.x) * VEC;
+      if (c < p.H) {
+        widen<T, VEC>(rx[j], s[j]);
+        if (r) {
+          float t[VEC];
+          widen<T, VEC>(rr[j], t);
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) s[j][i] += t[i];
+          // the stored sum is rounded once; the norm goes on with the fp32 sum
+          if (p.s_out) store_vec<T, VEC>(static_cast<T*>(p.s_out) + row * p.H + c, s[j]);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) s[j][i] = 0.f;
+      }
+    }
+  }
+  if (!active) {
+    const float z[VEC] = {};
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = (j * blockDim.x + threadIdx.x) * VEC;
+      if (c < p.H) {
+        if (p.y) store_vec<T, VEC>(static_cast<T*>(p.y) + row * p.H + c, z);
+        if (p.q) store_e4m3<VEC>(p.q + row * p.H + c, z, 1.f);
+      }
+    }
+    if (p.q && threadIdx.x == 0) p.scale[row] = 1.f;
+    return;
+  }
+  float ss = 0.f, mx = 0.f;
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int c = (j * blockDim.x + threadIdx.x) * VEC;
+    if (c < p.H) {
+      float wf[VEC];
+      widen<T, VEC>(load_raw<T, VEC>(w + c), wf);
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) {
+        ss = fmaf(s[j][i], s[j][i], ss);
+        s[j][i] *= wf[i];
+        mx = fmaxf(mx, fabsf(s[j][i]));
+      }
+    }
+  }
+  reduce_pair<true>(ss, mx, red, blockDim.x >> 5);
+  const float rstd = rsqrtf(ss / static_cast<float>(p.H) + p.eps);
+  const RowScale rs = row_scale(mx * rstd);
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int c = (j * blockDim.x + threadIdx.x) * VEC;
+    if (c < p.H) {
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) s[j][i] *= rstd;
+      if (p.y) store_vec<T, VEC>(static_cast<T*>(p.y) + row * p.H + c, s[j]);
+      if (p.q) store_e4m3<VEC>(p.q + row * p.H + c, s[j], rs.inv);
+    }
+  }
+  if (p.q && threadIdx.x == 0) p.scale[row] = rs.scale;
+}
+
+// Rows too long for the registers of a CTA: two walks over the row, the second
+// from L2 (a row of 2^20 fp32 elements is 4 MB).  One CTA of 1024 threads a
+// row, element by element.  x and r are read again in the second walk, after s
+// may have replaced one of them, so with r it reads what it needs first and
+// stores s last, each thread its own elements.
+template <typename T>
+__global__ void __launch_bounds__(1024)
+rmsnorm_fwd_long_kernel(const RmsNormFwdArgs p) {
+  __shared__ float2 red[32];
+  const long long row = blockIdx.x;
+  const T* x = static_cast<const T*>(p.x) + row * p.H;
+  const T* r = p.r ? static_cast<const T*>(p.r) + row * p.H : nullptr;
+  const T* w = static_cast<const T*>(p.w);
+  T* so = p.s_out ? static_cast<T*>(p.s_out) + row * p.H : nullptr;
+  const bool active = !p.mask || p.mask[row] != 0;
+  float ss = 0.f, mx = 0.f;
+  if (active) {
+    for (int c = threadIdx.x; c < p.H; c += blockDim.x) {
+      const float s = to_f32(x[c]) + (r ? to_f32(r[c]) : 0.f);
+      ss = fmaf(s, s, ss);
+      mx = fmaxf(mx, fabsf(s * to_f32(w[c])));
+    }
+    reduce_pair<true>(ss, mx, red, blockDim.x >> 5);
+  }
+  const float rstd = rsqrtf(ss / static_cast<float>(p.H) + p.eps);
+  const RowScale rs = active ? row_scale(mx * rstd) : RowScale{1.f, 1.f};
+  for (int c = threadIdx.x; c < p.H; c += blockDim.x) {
+    float y[1] = {0.f};
+    if (active || (r && so)) {
+      const float s[1] = {to_f32(x[c]) + (r ? to_f32(r[c]) : 0.f)};
+      if (active) y[0] = s[0] * to_f32(w[c]) * rstd;
+      if (r && so) store_vec<T, 1>(so + c, s);
+    }
+    if (p.y) store_vec<T, 1>(static_cast<T*>(p.y) + row * p.H + c, y);
+    if (p.q) store_e4m3<1>(p.q + row * p.H + c, y, rs.inv);
+  }
+  if (p.q && threadIdx.x == 0) p.scale[row] = rs.scale;
+}
+
+// ----------------------------------------------------------------- backward
+
+// A CTA walks rows blockIdx.x, blockIdx.x + gridDim.x, ... (blockDim.y rows at a
+// time where a warp holds a row); each thread keeps its columns' share of dw
+// in registers and adds it to the CTA's row of `partial` at the end.  The
+// number of partial rows and the order of every sum depend on the shape and
+// the machine only, so results repeat to the bit.
+template <typename T, int VEC, int NV>
+__global__ void __launch_bounds__(1024)
+rmsnorm_bwd_kernel(const RmsNormBwdArgs p) {
+  __shared__ float2 red[2][32];
+  const T* w = static_cast<const T*>(p.w);
+  Raw<T, VEC> rw[NV];
+  float acc[NV][VEC];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int c = (j * blockDim.x + threadIdx.x) * VEC;
+    if (c < p.H) rw[j] = load_raw<T, VEC>(w + c);
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) acc[j][i] = 0.f;
+  }
+  const float inv_h = 1.f / static_cast<float>(p.H);
+  int parity = 0;
+  const long long step = static_cast<long long>(gridDim.x) * blockDim.y;
+  for (long long row = static_cast<long long>(blockIdx.x) * blockDim.y + threadIdx.y; row < p.R;
+       row += step) {
+    const T* ds = p.ds ? static_cast<const T*>(p.ds) + row * p.H : nullptr;
+    T* dx = static_cast<T*>(p.dx) + row * p.H;
+    if (p.mask && p.mask[row] == 0) {   // the same for every thread of the group
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int c = (j * blockDim.x + threadIdx.x) * VEC;
+        if (c < p.H) {
+          float d[VEC] = {};
+          if (ds) widen<T, VEC>(load_raw<T, VEC>(ds + c), d);
+          store_vec<T, VEC>(dx + c, d);
+        }
+      }
+      continue;
+    }
+    const T* dy = static_cast<const T*>(p.dy) + row * p.H;
+    const T* sp = static_cast<const T*>(p.s) + row * p.H;
+    Raw<T, VEC> rdy[NV], rsv[NV], rds[NV];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = (j * blockDim.x + threadIdx.x) * VEC;
+      if (c < p.H) {
+        rdy[j] = load_raw<T, VEC>(dy + c);
+        rsv[j] = load_raw<T, VEC>(sp + c);
+        if (ds) rds[j] = load_raw<T, VEC>(ds + c);
+      }
+    }
+    float ss = 0.f, gs = 0.f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = (j * blockDim.x + threadIdx.x) * VEC;
+      if (c < p.H) {
+        float s[VEC], d[VEC], wf[VEC];
+        widen<T, VEC>(rsv[j], s);
+        widen<T, VEC>(rdy[j], d);
+        widen<T, VEC>(rw[j], wf);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+          ss = fmaf(s[i], s[i], ss);
+          gs = fmaf(d[i] * wf[i], s[i], gs);
+        }
+      }
+    }
+    reduce_pair<false>(ss, gs, red[parity], blockDim.x >> 5);
+    parity ^= 1;
+    const float rstd = rsqrtf(fmaf(ss, inv_h, p.eps));
+    const float c2 = gs * rstd * rstd * inv_h;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = (j * blockDim.x + threadIdx.x) * VEC;
+      if (c < p.H) {
+        float s[VEC], d[VEC], wf[VEC], o[VEC] = {};
+        widen<T, VEC>(rsv[j], s);
+        widen<T, VEC>(rdy[j], d);
+        widen<T, VEC>(rw[j], wf);
+        if (ds) widen<T, VEC>(rds[j], o);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+          o[i] = fmaf(rstd, fmaf(-s[i], c2, d[i] * wf[i]), o[i]);
+          acc[j][i] = fmaf(d[i], s[i] * rstd, acc[j][i]);
+        }
+        store_vec<T, VEC>(dx + c, o);
+      }
+    }
+  }
+  // one partial row a group: blockIdx.x * blockDim.y + threadIdx.y
+  float* out = p.partial + (static_cast<long long>(blockIdx.x) * blockDim.y + threadIdx.y) * p.H;
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int c = (j * blockDim.x + threadIdx.x) * VEC;
+    if (c < p.H) store_vec<float, VEC == 1 ? 1 : 4>(out + c, *reinterpret_cast<float(*)[VEC == 1 ? 1 : 4]>(&acc[j][0]));
+    if constexpr (VEC == 8)
+      if (c < p.H) store_vec<float, 4>(out + c + 4, *reinterpret_cast<float(*)[4]>(&acc[j][4]));
+  }
+}
+
+// Rows too long for registers: dx in two walks of the row, the row's rstd
+// kept for the dw pass.
+template <typename T>
+__global__ void __launch_bounds__(1024)
+rmsnorm_bwd_long_kernel(const RmsNormBwdArgs p) {
+  __shared__ float2 red[32];
+  const long long row = blockIdx.x;
+  const T* dy = static_cast<const T*>(p.dy) + row * p.H;
+  const T* sp = static_cast<const T*>(p.s) + row * p.H;
+  const T* w = static_cast<const T*>(p.w);
+  const T* ds = p.ds ? static_cast<const T*>(p.ds) + row * p.H : nullptr;
+  T* dx = static_cast<T*>(p.dx) + row * p.H;
+  const bool active = !p.mask || p.mask[row] != 0;
+  float ss = 0.f, gs = 0.f;
+  if (active) {
+    for (int c = threadIdx.x; c < p.H; c += blockDim.x) {
+      const float s = to_f32(sp[c]);
+      ss = fmaf(s, s, ss);
+      gs = fmaf(to_f32(dy[c]) * to_f32(w[c]), s, gs);
+    }
+    reduce_pair<false>(ss, gs, red, blockDim.x >> 5);
+  }
+  const float inv_h = 1.f / static_cast<float>(p.H);
+  const float rstd = rsqrtf(fmaf(ss, inv_h, p.eps));
+  const float c2 = gs * rstd * rstd * inv_h;
+  for (int c = threadIdx.x; c < p.H; c += blockDim.x) {
+    float o[1] = {ds ? to_f32(ds[c]) : 0.f};
+    if (active) o[0] = fmaf(rstd, fmaf(-to_f32(sp[c]), c2, to_f32(dy[c]) * to_f32(w[c])), o[0]);
+    store_vec<T, 1>(dx + c, o);
+  }
+  if (threadIdx.x == 0) p.rstd[row] = active ? rstd : 0.f;
+}
+
+// dw partials of long rows: CTA (x, y) sums columns [256 x, 256 x + 256) over
+// the rows y, y + gridDim.y, ...; inactive rows are not read.
+template <typename T>
+__global__ void __launch_bounds__(256)
+rmsnorm_dw_long_kernel(const RmsNormBwdArgs p) {
+  const long long c = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
+  if (c >= p.H) return;
+  float acc = 0.f;
+  for (long long row = blockIdx.y; row < p.R; row += gridDim.y)
+    if (!p.mask || p.mask[row] != 0)
+      acc = fmaf(to_f32(static_cast<const T*>(p.dy)[row * p.H + c]),
+                 to_f32(static_cast<const T*>(p.s)[row * p.H + c]) * p.rstd[row], acc);
+  p.partial[static_cast<long long>(blockIdx.y) * p.H + c] = acc;
+}
+
+// dw[c] = sum of the partial rows in a fixed order: 32 columns a CTA, its
+// warps take every 8th partial row, then the eight sums in order.
+constexpr int kDwWarps = 8;
+__global__ void __launch_bounds__(32 * kDwWarps)
+rmsnorm_dw_kernel(const float* __restrict__ partial, int n, int H, float* __restrict__ dw) {
+  __shared__ float sm[kDwWarps][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int c = blockIdx.x * 32 + lane;
+  float acc = 0.f;
+  if (c < H)
+    for (int i = warp; i < n; i += kDwWarps) acc += partial[static_cast<long long>(i) * H + c];
+  sm[warp][lane] = acc;
+  __syncthreads();
+  if (warp == 0 && c < H) {
+#pragma unroll
+    for (int i = 1; i < kDwWarps; ++i) acc += sm[i][lane];
+    dw[c] = acc;
+  }
+}
+
+// --------------------------------------------------------------- row shapes
+
+struct RowShape {
+  int vec;       // elements of a vector: 16 bytes where every row is aligned, else 1
+  int nv;        // vectors a thread: 1, 2, 4 or 8; 0: too long for registers
+  int threads;   // threads of a row, a multiple of 32
+  int rows;      // rows of a CTA (> 1 only where a warp holds a row)
+};
+
+// A row of H elements on the fewest vectors a thread that 1024 threads allow,
+// up to 8; short rows share a CTA, one warp each.
+RowShape row_shape(int H, int vec16) {
+  RowShape s;
+  s.vec = H % vec16 == 0 ? vec16 : 1;
+  const int n = (H + s.vec - 1) / s.vec;
+  s.nv = 1;
+  while (s.nv < 8 && n > 1024 * s.nv) s.nv *= 2;
+  if (n > 1024 * s.nv) return {s.vec, 0, 1024, 1};
+  s.threads = ((n + s.nv - 1) / s.nv + 31) / 32 * 32;
+  s.rows = s.threads == 32 ? 4 : 1;
+  return s;
+}
+
+}  // namespace
+
+// Partial rows of dw that rmsnorm_bwd writes at most, for any machine size (a
+// CTA of short rows writes four).
+long long rmsnorm_bwd_partials(long long R, long long H) {
+  const long long most = H <= 32768 ? 1024 : 32;
+  return R < 4 ? 4 : R < most ? R : most;
+}
+
+template <typename T, int VEC>
+static cudaError_t fwd_nv(const RmsNormFwdArgs& a, const RowShape& sh, cudaStream_t s) {
+  const dim3 block(sh.threads, sh.rows);
+  const unsigned grid = static_cast<unsigned>((a.R + sh.rows - 1) / sh.rows);
+  switch (sh.nv) {
+    case 1: rmsnorm_fwd_kernel<T, VEC, 1><<<grid, block, 0, s>>>(a); break;
+    case 2: rmsnorm_fwd_kernel<T, VEC, 2><<<grid, block, 0, s>>>(a); break;
+    case 4: rmsnorm_fwd_kernel<T, VEC, 4><<<grid, block, 0, s>>>(a); break;
+    default: rmsnorm_fwd_kernel<T, VEC, 8><<<grid, block, 0, s>>>(a); break;
+  }
+  return cudaGetLastError();
+}
+
+template <typename T>
+static cudaError_t fwd_t(const RmsNormFwdArgs& a, cudaStream_t s) {
+  const RowShape sh = row_shape(a.H, kVec16<T>);
+  if (sh.nv == 0) {
+    rmsnorm_fwd_long_kernel<T><<<static_cast<unsigned>(a.R), 1024, 0, s>>>(a);
+    return cudaGetLastError();
+  }
+  return sh.vec == 1 ? fwd_nv<T, 1>(a, sh, s) : fwd_nv<T, kVec16<T>>(a, sh, s);
+}
+
+cudaError_t launch_rmsnorm_fwd(const RmsNormFwdArgs& a, int is_bf16, cudaStream_t s) {
+  if (a.R == 0) return cudaSuccess;
+  return is_bf16 ? fwd_t<__nv_bfloat16>(a, s) : fwd_t<float>(a, s);
+}
+
+template <typename T, int VEC>
+static cudaError_t bwd_nv(const RmsNormBwdArgs& a, const RowShape& sh, unsigned grid,
+                          cudaStream_t s) {
+  const dim3 block(sh.threads, sh.rows);
+  switch (sh.nv) {
+    case 1: rmsnorm_bwd_kernel<T, VEC, 1><<<grid, block, 0, s>>>(a); break;
+    case 2: rmsnorm_bwd_kernel<T, VEC, 2><<<grid, block, 0, s>>>(a); break;
+    case 4: rmsnorm_bwd_kernel<T, VEC, 4><<<grid, block, 0, s>>>(a); break;
+    default: rmsnorm_bwd_kernel<T, VEC, 8><<<grid, block, 0, s>>>(a); break;
+  }
+  return cudaGetLastError();
+}
+
+template <typename T>
+static cudaError_t bwd_t(const RmsNormBwdArgs& a, int num_sms, int* n_partials, cudaStream_t s) {
+  const RowShape sh = row_shape(a.H, kVec16<T>);
+  const long long most = rmsnorm_bwd_partials(a.R, a.H);
+  if (sh.nv == 0) {
+    const int splits = static_cast<int>(most < 32 ? most : 32);
+    if (a.R > 0) rmsnorm_bwd_long_kernel<T><<<static_cast<unsigned>(a.R), 1024, 0, s>>>(a);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    rmsnorm_dw_long_kernel<T><<<dim3((a.H + 255) / 256, splits), 256, 0, s>>>(a);
+    *n_partials = splits;
+    return cudaGetLastError();
+  }
+  // resident CTAs: 2048 threads an SM, at most one row a CTA left over
+  int per_sm = 2048 / (sh.threads * sh.rows);
+  if (per_sm > 4) per_sm = 4;
+  long long grid = static_cast<long long>(num_sms) * per_sm;
+  const long long need = (a.R + sh.rows - 1) / sh.rows;
+  if (grid > need) grid = need;
+  if (grid * sh.rows > most) grid = most / sh.rows;
+  if (grid < 1) grid = 1;
+  *n_partials = static_cast<int>(grid * sh.rows);
+  return sh.vec == 1 ? bwd_nv<T, 1>(a, sh, static_cast<unsigned>(grid), s)
+                     : bwd_nv<T, kVec16<T>>(a, sh, static_cast<unsigned>(grid), s);
+}
+
+cudaError_t launch_rmsnorm_bwd(const RmsNormBwdArgs& a, int is_bf16, int num_sms, int* n_partials,
+                               cudaStream_t s) {
+  return is_bf16 ? bwd_t<__nv_bfloat16>(a, num_sms, n_partials, s)
+                 : bwd_t<float>(a, num_sms, n_partials, s);
+}
+
+cudaError_t launch_rmsnorm_dw(const float* partial, int n, int H, float* dw, cudaStream_t s) {
+  rmsnorm_dw_kernel<<<(H + 31) / 32, 32 * kDwWarps, 0, s>>>(partial, n, H, dw);
+  return cudaGetLastError();
+}
+
+}  // namespace eas

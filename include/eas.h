@@ -360,6 +360,110 @@ eas_status eas_lmhead_fwd_noalloc(const void* hidden, const void* weight,
                                   uint32_t flags, float* logprob, float* entropy, float* lse,
                                   void* stream);
 
+/* --------------------------------------------- norm before the LM head */
+
+/*
+ * Root-mean-square norm of rows, with the residual's addition, and an e4m3
+ * output with a scale for each row (what eas_lmhead_fwd_fp8 takes):
+ *   s = x + residual,  rstd = 1 / sqrt(mean(s^2) + eps),  y = s * weight * rstd,
+ *   amax = max |y|, y_scale = amax / 448, y_e4m3 = e4m3(y * (448 / amax))
+ * in fp32; s, y and y_e4m3 are each rounded once (y and the codes come from the
+ * unrounded sum; the codes from the unrounded y).  A row whose amax is 0, or
+ * below 2^-117, gets zero codes and scale 1.
+ *
+ *   x, residual [R, H], weight [H] : bf16 or fp32 (dtype); residual may be NULL
+ *   mask     [R] uint8 or NULL (every row active).  Inactive rows get y = 0,
+ *            zero codes and scale 1, whatever x holds there; s is written on
+ *            every row.
+ *   sum_out  [R, H] out, s rounded to dtype (what eas_rmsnorm_bwd takes), or
+ *            NULL; only with a residual (without one s is x).  May be x or
+ *            residual itself.
+ *   y        [R, H] out in dtype, or NULL
+ *   y_e4m3, y_scale : [R, H] uint8 and [R] fp32 out, or both NULL
+ * y and y_e4m3 must not overlap an input.  1 <= H <= 2^20, eps > 0, mean(s^2)
+ * within fp32.
+ */
+eas_status eas_rmsnorm_fwd(const void* x, const void* residual, const void* weight,
+                           const uint8_t* mask, int64_t R, int64_t H, eas_dtype dtype, float eps,
+                           void* sum_out, void* y, uint8_t* y_e4m3, float* y_scale, void* stream);
+
+/*
+ * Backward of eas_rmsnorm_fwd's y.  With g = dy * weight and rstd taken from s:
+ *   dx = ds + rstd * (g - s * rstd^2 / H * sum(g * s)),
+ *   dweight = sum over the active rows of dy * s * rstd.
+ * dx is the gradient of x and of the residual alike.
+ *
+ *   dy, s, weight : in dtype; s is the forward's sum_out (x without a residual)
+ *   ds       [R, H] gradient arriving at s from elsewhere (the residual
+ *            stream), or NULL.  May be dx itself.
+ *   mask     as in the forward: inactive rows' dy and s are not read, their dx
+ *            is ds or 0, and they add nothing to dweight
+ *   dx       [R, H] out in dtype; dweight [H] fp32 out; both overwritten
+ *   ws       eas_rmsnorm_bwd_workspace_size(R, H) bytes
+ * Sums are taken in a fixed order: results repeat to the bit.
+ */
+size_t eas_rmsnorm_bwd_workspace_size(int64_t R, int64_t H);
+
+eas_status eas_rmsnorm_bwd(const void* dy, const void* s, const void* weight, const void* ds,
+                           const uint8_t* mask, int64_t R, int64_t H, eas_dtype dtype, float eps,
+                           void* dx, float* dweight, void* ws, size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------- embedding */
+
+/*
+ * Embedding lookup with scaling: out[t] = scale * table[ids[t]].
+ *   ids      [T] int32; -1 is padding: its row of out is zero.  Any other id
+ *            outside [0, V) also gives a zero row, and EAS_ERR_INVALID_ARG in
+ *            the status word of ws.
+ *   table    [V, H], out [T, H] : bf16 or fp32 (dtype)
+ *   ws       at least 16 bytes for the status word, or NULL: no status is kept
+ */
+eas_status eas_embed_fwd(const int32_t* ids, const void* table, int64_t T, int64_t H, int64_t V,
+                         eas_dtype dtype, float scale, void* out, void* ws, size_t ws_bytes,
+                         void* stream);
+
+/*
+ * Its gradient: dweight[v] = scale * sum over t with ids[t] == v of dout[t],
+ * summed in fp32 over the tokens sorted by id, in a fixed order (results
+ * repeat to the bit).
+ *   dout     [T, H] in dtype; rows of padding and of bad ids are not read
+ *   accumulate : 0 = dweight is overwritten, every row written; 1 = the sums are
+ *            added to it and rows that no token names are left alone (tied
+ *            weights: the dweight eas_lmhead_bwd wrote)
+ *   dweight  [V, H] fp32
+ *   ws       eas_embed_bwd_workspace_size(T, H, V) bytes; holds the status word
+ */
+size_t eas_embed_bwd_workspace_size(int64_t T, int64_t H, int64_t V);
+
+eas_status eas_embed_bwd(const int32_t* ids, const void* dout, int64_t T, int64_t H, int64_t V,
+                         eas_dtype dtype, float scale, int32_t accumulate, float* dweight,
+                         void* ws, size_t ws_bytes, void* stream);
+
+/* ----------------------------------------------------- gradient clipping */
+
+/*
+ * Global norm of n gradients, and clipping:
+ *   norm = sqrt(sum over all tensors of g^2),
+ *   c = min(1, max_norm / (norm + 1e-6)),  out = c * g.
+ * Where the norm is not finite, c = 1: the caller sees the norm and skips its
+ * step.  Squares are added in fp64 (fp32 inside one 16-byte load), in a fixed
+ * order.
+ *
+ *   grads, outs, numels, dtypes, out_dtypes : HOST arrays of n entries, copied
+ *            before the call returns.  Tensors are contiguous, aligned to their
+ *            element, bf16 or fp32; outs[i] is grads[i] itself (same dtype: in
+ *            place) or another buffer, which no other entry may overlap.  outs
+ *            NULL: only the norm is computed (max_norm is not used).
+ *   norm     [1] fp32 device, out: the norm before clipping
+ *   ws       eas_clip_grad_norm_workspace_size(n) bytes
+ */
+size_t eas_clip_grad_norm_workspace_size(int32_t n);
+
+eas_status eas_clip_grad_norm(const void* const* grads, void* const* outs, const int64_t* numels,
+                              const int32_t* dtypes, const int32_t* out_dtypes, int32_t n,
+                              float max_norm, float* norm, void* ws, size_t ws_bytes,
+                              void* stream);
+
 /* ------------------------------------------------------------- utilities */
 
 /*
