@@ -115,7 +115,7 @@ const char* const kTraceNames[kTrCount] = {
     "dlogits_gemm_simt", "dhidden_gemm_simt", "dweight_gemm_simt", "memset",
     "bwd_chunk_gemm_tc", "dlogits_gemm_tc_e4m3",
     "rmsnorm_fwd", "rmsnorm_bwd", "rmsnorm_dweight", "embed_fwd", "embed_sort", "embed_bwd",
-    "grad_norm", "grad_clip"};
+    "grad_norm", "clip_grad_norm"};
 
 struct TraceRec {
   int kind;
@@ -1206,15 +1206,10 @@ eas_status eas_clip_grad_norm(const void* const* grads, void* const* outs, const
     eas_status st = device_info(&di);
     if (st != EAS_OK) return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    {
-      Trace tr_(kTrGradNorm, s);
-      EAS_CUDA(launch_grad_norm(list.data(), n, static_cast<double*>(ws), norm, di.sms, s),
-               "grad_norm");
-    }
-    if (outs) {
-      Trace tr_(kTrGradClip, s);
-      EAS_CUDA(launch_grad_clip(list.data(), n, norm, max_norm, di.sms, s), "grad_clip");
-    }
+    Trace tr_(outs ? kTrGradClip : kTrGradNorm, s);
+    EAS_CUDA(launch_clip_grad_norm(list.data(), n, outs != nullptr, max_norm,
+                                   static_cast<double*>(ws), norm, di.sms, s),
+             "clip_grad_norm");
     return EAS_OK;
   } catch (const std::bad_alloc&) {
     return fail(EAS_ERR_CUDA, "out of host memory");

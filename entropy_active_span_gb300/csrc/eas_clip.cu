@@ -4,11 +4,12 @@
 //   c = min(1, max_norm / (norm + 1e-6)),  out = c g   (c = 1: norm not finite).
 //
 // The list travels as a kernel argument: no table in device memory, no copy,
-// and a captured graph holds its own.  Work is cut into chunks of kChunk
-// elements over all tensors; a CTA finds a chunk's tensor by bisection.
-// Squares are added up in fp32 over the 16 bytes of a load, and those sums in
-// fp64 from there on.  Every CTA leaves one fp64 partial sum and whoever needs
-// the norm adds the partials in the same order, so results repeat to the bit.
+// and a captured graph holds its own.  Work is cut into chunks of equal length
+// over all tensors; a CTA finds a chunk's tensor by bisection.  Squares are
+// added up in fp32 over 32 elements and beyond that with their rounding errors
+// kept.  Every CTA leaves one fp64 partial sum; the clipping CTAs each add the
+// partials up themselves, in one order, so the norm needs no launch of its own
+// and results repeat to the bit.
 #include "eas_device.cuh"
 #include "eas_kernels.h"
 #include "eas_vec.cuh"
@@ -18,9 +19,10 @@ namespace eas {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kChunk = 16384;        // elements a chunk
+constexpr int kMaxLogChunk = 14;     // elements a chunk: 2^10 .. 2^14
+constexpr int kMinLogChunk = 10;
 constexpr int kMaxCtas = 1216;       // partials a launch leaves at most
-constexpr int kSmallList = 24;
+constexpr int kSmallList = 128;
 constexpr int kLargeList = 800;
 
 template <int N>
@@ -32,6 +34,7 @@ struct List {
   unsigned char kind[N];             // bit 0: in is bf16, bit 1: out is bf16
   int n;
   int n_chunks;
+  int log_chunk;
 };
 
 template <int N>
@@ -44,23 +47,58 @@ __device__ __forceinline__ int tensor_of(const List<N>& l, int chunk) {
   return lo;
 }
 
-// Sum of squares of one load.  Where the fp32 squares leave the normal range
-// (a gradient over 1e18 or all below 1e-15) they are taken again in fp64.
-template <int VEC>
-__device__ __forceinline__ double squares(const float (&f)[VEC]) {
-  float s = 0.f, m = 0.f;
-#pragma unroll
-  for (int i = 0; i < VEC; ++i) {
-    s = fmaf(f[i], f[i], s);
-    m = fmaxf(m, fabsf(f[i]));
+// A running sum of squares: hi + lo in fp32, exact to about 2^-48 (each group's
+// sum is added with its rounding error kept, Knuth's two-sum), and in fp64 what
+// leaves the range in which that holds.  fp64 sums from each 16-byte load on
+// were built first: this part's fp64 rate is far below its fp32 rate, and the
+// norm and clipping of 1.33 G gradients (0.53 G fp32, 0.81 G bf16, into bf16)
+// took 3370 us; this way 1482, which is the time of reading everything twice
+// and writing it once (10.1 GB at 6.8 TB/s).
+struct Squares {
+  float hi = 0.f, lo = 0.f;
+  double rest = 0.0;
+
+  __device__ __forceinline__ void add(float s) {
+    const float t = hi + s;
+    const float b = t - hi;
+    lo += (hi - (t - b)) + (s - b);
+    hi = t;
   }
-  if (m != 0.f && !(s > 1e-30f && s < 1e36f)) {
-    double d = 0.0;
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) d += static_cast<double>(f[i]) * f[i];
-    return d;
+  __device__ __forceinline__ double total() const {
+    return static_cast<double>(hi) + static_cast<double>(lo) + rest;
   }
-  return s;
+};
+
+// Adds the squares of a group of elements.  Where their fp32 sum could have
+// lost some (a gradient over 1e15 or everything below 1e-15) they are taken
+// again in fp64; a group of zeros is not.
+template <int U, int VEC>
+__device__ __forceinline__ void add_squares(Squares& acc, const float (&f)[U][VEC]) {
+  float part[U], m = 0.f;
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    part[u] = 0.f;
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) part[u] = fmaf(f[u][i], f[u][i], part[u]);
+  }
+#pragma unroll
+  for (int o = U / 2; o > 0; o /= 2)
+#pragma unroll
+    for (int u = 0; u < o; ++u) part[u] += part[u + o];
+  const float s = part[0];
+  if (s > 1e-30f && s < 1e30f) {
+    acc.add(s);
+    return;
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) m = fmaxf(m, fabsf(f[u][i]));
+  if (s == 0.f && m == 0.f) return;
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) acc.rest += static_cast<double>(f[u][i]) * f[u][i];
 }
 
 // Elements before the first 16-byte boundary at or after p.
@@ -70,33 +108,33 @@ __device__ __forceinline__ int head_of(const T* p) {
 }
 
 template <typename T>
-__device__ __forceinline__ double chunk_squares(const T* p, int n) {
+__device__ __forceinline__ void chunk_squares(Squares& acc, const T* p, int n) {
   constexpr int VEC = kVec16<T>;
-  constexpr int U = 4;
-  double acc = 0.0;
+  constexpr int U = 32 / VEC;          // 32 elements a group
   int head = head_of(p);
   if (head > n) head = n;
   const int vecs = (n - head) / VEC;
   const T* v = p + head;
-  for (int i = threadIdx.x; i < vecs; i += kThreads * U) {
+  int i = threadIdx.x;
+  for (; i + (U - 1) * kThreads < vecs; i += U * kThreads) {
     Raw<T, VEC> raw[U];
+    float f[U][VEC];
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (i + u * kThreads < vecs) raw[u] = load_raw<T, VEC>(v + static_cast<long long>(i + u * kThreads) * VEC);
+    for (int u = 0; u < U; ++u) raw[u] = load_raw<T, VEC>(v + static_cast<long long>(i + u * kThreads) * VEC);
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (i + u * kThreads < vecs) {
-        float f[VEC];
-        widen<T, VEC>(raw[u], f);
-        acc += squares<VEC>(f);
-      }
+    for (int u = 0; u < U; ++u) widen<T, VEC>(raw[u], f[u]);
+    add_squares<U, VEC>(acc, f);
+  }
+  for (; i < vecs; i += kThreads) {
+    float f[1][VEC];
+    widen<T, VEC>(load_raw<T, VEC>(v + static_cast<long long>(i) * VEC), f[0]);
+    add_squares<1, VEC>(acc, f);
   }
   const int tail = head + vecs * VEC;
-  for (int i = threadIdx.x; i < head + (n - tail); i += kThreads) {
-    const double f = to_f32(p[i < head ? i : tail + (i - head)]);
-    acc += f * f;
+  for (i = threadIdx.x; i < head + (n - tail); i += kThreads) {
+    const float f[1][1] = {{to_f32(p[i < head ? i : tail + (i - head)])}};
+    add_squares<1, 1>(acc, f);
   }
-  return acc;
 }
 
 __device__ __forceinline__ double block_sum(double v, double* sm) {
@@ -114,54 +152,68 @@ template <int N>
 __global__ void __launch_bounds__(kThreads)
 grad_squares_kernel(const __grid_constant__ List<N> l, double* partial) {
   __shared__ double sm[kThreads / 32];
-  double acc = 0.0;
+  Squares acc;
   for (int k = blockIdx.x; k < l.n_chunks; k += gridDim.x) {
     const int t = tensor_of(l, k);
-    const long long off = static_cast<long long>(k - l.first[t]) * kChunk;
+    const long long off = static_cast<long long>(k - l.first[t]) << l.log_chunk;
     const long long left = l.numel[t] - off;
-    const int n = static_cast<int>(left < kChunk ? left : kChunk);
+    const int n = static_cast<int>(left < (1 << l.log_chunk) ? left : (1 << l.log_chunk));
     if (l.kind[t] & 1)
-      acc += chunk_squares(static_cast<const __nv_bfloat16*>(l.in[t]) + off, n);
+      chunk_squares(acc, static_cast<const __nv_bfloat16*>(l.in[t]) + off, n);
     else
-      acc += chunk_squares(static_cast<const float*>(l.in[t]) + off, n);
+      chunk_squares(acc, static_cast<const float*>(l.in[t]) + off, n);
   }
-  acc = block_sum(acc, sm);
-  if (threadIdx.x == 0) partial[blockIdx.x] = acc;
+  const double sum = block_sum(acc.total(), sm);
+  if (threadIdx.x == 0) partial[blockIdx.x] = sum;
+}
+
+// The norm from the partial sums, the same to the bit in whatever CTA asks.
+__device__ __forceinline__ float norm_of(const double* partial, int n, double* sm) {
+  double acc = 0.0;
+  for (int i = threadIdx.x; i < n; i += kThreads) acc += partial[i];
+  return static_cast<float>(sqrt(block_sum(acc, sm)));
 }
 
 __global__ void __launch_bounds__(kThreads)
 grad_norm_kernel(const double* partial, int n, float* norm) {
   __shared__ double sm[kThreads / 32];
-  double acc = 0.0;
-  for (int i = threadIdx.x; i < n; i += kThreads) acc += partial[i];
-  acc = block_sum(acc, sm);
-  if (threadIdx.x == 0) *norm = static_cast<float>(sqrt(acc));
+  const float v = norm_of(partial, n, sm);
+  if (threadIdx.x == 0) *norm = v;
 }
 
 template <typename I, typename O>
 __device__ __forceinline__ void scale_chunk(const I* in, O* out, int n, float c) {
-  // vectors of 4 elements: 16 bytes of fp32, 8 of bf16
-  constexpr int VEC = 4;
+  constexpr int VEC = kVec16<I>;       // 16 bytes of input
+  constexpr int W = kVec16<O> < VEC ? kVec16<O> : VEC;
+  constexpr int U = 4;
   int head = head_of(in);
   if (head > n) head = n;
-  const bool vec = (reinterpret_cast<uintptr_t>(out + head) % (VEC * sizeof(O))) == 0;
+  // a vector's output is 16 bytes or two halves of them
+  const bool vec = (reinterpret_cast<uintptr_t>(out + head) % (W * sizeof(O))) == 0;
   const int vecs = vec ? (n - head) / VEC : 0;
-  for (int i = threadIdx.x; i < vecs; i += kThreads) {
-    float f[VEC];
-    if constexpr (sizeof(I) == 4) {
-      const float4 q = *reinterpret_cast<const float4*>(in + head + i * VEC);
-      f[0] = q.x; f[1] = q.y; f[2] = q.z; f[3] = q.w;
-    } else {
-      const uint2 q = *reinterpret_cast<const uint2*>(in + head + i * VEC);
-      f[0] = bf16_lo(q.x); f[1] = bf16_hi(q.x); f[2] = bf16_lo(q.y); f[3] = bf16_hi(q.y);
-    }
+  for (int i0 = threadIdx.x; i0 < vecs; i0 += U * kThreads) {
+    Raw<I, VEC> raw[U];
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) f[e] *= c;
-    if constexpr (sizeof(O) == 4)
-      *reinterpret_cast<float4*>(out + head + i * VEC) = make_float4(f[0], f[1], f[2], f[3]);
-    else
-      *reinterpret_cast<uint2*>(out + head + i * VEC) =
-          make_uint2(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]));
+    for (int u = 0; u < U; ++u)
+      if (i0 + u * kThreads < vecs)
+        raw[u] = load_raw<I, VEC>(in + head + static_cast<long long>(i0 + u * kThreads) * VEC);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (i0 + u * kThreads >= vecs) break;
+      O* to = out + head + static_cast<long long>(i0 + u * kThreads) * VEC;
+      float f[VEC];
+      widen<I, VEC>(raw[u], f);
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) f[e] *= c;
+      if constexpr (sizeof(O) == sizeof(I)) {
+        store_vec<O, VEC>(to, f);
+      } else if constexpr (sizeof(O) == 4) {
+        *reinterpret_cast<float4*>(to) = make_float4(f[0], f[1], f[2], f[3]);
+        *reinterpret_cast<float4*>(to + 4) = make_float4(f[4], f[5], f[6], f[7]);
+      } else {
+        *reinterpret_cast<uint2*>(to) = make_uint2(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]));
+      }
+    }
   }
   const int tail = head + vecs * VEC;
   for (int i = threadIdx.x; i < head + (n - tail); i += kThreads) {
@@ -173,17 +225,19 @@ __device__ __forceinline__ void scale_chunk(const I* in, O* out, int n, float c)
 
 template <int N>
 __global__ void __launch_bounds__(kThreads)
-grad_clip_kernel(const __grid_constant__ List<N> l, const float* norm, float max_norm) {
-  const float v = *norm;
-  float c = 1.f;
-  if (isfinite(v)) c = fminf(1.f, max_norm / (v + 1e-6f));
+grad_clip_kernel(const __grid_constant__ List<N> l, const double* partial, int n_partial,
+                 float* norm, float max_norm) {
+  __shared__ double sm[kThreads / 32];
+  const float v = norm_of(partial, n_partial, sm);
+  if (blockIdx.x == 0 && threadIdx.x == 0) *norm = v;
+  const float c = isfinite(v) ? fminf(1.f, max_norm / (v + 1e-6f)) : 1.f;
   // from the last chunk down: what the norm read last is still in L2
   for (int k = l.n_chunks - 1 - blockIdx.x; k >= 0; k -= gridDim.x) {
     const int t = tensor_of(l, k);
     if (c == 1.f && l.in[t] == l.out[t]) continue;   // in place: nothing changes
-    const long long off = static_cast<long long>(k - l.first[t]) * kChunk;
+    const long long off = static_cast<long long>(k - l.first[t]) << l.log_chunk;
     const long long left = l.numel[t] - off;
-    const int n = static_cast<int>(left < kChunk ? left : kChunk);
+    const int n = static_cast<int>(left < (1 << l.log_chunk) ? left : (1 << l.log_chunk));
     const __nv_bfloat16* ib = static_cast<const __nv_bfloat16*>(l.in[t]) + off;
     const float* fi = static_cast<const float*>(l.in[t]) + off;
     __nv_bfloat16* ob = static_cast<__nv_bfloat16*>(l.out[t]) + off;
@@ -197,16 +251,27 @@ grad_clip_kernel(const __grid_constant__ List<N> l, const float* norm, float max
   }
 }
 
+// log2 of the chunk: the largest that still gives every resident CTA one, so
+// that a short list is spread over the machine and a long one searches less.
+int log_chunk_of(const ClipTensor* t, int n, int num_sms) {
+  long long total = 0;
+  for (int i = 0; i < n; ++i) total += t[i].numel;
+  int lc = kMaxLogChunk;
+  while (lc > kMinLogChunk && (total >> lc) < 8LL * num_sms) --lc;
+  return lc;
+}
+
 // Tensors [at, at + N) of the list, the empty ones left out; returns where the
 // next launch goes on.
 template <int N>
-int fill(List<N>& l, const ClipTensor* t, int n, int at) {
+int fill(List<N>& l, const ClipTensor* t, int n, int at, int log_chunk) {
   l.n = 0;
+  l.log_chunk = log_chunk;
   long long chunks = 0;
   for (; at < n && l.n < N; ++at) {
     if (t[at].numel == 0) continue;
-    const long long c = (t[at].numel + kChunk - 1) / kChunk;
-    if (chunks + c > 0x7fffffffLL) break;
+    const long long c = (t[at].numel + (1LL << log_chunk) - 1) >> log_chunk;
+    if (chunks + c > 0x7fffffffLL) break;   // never the first: numel <= 2^40
     const int i = l.n++;
     l.in[i] = t[at].in;
     l.out[i] = t[at].out;
@@ -226,33 +291,28 @@ int ctas(int chunks, int num_sms) {
 }
 
 template <int N>
-cudaError_t norm_lists(const ClipTensor* t, int n, double* partial, int* n_partial, int num_sms,
-                       cudaStream_t s) {
+cudaError_t launch_lists(const ClipTensor* t, int n, bool clip, float max_norm, double* partial,
+                         float* norm, int num_sms, cudaStream_t s) {
+  const int lc = log_chunk_of(t, n, num_sms);
   List<N> l;
+  int np = 0;
   for (int at = 0; at < n;) {
-    at = fill(l, t, n, at);
+    at = fill(l, t, n, at, lc);
     if (l.n_chunks == 0) continue;
     const int g = ctas(l.n_chunks, num_sms);
-    grad_squares_kernel<N><<<g, kThreads, 0, s>>>(l, partial + *n_partial);
-    *n_partial += g;
-    const cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
+    grad_squares_kernel<N><<<g, kThreads, 0, s>>>(l, partial + np);
+    np += g;
   }
-  return cudaSuccess;
-}
-
-template <int N>
-cudaError_t clip_lists(const ClipTensor* t, int n, const float* norm, float max_norm, int num_sms,
-                       cudaStream_t s) {
-  List<N> l;
+  if (!clip || np == 0) {
+    grad_norm_kernel<<<1, kThreads, 0, s>>>(partial, np, norm);
+    return cudaGetLastError();
+  }
   for (int at = 0; at < n;) {
-    at = fill(l, t, n, at);
+    at = fill(l, t, n, at, lc);
     if (l.n_chunks == 0) continue;
-    grad_clip_kernel<N><<<ctas(l.n_chunks, num_sms), kThreads, 0, s>>>(l, norm, max_norm);
-    const cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
+    grad_clip_kernel<N><<<ctas(l.n_chunks, num_sms), kThreads, 0, s>>>(l, partial, np, norm, max_norm);
   }
-  return cudaSuccess;
+  return cudaGetLastError();
 }
 
 }  // namespace
@@ -262,21 +322,11 @@ size_t clip_workspace_bytes(long long n) {
   return static_cast<size_t>(lists) * kMaxCtas * sizeof(double);
 }
 
-cudaError_t launch_grad_norm(const ClipTensor* t, int n, double* partial, float* norm, int num_sms,
-                             cudaStream_t s) {
-  int np = 0;
-  const cudaError_t e = n <= kSmallList
-                            ? norm_lists<kSmallList>(t, n, partial, &np, num_sms, s)
-                            : norm_lists<kLargeList>(t, n, partial, &np, num_sms, s);
-  if (e != cudaSuccess) return e;
-  grad_norm_kernel<<<1, kThreads, 0, s>>>(partial, np, norm);
-  return cudaGetLastError();
-}
-
-cudaError_t launch_grad_clip(const ClipTensor* t, int n, const float* norm, float max_norm,
-                             int num_sms, cudaStream_t s) {
-  return n <= kSmallList ? clip_lists<kSmallList>(t, n, norm, max_norm, num_sms, s)
-                         : clip_lists<kLargeList>(t, n, norm, max_norm, num_sms, s);
+cudaError_t launch_clip_grad_norm(const ClipTensor* t, int n, bool clip, float max_norm,
+                                  double* partial, float* norm, int num_sms, cudaStream_t s) {
+  return n <= kSmallList
+             ? launch_lists<kSmallList>(t, n, clip, max_norm, partial, norm, num_sms, s)
+             : launch_lists<kLargeList>(t, n, clip, max_norm, partial, norm, num_sms, s);
 }
 
 }  // namespace eas

@@ -239,10 +239,9 @@ struct ClipTensor {
   int in_bf16, out_bf16;
 };
 size_t clip_workspace_bytes(long long n_tensors);
-cudaError_t launch_grad_norm(const ClipTensor* t, int n, double* partial, float* norm, int num_sms,
-                             cudaStream_t s);
-cudaError_t launch_grad_clip(const ClipTensor* t, int n, const float* norm, float max_norm,
-                             int num_sms, cudaStream_t s);
+// The norm, and with `clip` the scaled tensors too.
+cudaError_t launch_clip_grad_norm(const ClipTensor* t, int n, bool clip, float max_norm,
+                                  double* partial, float* norm, int num_sms, cudaStream_t s);
 
 // ---- helpers the C-ABI translation units share (eas_api.cu) ----
 size_t lmhead_fwd_workspace_bytes(long long T, long long H, long long V, int dtype);
