@@ -213,6 +213,7 @@ rmsnorm_fwd_long_kernel(const RmsNormFwdArgs p) {
 
 // ----------------------------------------------------------------- backward
 
+// Rows that the ring kernel below does not take (unaligned ones, and beyond 32 KB).
 // A CTA walks rows blockIdx.x, blockIdx.x + gridDim.x, ... (blockDim.y rows at a
 // time where a warp holds a row); each thread keeps its columns' share of dw
 // in registers and adds it to the CTA's row of `partial` at the end.  The
@@ -312,6 +313,243 @@ rmsnorm_bwd_kernel(const RmsNormBwdArgs p) {
   }
 }
 
+// The same for aligned rows, with the loads running ahead: each thread copies
+// the vectors that it will itself consume into its own slots of a ring in
+// shared memory, kStages rows deep, with cp.async.  A thread waits for its own
+// copies only, so the ring needs no barrier; the one barrier a row is the
+// reduction's.  With a mask the group first lists its active rows and fills the
+// others while the first copies are on their way, so that the ring holds
+// active rows alone.
+//
+// A CTA holds one row at a time, or (kShort) each of its eight warps its own
+// rows, blockDim.x lanes a row.
+__device__ __forceinline__ void cp_async16(void* smem, const void* gmem) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(smem)), "l"(gmem) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+constexpr int kListRows = 512;    // rows a group lists at a time
+constexpr int kShortWarps = 8;
+
+template <typename T, int NV, int kStages, bool kShort>
+__global__ void __launch_bounds__(kShort ? 256 : 512, kShort ? 2 : 1)
+rmsnorm_bwd_ring_kernel(const RmsNormBwdArgs p) {
+  constexpr int VEC = kVec16<T>;
+  // [kStages][2 or 3][NV][threads of the CTA].  Where it started on a 16-byte
+  // but no 128-byte boundary, each cp.async fetched its sectors from L2 twice.
+  extern __shared__ __align__(128) uint4 ring[];
+  __shared__ float2 red[2][32];
+  __shared__ int listed;
+  __shared__ unsigned short list[kShort ? kShortWarps : 1][kListRows];
+  const int cta = blockDim.x * blockDim.y;
+  const int tid = threadIdx.y * blockDim.x + threadIdx.x;
+  const int lane = tid & 31, warp = tid >> 5;
+  const int group = kShort ? warp : 0;                    // who shares a list of rows
+  const int groups = kShort ? kShortWarps : 1;
+  const int abreast = kShort ? 32 / blockDim.x : 1;       // rows a group holds at a time
+  const int sub = kShort ? lane / blockDim.x : 0;
+  const int arrays = p.ds ? 3 : 2;
+  const T* dy = static_cast<const T*>(p.dy);
+  const T* sv = static_cast<const T*>(p.s);
+  const T* ds = static_cast<const T*>(p.ds);
+  T* dx = static_cast<T*>(p.dx);
+  const T* w = static_cast<const T*>(p.w);
+  Raw<T, VEC> rw[NV];
+  float acc[NV][VEC];
+  bool in[NV];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int c = (j * blockDim.x + threadIdx.x) * VEC;
+    in[j] = c < p.H;
+    if (in[j]) rw[j] = load_raw<T, VEC>(w + c);
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) acc[j][i] = 0.f;
+  }
+  const float inv_h = 1.f / static_cast<float>(p.H);
+  // this group's rows: first, first + step, ...
+  const long long first = static_cast<long long>(blockIdx.x) * groups + group;
+  const long long step = static_cast<long long>(gridDim.x) * groups;
+  const long long rows = first < p.R ? (p.R - first + step - 1) / step : 0;
+  int parity = 0;
+
+  for (long long base = 0; base < rows; base += kListRows) {
+    const int span = static_cast<int>(rows - base < kListRows ? rows - base : kListRows);
+    int n = span;
+    unsigned short* mine = list[group];
+    if (p.mask) {
+      // a warp of the group lists the active rows from the front and the
+      // others from the back
+      if (kShort || warp == 0) {
+        int on = 0, off = 0;
+        for (int i0 = 0; i0 < span; i0 += 32) {
+          const int i = i0 + lane;
+          const bool valid = i < span;
+          const bool a = valid && p.mask[first + (base + i) * step] != 0;
+          const unsigned m = __ballot_sync(0xffffffffu, a);
+          const unsigned z = __ballot_sync(0xffffffffu, valid && !a);
+          const unsigned below = (1u << lane) - 1;
+          if (a) mine[on + __popc(m & below)] = static_cast<unsigned short>(i);
+          else if (valid) mine[kListRows - 1 - off - __popc(z & below)] = static_cast<unsigned short>(i);
+          on += __popc(m);
+          off += __popc(z);
+        }
+        n = on;
+        if (!kShort && lane == 0) listed = on;
+      }
+      if constexpr (kShort) {
+        __syncwarp();
+      } else {
+        __syncthreads();
+        n = listed;
+      }
+    }
+    auto row_at = [&](int k) -> long long {
+      return first + (base + (p.mask ? mine[k] : k)) * step;
+    };
+    auto issue = [&](int k) {
+      const int e = k * abreast + sub;
+      if (e < n) {
+        const long long off = row_at(e) * p.H;
+        uint4* slot = ring + static_cast<size_t>(k % kStages) * arrays * NV * cta + tid;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+          const int c = (j * blockDim.x + threadIdx.x) * VEC;
+          if (in[j]) {
+            cp_async16(slot + j * cta, dy + off + c);
+            cp_async16(slot + (NV + j) * cta, sv + off + c);
+            if (ds) cp_async16(slot + (2 * NV + j) * cta, ds + off + c);
+          }
+        }
+      }
+      cp_async_commit();
+    };
+#pragma unroll
+    for (int k = 0; k < kStages - 1; ++k) issue(k);
+
+    if (p.mask && !(ds && static_cast<const void*>(ds) == p.dx)) {   // in place: ds is there already
+#pragma unroll 2
+      for (int e = sub; e < span - n; e += abreast) {
+        const long long off = (first + (base + mine[kListRows - 1 - e]) * step) * p.H;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+          const int c = (j * blockDim.x + threadIdx.x) * VEC;
+          if (in[j])
+            *reinterpret_cast<uint4*>(dx + off + c) =
+                ds ? *reinterpret_cast<const uint4*>(ds + off + c) : make_uint4(0, 0, 0, 0);
+        }
+      }
+    }
+
+    for (int k = 0; k * abreast < n; ++k) {
+      issue(k + kStages - 1);
+      cp_async_wait<kStages - 1>();
+      const uint4* slot = ring + static_cast<size_t>(k % kStages) * arrays * NV * cta + tid;
+      const int e = k * abreast + sub;
+      const bool valid = !kShort || e < n;
+      Raw<T, VEC> rdy[NV], rsv[NV];
+      float ss = 0.f, gs = 0.f;
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        if (in[j] && valid) {
+          rdy[j].v = slot[j * cta];
+          rsv[j].v = slot[(NV + j) * cta];
+          float s[VEC], d[VEC], wf[VEC];
+          widen<T, VEC>(rsv[j], s);
+          widen<T, VEC>(rdy[j], d);
+          widen<T, VEC>(rw[j], wf);
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) {
+            ss = fmaf(s[i], s[i], ss);
+            gs = fmaf(d[i] * wf[i], s[i], gs);
+          }
+        }
+      }
+      if constexpr (kShort) {
+        for (int o = blockDim.x / 2; o > 0; o /= 2) {
+          ss += __shfl_xor_sync(0xffffffffu, ss, o);
+          gs += __shfl_xor_sync(0xffffffffu, gs, o);
+        }
+      } else {
+        reduce_pair<false>(ss, gs, red[parity], blockDim.x >> 5);
+        parity ^= 1;
+      }
+      if (!valid) continue;
+      const float rstd = rsqrtf(fmaf(ss, inv_h, p.eps));
+      const float c2 = gs * rstd * rstd * inv_h;
+      const long long off = row_at(e) * p.H;
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        if (in[j]) {
+          const int c = (j * blockDim.x + threadIdx.x) * VEC;
+          float s[VEC], d[VEC], wf[VEC], o[VEC] = {};
+          widen<T, VEC>(rsv[j], s);
+          widen<T, VEC>(rdy[j], d);
+          widen<T, VEC>(rw[j], wf);
+          if (ds) {
+            Raw<T, VEC> r;
+            r.v = slot[(2 * NV + j) * cta];
+            widen<T, VEC>(r, o);
+          }
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) {
+            o[i] = fmaf(rstd, fmaf(-s[i], c2, d[i] * wf[i]), o[i]);
+            acc[j][i] = fmaf(d[i], s[i] * rstd, acc[j][i]);
+          }
+          store_vec<T, VEC>(dx + off + c, o);
+        }
+      }
+    }
+    cp_async_wait<0>();
+    // the list is written again only after every warp is done with it
+    if (p.mask && base + kListRows < rows) {
+      if constexpr (kShort) __syncwarp(); else __syncthreads();
+    }
+  }
+
+  float* out = p.partial + static_cast<long long>(blockIdx.x) * p.H;
+  if constexpr (kShort) {
+    // lanes that hold the same columns, then the warps in order (the ring, whose
+    // copies have all landed, is at least as large as the warps' sums)
+    __syncthreads();
+    float* sums = reinterpret_cast<float*>(ring);
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+#pragma unroll
+      for (int i = 0; i < VEC; ++i)
+        for (int o = blockDim.x; o < 32; o *= 2) acc[j][i] += __shfl_xor_sync(0xffffffffu, acc[j][i], o);
+      const int c = (j * blockDim.x + threadIdx.x) * VEC;
+      if (in[j] && sub == 0) {
+#pragma unroll
+        for (int h = 0; h < VEC; h += 4)
+          *reinterpret_cast<float4*>(sums + warp * p.H + c + h) =
+              make_float4(acc[j][h], acc[j][h + 1], acc[j][h + 2], acc[j][h + 3]);
+      }
+    }
+    __syncthreads();
+    for (int c = tid; c < p.H; c += cta) {
+      float t = sums[c];
+#pragma unroll
+      for (int g = 1; g < kShortWarps; ++g) t += sums[g * p.H + c];
+      out[c] = t;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = (j * blockDim.x + threadIdx.x) * VEC;
+      if (in[j]) {
+#pragma unroll
+        for (int h = 0; h < VEC; h += 4)
+          *reinterpret_cast<float4*>(out + c + h) =
+              make_float4(acc[j][h], acc[j][h + 1], acc[j][h + 2], acc[j][h + 3]);
+      }
+    }
+  }
+}
+
 // Rows too long for registers: dx in two walks of the row, the row's rstd
 // kept for the dw pass.
 template <typename T>
@@ -361,16 +599,18 @@ rmsnorm_dw_long_kernel(const RmsNormBwdArgs p) {
 }
 
 // dw[c] = sum of the partial rows in a fixed order: 32 columns a CTA, its
-// warps take every 8th partial row, then the eight sums in order.
-constexpr int kDwWarps = 8;
+// warps take every kDwWarps-th partial row, then the warps' sums in order.
+constexpr int kDwWarps = 16;
 __global__ void __launch_bounds__(32 * kDwWarps)
 rmsnorm_dw_kernel(const float* __restrict__ partial, int n, int H, float* __restrict__ dw) {
   __shared__ float sm[kDwWarps][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
   float acc = 0.f;
-  if (c < H)
+  if (c < H) {
+#pragma unroll 8
     for (int i = warp; i < n; i += kDwWarps) acc += partial[static_cast<long long>(i) * H + c];
+  }
   sm[warp][lane] = acc;
   __syncthreads();
   if (warp == 0 && c < H) {
@@ -389,14 +629,17 @@ struct RowShape {
   int rows;      // rows of a CTA (> 1 only where a warp holds a row)
 };
 
-// A row of H elements on the fewest vectors a thread that 1024 threads allow,
-// up to 8; short rows share a CTA, one warp each.
+// A row of H elements in registers.  Aligned rows: the fewest vectors a thread
+// that 1024 threads allow.  Element by element: up to eight a thread before a
+// CTA grows beyond 256 threads, so that several rows share an SM.  Rows that a
+// warp can hold share a CTA, one warp each.
 RowShape row_shape(int H, int vec16) {
   RowShape s;
   s.vec = H % vec16 == 0 ? vec16 : 1;
   const int n = (H + s.vec - 1) / s.vec;
+  const int wide = s.vec == 1 ? 256 : 1024;
   s.nv = 1;
-  while (s.nv < 8 && n > 1024 * s.nv) s.nv *= 2;
+  while (s.nv < 8 && n > wide * s.nv) s.nv *= 2;
   if (n > 1024 * s.nv) return {s.vec, 0, 1024, 1};
   s.threads = ((n + s.nv - 1) / s.nv + 31) / 32 * 32;
   s.rows = s.threads == 32 ? 4 : 1;
@@ -406,10 +649,10 @@ RowShape row_shape(int H, int vec16) {
 }  // namespace
 
 // Partial rows of dw that rmsnorm_bwd writes at most, for any machine size (a
-// CTA of short rows writes four).
+// CTA of short rows writes eight).
 long long rmsnorm_bwd_partials(long long R, long long H) {
   const long long most = H <= 32768 ? 1024 : 32;
-  return R < 4 ? 4 : R < most ? R : most;
+  return R < 8 ? 8 : R < most ? R : most;
 }
 
 template <typename T, int VEC>
@@ -444,19 +687,84 @@ template <typename T, int VEC>
 static cudaError_t bwd_nv(const RmsNormBwdArgs& a, const RowShape& sh, unsigned grid,
                           cudaStream_t s) {
   const dim3 block(sh.threads, sh.rows);
-  switch (sh.nv) {
-    case 1: rmsnorm_bwd_kernel<T, VEC, 1><<<grid, block, 0, s>>>(a); break;
-    case 2: rmsnorm_bwd_kernel<T, VEC, 2><<<grid, block, 0, s>>>(a); break;
-    case 4: rmsnorm_bwd_kernel<T, VEC, 4><<<grid, block, 0, s>>>(a); break;
-    default: rmsnorm_bwd_kernel<T, VEC, 8><<<grid, block, 0, s>>>(a); break;
+  if constexpr (VEC == 1) {
+    if (sh.nv == 1) rmsnorm_bwd_kernel<T, VEC, 1><<<grid, block, 0, s>>>(a);
+    else if (sh.nv == 2) rmsnorm_bwd_kernel<T, VEC, 2><<<grid, block, 0, s>>>(a);
   }
+  if (sh.nv == 4) rmsnorm_bwd_kernel<T, VEC, 4><<<grid, block, 0, s>>>(a);
+  else if (sh.nv == 8) rmsnorm_bwd_kernel<T, VEC, 8><<<grid, block, 0, s>>>(a);
   return cudaGetLastError();
+}
+
+// The ring kernel's shape for rows of H elements that start on 16-byte
+// boundaries; stages 0: none (longer rows).
+// About 512 threads an SM, two or four vectors each: at [65536, 8192] bf16 with
+// ds, one row by 1024 threads of one vector took 742 us, by 512 of two 600.
+// Three rows deep: 600 us against 630 with two and 639 with four; at
+// [65536, 4096] fp32 477 against 508 and 525.  Short rows, two CTAs an SM (room
+// for 128 registers) against three: [524288, 128] bf16 68 us against 81.
+struct RingShape {
+  int nv, lanes, groups;   // block (lanes, groups); groups > 1: rows within warps
+  int ctas, stages;
+  size_t smem;
+};
+
+RingShape ring_shape(int H, int vec16, int arrays) {
+  RingShape r = {};
+  const int n = H / vec16;
+  if (H % vec16 != 0 || n > 2048) return r;
+  if (n <= 128) {
+    r.nv = n <= 64 ? 2 : 4;
+    r.lanes = n <= 16 ? 8 : n <= 32 ? 16 : 32;
+    r.groups = 32 * kShortWarps / r.lanes;
+  } else {
+    r.nv = n <= 1024 ? 2 : 4;
+    r.lanes = ((n + r.nv - 1) / r.nv + 31) / 32 * 32;
+    r.groups = 1;
+  }
+  const int cta = r.lanes * r.groups;
+  r.ctas = cta < 512 ? 512 / cta : 1;
+  const size_t stage = static_cast<size_t>(arrays) * r.nv * cta * 16;
+  r.stages = r.ctas * 3 * stage <= 200u << 10 ? 3 : 2;
+  r.smem = r.stages * stage;
+  return r;
+}
+
+template <typename T, int NV, int S, bool kShort>
+static cudaError_t ring_launch(const RmsNormBwdArgs& a, const RingShape& r, unsigned grid,
+                               cudaStream_t s) {
+  const cudaError_t e = cudaFuncSetAttribute(rmsnorm_bwd_ring_kernel<T, NV, S, kShort>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             static_cast<int>(r.smem));
+  if (e != cudaSuccess) return e;
+  rmsnorm_bwd_ring_kernel<T, NV, S, kShort><<<grid, dim3(r.lanes, r.groups), r.smem, s>>>(a);
+  return cudaGetLastError();
+}
+
+template <typename T, int NV, bool kShort>
+static cudaError_t ring_stages(const RmsNormBwdArgs& a, const RingShape& r, unsigned grid,
+                               cudaStream_t s) {
+  return r.stages == 2 ? ring_launch<T, NV, 2, kShort>(a, r, grid, s)
+                       : ring_launch<T, NV, 3, kShort>(a, r, grid, s);
 }
 
 template <typename T>
 static cudaError_t bwd_t(const RmsNormBwdArgs& a, int num_sms, int* n_partials, cudaStream_t s) {
   const RowShape sh = row_shape(a.H, kVec16<T>);
   const long long most = rmsnorm_bwd_partials(a.R, a.H);
+  const RingShape ring = ring_shape(a.H, kVec16<T>, a.ds ? 3 : 2);
+  if (ring.stages > 0) {
+    const int abreast = ring.groups > 1 ? kShortWarps : 1;
+    long long grid = static_cast<long long>(num_sms) * ring.ctas;
+    const long long need = (a.R + abreast - 1) / abreast;
+    if (grid > need) grid = need > 0 ? need : 1;
+    if (grid > most) grid = most;
+    *n_partials = static_cast<int>(grid);
+    const unsigned g = static_cast<unsigned>(grid);
+    if (ring.groups > 1)
+      return ring.nv == 2 ? ring_stages<T, 2, true>(a, ring, g, s) : ring_stages<T, 4, true>(a, ring, g, s);
+    return ring.nv == 2 ? ring_stages<T, 2, false>(a, ring, g, s) : ring_stages<T, 4, false>(a, ring, g, s);
+  }
   if (sh.nv == 0) {
     const int splits = static_cast<int>(most < 32 ? most : 32);
     if (a.R > 0) rmsnorm_bwd_long_kernel<T><<<static_cast<unsigned>(a.R), 1024, 0, s>>>(a);
