@@ -24,6 +24,7 @@ the clipping of all gradients by their global norm.
 from __future__ import annotations
 
 import ctypes
+from array import array
 
 import torch
 
@@ -53,7 +54,13 @@ def ctypes_ptr(t: torch.Tensor) -> int:
     return t.data_ptr()
 
 
+# The handle alone where torch has the call for it: a Stream object costs 2 us.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(device) -> int:
+    if _raw_stream is not None and device.index is not None:
+        return _raw_stream(device.index)
     return torch.cuda.current_stream(device).cuda_stream
 
 
@@ -431,23 +438,38 @@ def fused_logprob_entropy(hidden, weight, targets, mask, spans=None, num_spans=N
 
 # ------------------------------------------------- operators around the LM head
 
+_ROW_CODES = {torch.bfloat16: EAS_BF16, torch.float32: EAS_FP32}
+
+
 def _row_code(t: torch.Tensor, name: str) -> int:
     """dtype code of a row operator's tensor; refuses what no kernel can read."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must be on a CUDA device, got {t.device}")
-    if t.dtype == torch.bfloat16:
-        return EAS_BF16
-    if t.dtype == torch.float32:
-        return EAS_FP32
-    raise TypeError(f"{name} must be bfloat16 or float32, got {t.dtype}")
+    code = _ROW_CODES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name} must be bfloat16 or float32, got {t.dtype}")
+    return code
+
+
+def _row_codes(ts, name: str) -> array:
+    """_row_code of each tensor of a list."""
+    try:
+        codes = array("i", [_ROW_CODES[t.dtype] for t in ts])
+        if all([t.is_cuda for t in ts]):
+            return codes
+    except (AttributeError, KeyError):
+        pass
+    return array("i", [_row_code(t, name) for t in ts])
 
 
 def _need_shape(t: torch.Tensor, name: str, dtype: torch.dtype, device, shape) -> None:
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
+            and t.device == device and t.is_contiguous()):
+        return
     _need(t, name, dtype, device)
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
 def rmsnorm_fwd(x, weight, eps: float = 1e-6, residual=None, mask=None, want_y: bool = True,
@@ -461,45 +483,54 @@ def rmsnorm_fwd(x, weight, eps: float = 1e-6, residual=None, mask=None, want_y: 
     zero codes and scale 1.  out: buffers for the four, None where one is to be
     allocated; s may be x or residual itself."""
     code = _row_code(x, "x")
-    dev, dt = x.device, x.dtype
-    if x.dim() != 2:
+    dev, dt, shape = x.device, x.dtype, x.shape
+    if len(shape) != 2:
         raise ValueError("x must be [R, H]")
-    R, H = x.shape
-    _need(x, "x", dt, dev)
+    R, H = shape
+    _need_shape(x, "x", dt, dev, shape)
     _need_shape(weight, "weight", dt, dev, (H,))
+    r = m = yp = qp = sp = scp = None
     if residual is not None:
-        _need_shape(residual, "residual", dt, dev, x.shape)
+        _need_shape(residual, "residual", dt, dev, shape)
+        r = residual.data_ptr()
     if mask is not None:
         _need_shape(mask, "mask", torch.uint8, dev, (R,))
+        m = mask.data_ptr()
     y, q, scale, s = out if out is not None else (None, None, None, None)
-    if not want_y:
+    if want_y:
+        if y is None:
+            y = torch.empty_like(x)
+        else:
+            _need_shape(y, "y", dt, dev, shape)
+        yp = y.data_ptr()
+    else:
         y = None
-    elif y is None:
-        y = torch.empty_like(x)
-    else:
-        _need_shape(y, "y", dt, dev, x.shape)
-    if not want_e4m3:
-        q = scale = None
-    else:
+    if want_e4m3:
         if q is None:
-            q = torch.empty((R, H), dtype=torch.uint8, device=dev)
+            q = torch.empty(shape, dtype=torch.uint8, device=dev)
         else:
             q = _as_codes(q)
-            _need_shape(q, "y_e4m3", torch.uint8, dev, x.shape)
+            _need_shape(q, "y_e4m3", torch.uint8, dev, shape)
         if scale is None:
             scale = torch.empty(R, dtype=torch.float32, device=dev)
         else:
             _need_shape(scale, "y_scale", torch.float32, dev, (R,))
-    if residual is None or not want_sum:
-        s = None
-    elif s is None:
-        s = torch.empty_like(x)
+        qp, scp = q.data_ptr(), scale.data_ptr()
     else:
-        _need_shape(s, "s", dt, dev, x.shape)
-    _lib.check(_lib.load().eas_rmsnorm_fwd(
-        _ptr(x), _ptr(residual), _ptr(weight), _ptr(mask), R, H, code, eps, _ptr(s), _ptr(y),
-        _ptr(q), _ptr(scale), _stream(dev)))
-    return y, q, scale, (x if residual is None and want_sum else s)
+        q = scale = None
+    if not want_sum:
+        s = None
+    elif residual is None:
+        s = x
+    else:
+        if s is None:
+            s = torch.empty_like(x)
+        else:
+            _need_shape(s, "s", dt, dev, shape)
+        sp = s.data_ptr()
+    _lib.check(_lib.load().eas_rmsnorm_fwd(x.data_ptr(), r, weight.data_ptr(), m, R, H, code, eps,
+                                           sp, yp, qp, scp, _stream(dev)))
+    return y, q, scale, s
 
 
 def rmsnorm_bwd_workspace_size(R: int, H: int) -> int:
@@ -611,25 +642,25 @@ def clip_grad_norm(grads, max_norm: float | None, out=None, ws=None, norm=None):
     the norm alone.  Where the norm is not finite nothing is scaled."""
     grads = list(grads)
     outs = grads if out is None else list(out)
-    if len(outs) != len(grads):
+    n = len(grads)
+    if len(outs) != n:
         raise ValueError("out must have one tensor for each gradient")
-    if not grads:
+    if n == 0:
         raise ValueError("no gradients")
-    codes = [_row_code(g, "grads") for g in grads]
+    codes = _row_codes(grads, "grads")
     dev = grads[0].device
     for g in grads:
-        if g.device != dev:
-            raise ValueError(f"gradient on {g.device}, expected {dev}")
-        if not g.is_contiguous():
-            raise ValueError("gradients must be contiguous")
-    out_codes = codes
+        if g.device != dev or not g.is_contiguous():
+            raise ValueError(f"gradients must be contiguous and on one device ({dev})")
+    ptrs = array("Q", [g.data_ptr() for g in grads])
+    out_codes, out_ptrs = codes, ptrs
     if out is not None:
-        out_codes = [_row_code(o, "out") for o in outs]
+        out_codes = _row_codes(outs, "out")
         for g, o in zip(grads, outs):
-            if o.device != dev or o.shape != g.shape or not o.is_contiguous():
+            if o.shape != g.shape or o.device != dev or not o.is_contiguous():
                 raise ValueError("out must be contiguous and have the gradients' shapes and device")
-    n = len(grads)
-    ptrs, i32 = ctypes.c_void_p * n, ctypes.c_int32 * n
+        out_ptrs = array("Q", [o.data_ptr() for o in outs])
+    numels = array("q", [g.numel() for g in grads])
     if norm is None:
         norm = torch.empty(1, dtype=torch.float32, device=dev)
     else:
@@ -638,9 +669,9 @@ def clip_grad_norm(grads, max_norm: float | None, out=None, ws=None, norm=None):
         ws = workspace(clip_grad_norm_workspace_size(n), dev)
     clip = max_norm is not None
     _lib.check(_lib.load().eas_clip_grad_norm(
-        ptrs(*[g.data_ptr() for g in grads]), ptrs(*[o.data_ptr() for o in outs]) if clip else None,
-        (ctypes.c_int64 * n)(*[g.numel() for g in grads]), i32(*codes), i32(*out_codes), n,
-        max_norm if clip else 0.0, _ptr(norm), _ptr(ws), ws.numel(), _stream(dev)))
+        ptrs.buffer_info()[0], out_ptrs.buffer_info()[0] if clip else None,
+        numels.buffer_info()[0], codes.buffer_info()[0], out_codes.buffer_info()[0], n,
+        max_norm if clip else 0.0, norm.data_ptr(), ws.data_ptr(), ws.numel(), _stream(dev)))
     return norm
 
 

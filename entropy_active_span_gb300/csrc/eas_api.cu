@@ -1128,14 +1128,10 @@ eas_status eas_embed_bwd(const int32_t* ids, const void* dout, int64_t T, int64_
                           accumulate, at<char>(ws, align_up(sizeof(DevStatus))),
                           static_cast<DevStatus*>(ws)};
   {
-    Trace tr_(kTrMemset, s);
-    EAS_CUDA(cudaMemsetAsync(ws, 0, sizeof(DevStatus), s), "clear status");
-  }
-  if (T > 0) {
     Trace tr_(kTrEmbedSort, s);
     EAS_CUDA(launch_embed_sort(a, s), "embed_sort");
   }
-  {
+  if (T > 0 || !accumulate) {
     Trace tr_(kTrEmbedBwd, s);
     EAS_CUDA(launch_embed_bwd(a, dtype == EAS_BF16, s), "embed_bwd");
   }

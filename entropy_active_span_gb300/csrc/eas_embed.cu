@@ -66,7 +66,8 @@ embed_fwd_kernel(const EmbedFwdArgs p) {
 
 // -------------------------------------------------------------------- sort
 
-// LSD radix sort of (id, token), kSortBins digits a pass.  A tile is a
+// LSD radix sort of (id, token), kSortBins digits a pass: here over several
+// launches, for lists that the cluster sort below does not hold.  A tile is a
 // multiple of kSortSub tokens so that there are at most kSortTiles tiles.
 constexpr int kSortBits = 9;
 constexpr int kSortBins = 1 << kSortBits;
@@ -100,6 +101,7 @@ __device__ __forceinline__ int sort_key(const SortPass& p, long long i) {
 __global__ void __launch_bounds__(kSortThreads) sort_hist_kernel(const SortPass p) {
   __shared__ int cnt[kSortBins];
   cnt[threadIdx.x] = 0;
+  wait_for_launch_before();
   __syncthreads();
   const long long lo = blockIdx.x * p.tile;
   const long long hi = lo + p.tile < p.T ? lo + p.tile : p.T;
@@ -120,6 +122,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_scatter_kernel(const SortPa
   __shared__ int cnt[kSortWarps][kSortBins];
   __shared__ int warp_sum[kSortWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  wait_for_launch_before();
 
   // where this tile's tokens of digit `tid` start
   int before = 0, total = 0;
@@ -182,6 +185,155 @@ __global__ void __launch_bounds__(kSortThreads) sort_scatter_kernel(const SortPa
   }
 }
 
+// The whole sort in one launch, for lists that fit the shared memory of a
+// cluster of eight CTAs.  CTA 0 .. 7 hold the list, 1024 * kRounds pairs each;
+// a pass ranks every warp's run of digits, adds the counts up over warps and
+// (through distributed shared memory) over CTAs, and moves each pair to its
+// place in whichever CTA holds that.  A thread keeps its pairs in registers
+// meanwhile, so one buffer is enough.
+constexpr int kClusterCtas = 8;
+constexpr int kClusterThreads = 1024;
+constexpr int kClusterWarps = kClusterThreads / 32;
+constexpr int kClusterRounds = 4;
+constexpr long long kClusterMost = 1ll * kClusterCtas * kClusterThreads * kClusterRounds;
+
+struct ClusterSort {
+  const int* ids;
+  int* keys_out;
+  int* pos_out;
+  long long T;
+  int V;
+  int passes;
+  DevStatus* status;
+};
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t peer_smem(uint32_t addr, int rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ int peer_load(uint32_t addr) {
+  int v;
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ void peer_store2(uint32_t addr, int a, int b) {
+  asm volatile("st.shared::cluster.v2.s32 [%0], {%1, %2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
+}
+
+template <int kRounds>
+__global__ void __cluster_dims__(kClusterCtas, 1, 1) __launch_bounds__(kClusterThreads)
+cluster_sort_kernel(const ClusterSort p) {
+  constexpr int kTile = kClusterThreads * kRounds;
+  // (key, token) pairs of this CTA [kTile], then counts [warps][digits]
+  extern __shared__ __align__(128) unsigned char smem[];
+  int2* pair = reinterpret_cast<int2*>(smem);
+  unsigned short(*cnt)[kSortBins] = reinterpret_cast<unsigned short(*)[kSortBins]>(smem + sizeof(int2) * kTile);
+  __shared__ int hist[kSortBins];
+  __shared__ int base[kSortBins];
+  __shared__ int warp_sum[kSortBins / 32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int rank = blockIdx.x;          // the first cluster: its rank is the block index
+  const int T = static_cast<int>(p.T);
+  if (rank == 0 && tid == 0) {
+    p.status->code = kStOk;
+    p.status->where = p.status->info = 0;
+  }
+  cluster_sync();                       // the status is clear, and every CTA runs
+  int key[kRounds], pos[kRounds];
+  unsigned short below[kRounds];
+  const int first = rank * kTile + warp * (32 * kRounds) + lane;
+#pragma unroll
+  for (int r = 0; r < kRounds; ++r) {
+    const int i = first + 32 * r;
+    key[r] = -1;
+    pos[r] = i;
+    if (i < T) {
+      const int id = p.ids[i];
+      if (id < -1 || id >= p.V) report(p.status, kStInvalidArg, kWhereEmbed, i);
+      key[r] = id >= 0 && id < p.V ? id : p.V;      // padding and bad ids go last
+    }
+  }
+  for (int pass = 0; pass < p.passes; ++pass) {
+    const int shift = pass * kSortBits;
+    if (pass > 0) {
+#pragma unroll
+      for (int r = 0; r < kRounds; ++r) {
+        const int i = first + 32 * r;
+        const int2 kp = pair[i - rank * kTile];
+        key[r] = i < T ? kp.x : -1;
+        pos[r] = kp.y;
+      }
+    }
+    for (int i = tid; i < kClusterWarps * kSortBins / 2; i += kClusterThreads)
+      reinterpret_cast<uint32_t*>(&cnt[0][0])[i] = 0;
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < kRounds; ++r) {
+      const int digit = key[r] >= 0 ? (key[r] >> shift) & (kSortBins - 1) : kSortBins;
+      const unsigned same = __match_any_sync(0xffffffffu, digit);
+      const int mine = __popc(same & ((1u << lane) - 1));
+      below[r] = static_cast<unsigned short>(mine);
+      if (key[r] >= 0) below[r] += cnt[warp][digit];
+      __syncwarp();
+      if (key[r] >= 0 && mine == 0) cnt[warp][digit] += static_cast<unsigned short>(__popc(same));
+      __syncwarp();
+    }
+    __syncthreads();
+    if (tid < kSortBins) {
+      int n = 0;
+#pragma unroll 8
+      for (int w = 0; w < kClusterWarps; ++w) {
+        const int c = cnt[w][tid];
+        cnt[w][tid] = static_cast<unsigned short>(n);
+        n += c;
+      }
+      hist[tid] = n;
+    }
+    cluster_sync();                     // every CTA's counts are out, its pairs in registers
+    int before = 0, total = 0, x = 0;
+    if (tid < kSortBins) {
+#pragma unroll
+      for (int c = 0; c < kClusterCtas; ++c) {
+        const int n = peer_load(peer_smem(smem_u32(&hist[tid]), c));
+        if (c < rank) before += n;
+        total += n;
+      }
+      x = total;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      if (lane == 31) warp_sum[warp] = x;
+    }
+    __syncthreads();
+    if (tid < kSortBins) {
+      int at = before + x - total;
+      for (int w = 0; w < warp; ++w) at += warp_sum[w];
+      base[tid] = at;
+    }
+    __syncthreads();
+    const bool last = pass + 1 == p.passes;
+#pragma unroll
+    for (int r = 0; r < kRounds; ++r) {
+      if (key[r] < 0) continue;
+      const int digit = (key[r] >> shift) & (kSortBins - 1);
+      const int to = base[digit] + cnt[warp][digit] + below[r];
+      if (last) {
+        p.keys_out[to] = key[r];
+        p.pos_out[to] = pos[r];
+      } else {
+        peer_store2(peer_smem(smem_u32(&pair[to % kTile]), to / kTile), key[r], pos[r]);
+      }
+    }
+    cluster_sync();                     // the pairs have arrived, and hist has been read
+  }
+}
+
 // --------------------------------------------------------------- summation
 
 struct SumArgs {
@@ -195,6 +347,8 @@ struct SumArgs {
   int chunk;
   float scale;
   int accumulate;
+  int sum_ctas;
+  int zero_rows;          // rows of dw a zeroing CTA looks after
 };
 
 template <int VEC>
@@ -217,12 +371,47 @@ constexpr int kSumThreads = 128;
 constexpr int kSumUnroll = 8;
 constexpr int kMaxChunk = 128;
 
-// CTA (x, y): chunk x of the sorted tokens, kSumThreads * VEC columns.
+// Zeros in rows [v0, v0 + p.zero_rows) of dw, but for those that a token names:
+// each row's id is looked up in the sorted list.
+__device__ __forceinline__ void zero_rows(const SumArgs& p, int block, int* skip) {
+  const long long v0 = static_cast<long long>(block) * p.zero_rows;
+  if (threadIdx.x < p.zero_rows) {
+    const long long v = v0 + threadIdx.x;
+    long long lo = 0, hi = p.T;
+    while (lo < hi) {
+      const long long mid = (lo + hi) >> 1;
+      if (p.keys[mid] < v) lo = mid + 1; else hi = mid;
+    }
+    skip[threadIdx.x] = v >= p.V || (lo < p.T && p.keys[lo] == v);
+  }
+  __syncthreads();
+  for (int r = 0; r < p.zero_rows; ++r) {
+    if (skip[r]) continue;
+    float* row = p.dw + (v0 + r) * p.H;
+    if (p.H % 4 == 0) {
+      for (int c = threadIdx.x * 4; c < p.H; c += kSumThreads * 4)
+        *reinterpret_cast<float4*>(row + c) = make_float4(0.f, 0.f, 0.f, 0.f);
+    } else {
+      for (int c = threadIdx.x; c < p.H; c += kSumThreads) row[c] = 0.f;
+    }
+  }
+}
+
+// CTA b < p.sum_ctas: chunk b / slabs of the sorted tokens, kSumThreads * VEC
+// columns.  The CTAs after them fill the rows that no token names, so that
+// their stores run beside the others' loads.
 template <typename T, int VEC>
 __global__ void __launch_bounds__(kSumThreads) embed_sum_kernel(const SumArgs p) {
   __shared__ int keys[kMaxChunk + 2];   // [0]: the key before the chunk, [n + 1]: the one after
   __shared__ int pos[kMaxChunk];
-  const long long i0 = static_cast<long long>(blockIdx.x) * p.chunk;
+  wait_for_launch_before();
+  if (blockIdx.x >= p.sum_ctas) {
+    zero_rows(p, blockIdx.x - p.sum_ctas, keys);
+    return;
+  }
+  const int slabs = (p.H + kSumThreads * VEC - 1) / (kSumThreads * VEC);
+  const int chunk = blockIdx.x / slabs, slab = blockIdx.x - chunk * slabs;
+  const long long i0 = static_cast<long long>(chunk) * p.chunk;
   const int n = static_cast<int>(p.T - i0 < p.chunk ? p.T - i0 : p.chunk);
   for (int i = threadIdx.x; i < n + 2; i += kSumThreads) {
     const long long k = i0 + i - 1;
@@ -230,7 +419,7 @@ __global__ void __launch_bounds__(kSumThreads) embed_sum_kernel(const SumArgs p)
     if (i < n) pos[i] = p.pos[i0 + i];
   }
   __syncthreads();
-  const int c = (blockIdx.y * kSumThreads + threadIdx.x) * VEC;
+  const int c = (slab * kSumThreads + threadIdx.x) * VEC;
   if (c >= p.H) return;
   const T* dout = static_cast<const T*>(p.dout) + c;
   float acc[VEC] = {};
@@ -257,7 +446,7 @@ __global__ void __launch_bounds__(kSumThreads) embed_sum_kernel(const SumArgs p)
           if (!from_before && !goes_on) {
             put_row<VEC>(p.dw + static_cast<long long>(key) * p.H + c, acc, p.scale, p.accumulate);
           } else {
-            float* q = p.partial + (2ll * blockIdx.x + (from_before ? 0 : 1)) * p.H + c;
+            float* q = p.partial + (2ll * chunk + (from_before ? 0 : 1)) * p.H + c;
             put_row<VEC>(q, acc, 1.f, 0);
           }
           start = k + 1;
@@ -272,6 +461,7 @@ __global__ void __launch_bounds__(kSumThreads) embed_sum_kernel(const SumArgs p)
 // Adds up the runs that cross chunks: the CTAs of the chunk in which a run
 // starts walk the chunks it covers.
 __global__ void __launch_bounds__(kSumThreads) embed_join_kernel(const SumArgs p, int n_chunks) {
+  wait_for_launch_before();
   const long long end = static_cast<long long>(blockIdx.x + 1) * p.chunk;
   if (end >= p.T) return;
   const int key = p.keys[end - 1];
@@ -291,31 +481,6 @@ __global__ void __launch_bounds__(kSumThreads) embed_join_kernel(const SumArgs p
   for (int k = blockIdx.x + 1; k <= last; ++k) acc += p.partial[2ll * k * p.H + c];
   const float a[1] = {acc};
   put_row<1>(p.dw + static_cast<long long>(key) * p.H + c, a, p.scale, p.accumulate);
-}
-
-// Zeros in the rows of dw that no token touches: a row's id is looked up in
-// the sorted list.
-constexpr int kZeroRows = 8;
-template <int VEC>
-__global__ void __launch_bounds__(256) embed_zero_kernel(const SumArgs p) {
-  __shared__ int skip[kZeroRows];
-  const int v0 = blockIdx.x * kZeroRows;
-  if (threadIdx.x < kZeroRows) {
-    const int v = v0 + threadIdx.x;
-    long long lo = 0, hi = p.T;
-    while (lo < hi) {
-      const long long mid = (lo + hi) >> 1;
-      if (p.keys[mid] < v) lo = mid + 1; else hi = mid;
-    }
-    skip[threadIdx.x] = v >= p.V || (lo < p.T && p.keys[lo] == v);
-  }
-  __syncthreads();
-  const float z[VEC] = {};
-  for (int r = 0; r < kZeroRows; ++r) {
-    if (skip[r]) continue;
-    float* row = p.dw + static_cast<long long>(v0 + r) * p.H;
-    for (int c = threadIdx.x * VEC; c < p.H; c += 256 * VEC) store_vec<float, VEC>(row + c, z);
-  }
 }
 
 size_t up(size_t x) { return (x + 255) / 256 * 256; }
@@ -338,6 +503,9 @@ SumArgs sum_args(const EmbedBwdArgs& a, const EmbedBwdPlan& pl, int buf) {
   s.chunk = pl.chunk;
   s.scale = a.scale;
   s.accumulate = a.accumulate;
+  s.sum_ctas = 0;
+  const long long rows = 32768 / (a.H > 0 ? a.H : 1);   // 128 KB of dw
+  s.zero_rows = static_cast<int>(rows < 4 ? 4 : rows > kSumThreads ? kSumThreads : rows);
   return s;
 }
 
@@ -390,9 +558,35 @@ EmbedBwdPlan embed_bwd_plan(long long T, long long H, long long V) {
   return p;
 }
 
+template <int kRounds>
+static cudaError_t cluster_sort(const ClusterSort& p, cudaStream_t s) {
+  const int smem = kClusterThreads * kRounds * static_cast<int>(sizeof(int2)) +
+                   kClusterWarps * kSortBins * static_cast<int>(sizeof(short));
+  const cudaError_t e = cudaFuncSetAttribute(cluster_sort_kernel<kRounds>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  cluster_sort_kernel<kRounds><<<kClusterCtas, kClusterThreads, smem, s>>>(p);
+  return cudaGetLastError();
+}
+
 cudaError_t launch_embed_sort(const EmbedBwdArgs& a, cudaStream_t s) {
   const EmbedBwdPlan pl = embed_bwd_plan(a.T, a.H, a.V);
   const int passes = sort_passes(a.V);
+  if (a.T <= kClusterMost) {
+    ClusterSort p;
+    p.ids = a.ids;
+    p.keys_out = reinterpret_cast<int*>(a.scratch + pl.keys[(passes - 1) & 1]);
+    p.pos_out = reinterpret_cast<int*>(a.scratch + pl.pos[(passes - 1) & 1]);
+    p.T = a.T;
+    p.V = a.V;
+    p.passes = passes;
+    p.status = a.status;
+    const long long per = 1ll * kClusterCtas * kClusterThreads;
+    return a.T <= per ? cluster_sort<1>(p, s)
+                      : a.T <= 2 * per ? cluster_sort<2>(p, s) : cluster_sort<4>(p, s);
+  }
+  cudaError_t e = cudaMemsetAsync(a.status, 0, sizeof(DevStatus), s);
+  if (e != cudaSuccess) return e;
   for (int i = 0; i < passes; ++i) {
     SortPass p;
     p.ids = i == 0 ? a.ids : nullptr;
@@ -407,39 +601,42 @@ cudaError_t launch_embed_sort(const EmbedBwdArgs& a, cudaStream_t s) {
     p.tile = sort_tile(a.T);
     p.n_tiles = static_cast<int>((a.T + p.tile - 1) / p.tile);
     p.status = a.status;
-    sort_hist_kernel<<<p.n_tiles, kSortThreads, 0, s>>>(p);
-    sort_scatter_kernel<<<p.n_tiles, kSortThreads, 0, s>>>(p);
+    if (i == 0) {
+      sort_hist_kernel<<<p.n_tiles, kSortThreads, 0, s>>>(p);
+      e = cudaGetLastError();
+    } else {
+      e = launch_overlapped(sort_hist_kernel, dim3(p.n_tiles), dim3(kSortThreads), 0, s, p);
+    }
+    if (e == cudaSuccess)
+      e = launch_overlapped(sort_scatter_kernel, dim3(p.n_tiles), dim3(kSortThreads), 0, s, p);
+    if (e != cudaSuccess) return e;
   }
-  return cudaGetLastError();
+  return cudaSuccess;
 }
 
 template <typename T, int VEC>
-static void sum_t(const SumArgs& s, int n_chunks, cudaStream_t st) {
-  const dim3 grid(n_chunks, (s.H + kSumThreads * VEC - 1) / (kSumThreads * VEC));
-  embed_sum_kernel<T, VEC><<<grid, kSumThreads, 0, st>>>(s);
+static cudaError_t sum_t(SumArgs s, int n_chunks, cudaStream_t st) {
+  const long long slabs = (s.H + kSumThreads * VEC - 1) / (kSumThreads * VEC);
+  const long long zeros = s.accumulate ? 0 : (static_cast<long long>(s.V) + s.zero_rows - 1) / s.zero_rows;
+  s.sum_ctas = static_cast<int>(n_chunks * slabs);
+  return launch_overlapped(embed_sum_kernel<T, VEC>, dim3(static_cast<unsigned>(s.sum_ctas + zeros)),
+                           dim3(kSumThreads), 0, st, s);
 }
 
 cudaError_t launch_embed_bwd(const EmbedBwdArgs& a, int is_bf16, cudaStream_t st) {
   const EmbedBwdPlan pl = embed_bwd_plan(a.T, a.H, a.V);
   const SumArgs s = sum_args(a, pl, (sort_passes(a.V) - 1) & 1);
-  if (!a.accumulate) {
-    const unsigned g = static_cast<unsigned>((static_cast<long long>(a.V) + kZeroRows - 1) / kZeroRows);
-    if (a.H % 4 == 0) embed_zero_kernel<4><<<g, 256, 0, st>>>(s);
-    else embed_zero_kernel<1><<<g, 256, 0, st>>>(s);
-  }
-  if (a.T == 0) return cudaGetLastError();
   const int n_chunks = static_cast<int>((a.T + pl.chunk - 1) / pl.chunk);
   const int vec16 = is_bf16 ? 8 : 4;
-  if (a.H % vec16 == 0) {
-    if (is_bf16) sum_t<__nv_bfloat16, 8>(s, n_chunks, st);
-    else sum_t<float, 4>(s, n_chunks, st);
-  } else {
-    if (is_bf16) sum_t<__nv_bfloat16, 1>(s, n_chunks, st);
-    else sum_t<float, 1>(s, n_chunks, st);
-  }
-  if (n_chunks > 1)
-    embed_join_kernel<<<dim3(n_chunks, (a.H + kSumThreads - 1) / kSumThreads), kSumThreads, 0, st>>>(s, n_chunks);
-  return cudaGetLastError();
+  cudaError_t e;
+  if (a.H % vec16 == 0)
+    e = is_bf16 ? sum_t<__nv_bfloat16, 8>(s, n_chunks, st) : sum_t<float, 4>(s, n_chunks, st);
+  else
+    e = is_bf16 ? sum_t<__nv_bfloat16, 1>(s, n_chunks, st) : sum_t<float, 1>(s, n_chunks, st);
+  if (e != cudaSuccess || n_chunks <= 1) return e;
+  return launch_overlapped(embed_join_kernel,
+                           dim3(n_chunks, (a.H + kSumThreads - 1) / kSumThreads), dim3(kSumThreads),
+                           0, st, s, n_chunks);
 }
 
 }  // namespace eas

@@ -10,6 +10,25 @@ namespace eas {
 struct DevStatus;
 struct Sched;
 
+// Launches a kernel that may begin before the launch in front of it on the
+// stream has ended; it calls wait_for_launch_before() ahead of its first use of
+// that launch's results, or at its end.
+template <typename... P, typename... A>
+cudaError_t launch_overlapped(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem,
+                              cudaStream_t s, A... args) {
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+
 // ---- span builder and row schedule (eas_sched.cu) ----
 cudaError_t launch_spans_build(const uint8_t* mask, long long T, int max_gap, int* spans,
                                long long cap, int* num_spans, DevStatus* st, cudaStream_t s);
@@ -228,6 +247,7 @@ struct EmbedBwdArgs {
   char* scratch;
   DevStatus* status;
 };
+// The sort clears the status word.
 cudaError_t launch_embed_sort(const EmbedBwdArgs& a, cudaStream_t s);
 cudaError_t launch_embed_bwd(const EmbedBwdArgs& a, int is_bf16, cudaStream_t s);
 

@@ -108,9 +108,10 @@ def test_a_run_across_many_chunks():
     check_bwd(ids, dout, V, 1.0, dw)
 
 
-@pytest.mark.parametrize("T", [262144 + 77, 600000])
+@pytest.mark.parametrize("T", [8192, 8193, 20000, 50001, 131072, 131073, 262144 + 77, 600000])
 def test_large_sorts(T):
-    """Several sort tiles, and tiles of several rounds: integers, so exact."""
+    """The sort in one launch at each of its sizes, and beyond them over several:
+    integers, so exact."""
     V, H = 152064, 8
     ids = make_ids(T, V, "padded", seed=3)
     dout = torch.ones(T, H, dtype=torch.bfloat16, device="cuda")
