@@ -1100,7 +1100,7 @@ eas_status eas_embed_fwd(const int32_t* ids, const void* table, int64_t T, int64
   const EmbedFwdArgs a = {ids, table, out, T, static_cast<int>(V), static_cast<int>(H), scale,
                           static_cast<DevStatus*>(ws)};
   Trace tr_(kTrEmbedFwd, s);
-  EAS_CUDA(launch_embed_fwd(a, dtype == EAS_BF16, s), "embed_fwd");
+  EAS_CUDA(launch_embed_fwd(a, dtype == EAS_BF16, di.sms, s), "embed_fwd");
   return EAS_OK;
 }
 

@@ -226,7 +226,7 @@ struct EmbedFwdArgs {
   float scale;
   DevStatus* status;      // or null
 };
-cudaError_t launch_embed_fwd(const EmbedFwdArgs& a, int is_bf16, cudaStream_t s);
+cudaError_t launch_embed_fwd(const EmbedFwdArgs& a, int is_bf16, int num_sms, cudaStream_t s);
 
 struct EmbedBwdPlan {     // sizes of the backward's scratch, in bytes from its start
   size_t keys[2], pos[2]; // the sort's two buffers of (id, token)

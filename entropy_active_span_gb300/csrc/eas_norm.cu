@@ -317,12 +317,13 @@ rmsnorm_bwd_kernel(const RmsNormBwdArgs p) {
 // the vectors that it will itself consume into its own slots of a ring in
 // shared memory, kStages rows deep, with cp.async.  A thread waits for its own
 // copies only, so the ring needs no barrier; the one barrier a row is the
-// reduction's.  With a mask the group first lists its active rows and fills the
-// others while the first copies are on their way, so that the ring holds
-// active rows alone.
+// reduction's.  With a mask the group lists its active rows, and the ring holds
+// those alone; the others are norm_bwd_fill_kernel's.
 //
 // A CTA holds one row at a time, or (kShort) each of its eight warps its own
-// rows, blockDim.x lanes a row.
+// rows, blockDim.x lanes a row.  Whether there is a ds and a mask is compiled in
+// for the longer rows: [65536, 5120] bf16 with ds took 447 us deciding in the
+// loop and 397 without.
 __device__ __forceinline__ void cp_async16(void* smem, const void* gmem) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(smem)), "l"(gmem) : "memory");
 }
@@ -335,10 +336,11 @@ __device__ __forceinline__ void cp_async_wait() {
 constexpr int kListRows = 512;    // rows a group lists at a time
 constexpr int kShortWarps = 8;
 
-template <typename T, int NV, int kStages, bool kShort>
+template <typename T, int NV, int kStages, bool kShort, bool kDs, bool kMask>
 __global__ void __launch_bounds__(kShort ? 256 : 512, kShort ? 2 : 1)
 rmsnorm_bwd_ring_kernel(const RmsNormBwdArgs p) {
   constexpr int VEC = kVec16<T>;
+  launch_dependents();                  // the rows left out, on what this grid leaves free
   // [kStages][2 or 3][NV][threads of the CTA].  Where it started on a 16-byte
   // but no 128-byte boundary, each cp.async fetched its sectors from L2 twice.
   extern __shared__ __align__(128) uint4 ring[];
@@ -352,7 +354,10 @@ rmsnorm_bwd_ring_kernel(const RmsNormBwdArgs p) {
   const int groups = kShort ? kShortWarps : 1;
   const int abreast = kShort ? 32 / blockDim.x : 1;       // rows a group holds at a time
   const int sub = kShort ? lane / blockDim.x : 0;
-  const int arrays = p.ds ? 3 : 2;
+  // short rows decide while they run
+  const bool with_ds = kShort ? p.ds != nullptr : kDs;
+  const bool masked = kShort ? p.mask != nullptr : kMask;
+  const int arrays = with_ds ? 3 : 2;
   const T* dy = static_cast<const T*>(p.dy);
   const T* sv = static_cast<const T*>(p.s);
   const T* ds = static_cast<const T*>(p.ds);
@@ -380,22 +385,16 @@ rmsnorm_bwd_ring_kernel(const RmsNormBwdArgs p) {
     const int span = static_cast<int>(rows - base < kListRows ? rows - base : kListRows);
     int n = span;
     unsigned short* mine = list[group];
-    if (p.mask) {
-      // a warp of the group lists the active rows from the front and the
-      // others from the back
+    if (masked) {
+      // a warp of the group lists the active rows
       if (kShort || warp == 0) {
-        int on = 0, off = 0;
+        int on = 0;
         for (int i0 = 0; i0 < span; i0 += 32) {
           const int i = i0 + lane;
-          const bool valid = i < span;
-          const bool a = valid && p.mask[first + (base + i) * step] != 0;
+          const bool a = i < span && p.mask[first + (base + i) * step] != 0;
           const unsigned m = __ballot_sync(0xffffffffu, a);
-          const unsigned z = __ballot_sync(0xffffffffu, valid && !a);
-          const unsigned below = (1u << lane) - 1;
-          if (a) mine[on + __popc(m & below)] = static_cast<unsigned short>(i);
-          else if (valid) mine[kListRows - 1 - off - __popc(z & below)] = static_cast<unsigned short>(i);
+          if (a) mine[on + __popc(m & ((1u << lane) - 1))] = static_cast<unsigned short>(i);
           on += __popc(m);
-          off += __popc(z);
         }
         n = on;
         if (!kShort && lane == 0) listed = on;
@@ -408,7 +407,7 @@ rmsnorm_bwd_ring_kernel(const RmsNormBwdArgs p) {
       }
     }
     auto row_at = [&](int k) -> long long {
-      return first + (base + (p.mask ? mine[k] : k)) * step;
+      return first + (base + (masked ? mine[k] : k)) * step;
     };
     auto issue = [&](int k) {
       const int e = k * abreast + sub;
@@ -421,7 +420,7 @@ rmsnorm_bwd_ring_kernel(const RmsNormBwdArgs p) {
           if (in[j]) {
             cp_async16(slot + j * cta, dy + off + c);
             cp_async16(slot + (NV + j) * cta, sv + off + c);
-            if (ds) cp_async16(slot + (2 * NV + j) * cta, ds + off + c);
+            if (with_ds) cp_async16(slot + (2 * NV + j) * cta, ds + off + c);
           }
         }
       }
@@ -429,20 +428,6 @@ rmsnorm_bwd_ring_kernel(const RmsNormBwdArgs p) {
     };
 #pragma unroll
     for (int k = 0; k < kStages - 1; ++k) issue(k);
-
-    if (p.mask && !(ds && static_cast<const void*>(ds) == p.dx)) {   // in place: ds is there already
-#pragma unroll 2
-      for (int e = sub; e < span - n; e += abreast) {
-        const long long off = (first + (base + mine[kListRows - 1 - e]) * step) * p.H;
-#pragma unroll
-        for (int j = 0; j < NV; ++j) {
-          const int c = (j * blockDim.x + threadIdx.x) * VEC;
-          if (in[j])
-            *reinterpret_cast<uint4*>(dx + off + c) =
-                ds ? *reinterpret_cast<const uint4*>(ds + off + c) : make_uint4(0, 0, 0, 0);
-        }
-      }
-    }
 
     for (int k = 0; k * abreast < n; ++k) {
       issue(k + kStages - 1);
@@ -489,7 +474,7 @@ rmsnorm_bwd_ring_kernel(const RmsNormBwdArgs p) {
           widen<T, VEC>(rsv[j], s);
           widen<T, VEC>(rdy[j], d);
           widen<T, VEC>(rw[j], wf);
-          if (ds) {
+          if (with_ds) {
             Raw<T, VEC> r;
             r.v = slot[(2 * NV + j) * cta];
             widen<T, VEC>(r, o);
@@ -505,7 +490,7 @@ rmsnorm_bwd_ring_kernel(const RmsNormBwdArgs p) {
     }
     cp_async_wait<0>();
     // the list is written again only after every warp is done with it
-    if (p.mask && base + kListRows < rows) {
+    if (masked && base + kListRows < rows) {
       if constexpr (kShort) __syncwarp(); else __syncthreads();
     }
   }
@@ -548,6 +533,30 @@ rmsnorm_bwd_ring_kernel(const RmsNormBwdArgs p) {
       }
     }
   }
+}
+
+// dx = ds or 0 on the inactive rows, for the ring kernel; it runs beside that
+// one.  Small CTAs in the order of the rows: where the ring kernel's CTAs wrote
+// these rows themselves, one a SM and each at its own pace, [131072, 7168] bf16
+// with 10 % active rows took 388 us against 350.
+struct FillArgs {
+  const uint4* ds;        // or null
+  uint4* dx;
+  const uint8_t* mask;
+  long long R;
+  int vecs;               // 16-byte vectors of a row
+  int rows;               // rows of a CTA
+};
+__global__ void __launch_bounds__(256) norm_bwd_fill_kernel(const FillArgs p) {
+  const long long r0 = static_cast<long long>(blockIdx.x) * p.rows;
+  for (int r = threadIdx.y; r < p.rows && r0 + r < p.R; r += blockDim.y) {
+    if (p.mask[r0 + r] != 0) continue;
+    const long long off = (r0 + r) * p.vecs;
+#pragma unroll 4
+    for (int v = threadIdx.x; v < p.vecs; v += blockDim.x)
+      p.dx[off + v] = p.ds ? p.ds[off + v] : make_uint4(0, 0, 0, 0);
+  }
+  wait_for_launch_before();   // whoever waits for this launch waits for the ring kernel too
 }
 
 // Rows too long for registers: dx in two walks of the row, the row's rstd
@@ -730,22 +739,34 @@ RingShape ring_shape(int H, int vec16, int arrays) {
   return r;
 }
 
-template <typename T, int NV, int S, bool kShort>
+template <typename T, int NV, int S, bool kShort, bool kDs, bool kMask>
 static cudaError_t ring_launch(const RmsNormBwdArgs& a, const RingShape& r, unsigned grid,
                                cudaStream_t s) {
-  const cudaError_t e = cudaFuncSetAttribute(rmsnorm_bwd_ring_kernel<T, NV, S, kShort>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize,
+  const auto kernel = rmsnorm_bwd_ring_kernel<T, NV, S, kShort, kDs, kMask>;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              static_cast<int>(r.smem));
   if (e != cudaSuccess) return e;
-  rmsnorm_bwd_ring_kernel<T, NV, S, kShort><<<grid, dim3(r.lanes, r.groups), r.smem, s>>>(a);
+  kernel<<<grid, dim3(r.lanes, r.groups), r.smem, s>>>(a);
   return cudaGetLastError();
 }
 
-template <typename T, int NV, bool kShort>
-static cudaError_t ring_stages(const RmsNormBwdArgs& a, const RingShape& r, unsigned grid,
-                               cudaStream_t s) {
-  return r.stages == 2 ? ring_launch<T, NV, 2, kShort>(a, r, grid, s)
-                       : ring_launch<T, NV, 3, kShort>(a, r, grid, s);
+template <typename T, int NV, int S>
+static cudaError_t ring_kind(const RmsNormBwdArgs& a, const RingShape& r, unsigned grid,
+                             cudaStream_t s) {
+  if (r.groups > 1) return ring_launch<T, NV, S, true, false, false>(a, r, grid, s);
+  if (a.ds)
+    return a.mask ? ring_launch<T, NV, S, false, true, true>(a, r, grid, s)
+                  : ring_launch<T, NV, S, false, true, false>(a, r, grid, s);
+  return a.mask ? ring_launch<T, NV, S, false, false, true>(a, r, grid, s)
+                : ring_launch<T, NV, S, false, false, false>(a, r, grid, s);
+}
+
+template <typename T>
+static cudaError_t ring_run(const RmsNormBwdArgs& a, const RingShape& r, unsigned grid,
+                            cudaStream_t s) {
+  if (r.nv == 2)
+    return r.stages == 2 ? ring_kind<T, 2, 2>(a, r, grid, s) : ring_kind<T, 2, 3>(a, r, grid, s);
+  return r.stages == 2 ? ring_kind<T, 4, 2>(a, r, grid, s) : ring_kind<T, 4, 3>(a, r, grid, s);
 }
 
 template <typename T>
@@ -760,10 +781,16 @@ static cudaError_t bwd_t(const RmsNormBwdArgs& a, int num_sms, int* n_partials, 
     if (grid > need) grid = need > 0 ? need : 1;
     if (grid > most) grid = most;
     *n_partials = static_cast<int>(grid);
-    const unsigned g = static_cast<unsigned>(grid);
-    if (ring.groups > 1)
-      return ring.nv == 2 ? ring_stages<T, 2, true>(a, ring, g, s) : ring_stages<T, 4, true>(a, ring, g, s);
-    return ring.nv == 2 ? ring_stages<T, 2, false>(a, ring, g, s) : ring_stages<T, 4, false>(a, ring, g, s);
+    const cudaError_t e = ring_run<T>(a, ring, static_cast<unsigned>(grid), s);
+    if (e != cudaSuccess || !a.mask || a.ds == a.dx || a.R == 0) return e;   // in place: ds is there
+    FillArgs f = {static_cast<const uint4*>(a.ds), static_cast<uint4*>(a.dx), a.mask, a.R,
+                  a.H / kVec16<T>, 0};
+    f.rows = f.vecs >= 4096 ? 1 : 4096 / f.vecs < 256 ? 4096 / f.vecs : 256;   // about 64 KB
+    int tx = 16;
+    while (tx < 256 && tx < f.vecs) tx *= 2;
+    const long long fill = (a.R + f.rows - 1) / f.rows;
+    return launch_overlapped(norm_bwd_fill_kernel, dim3(static_cast<unsigned>(fill)),
+                             dim3(tx, 256 / tx), 0, s, f);
   }
   if (sh.nv == 0) {
     const int splits = static_cast<int>(most < 32 ? most : 32);
