@@ -1028,7 +1028,7 @@ eas_status eas_rmsnorm_fwd(const void* x, const void* residual, const void* weig
   const RmsNormFwdArgs a = {x, residual, weight, mask, sum_out, y, y_e4m3, y_scale,
                             R, static_cast<int>(H), eps};
   Trace tr_(kTrNormFwd, s);
-  EAS_CUDA(launch_rmsnorm_fwd(a, dtype == EAS_BF16, s), "rmsnorm_fwd");
+  EAS_CUDA(launch_rmsnorm_fwd(a, dtype == EAS_BF16, di.sms, s), "rmsnorm_fwd");
   return EAS_OK;
 }
 

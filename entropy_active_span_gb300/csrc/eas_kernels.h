@@ -195,7 +195,7 @@ struct RmsNormFwdArgs {
   int H;
   float eps;
 };
-cudaError_t launch_rmsnorm_fwd(const RmsNormFwdArgs& a, int is_bf16, cudaStream_t s);
+cudaError_t launch_rmsnorm_fwd(const RmsNormFwdArgs& a, int is_bf16, int num_sms, cudaStream_t s);
 
 struct RmsNormBwdArgs {
   const void* dy;         // [R][H]
