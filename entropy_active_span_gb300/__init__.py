@@ -454,10 +454,11 @@ def _row_code(t: torch.Tensor, name: str) -> int:
 
 
 def _row_codes(ts, name: str) -> array:
-    """_row_code of each tensor of a list."""
+    """_row_code of each tensor of a list (of the first one's device: the caller
+    checks that the others are on it)."""
     try:
         codes = array("i", [_ROW_CODES[t.dtype] for t in ts])
-        if all([t.is_cuda for t in ts]):
+        if ts[0].is_cuda:
             return codes
     except (AttributeError, KeyError):
         pass
@@ -647,20 +648,22 @@ def clip_grad_norm(grads, max_norm: float | None, out=None, ws=None, norm=None):
         raise ValueError("out must have one tensor for each gradient")
     if n == 0:
         raise ValueError("no gradients")
+    # maps over the methods themselves: a list has hundreds of tensors, and what
+    # the host does for each is the whole time of a small call
+    T = torch.Tensor
     codes = _row_codes(grads, "grads")
-    dev = grads[0].device
-    for g in grads:
-        if g.device != dev or not g.is_contiguous():
-            raise ValueError(f"gradients must be contiguous and on one device ({dev})")
-    ptrs = array("Q", [g.data_ptr() for g in grads])
+    dev, index = grads[0].device, grads[0].get_device()
+    if not (all(map(T.is_contiguous, grads)) and set(map(T.get_device, grads)) == {index}):
+        raise ValueError(f"gradients must be contiguous and on one device ({dev})")
+    ptrs = array("Q", map(T.data_ptr, grads))
     out_codes, out_ptrs = codes, ptrs
     if out is not None:
         out_codes = _row_codes(outs, "out")
-        for g, o in zip(grads, outs):
-            if o.shape != g.shape or o.device != dev or not o.is_contiguous():
-                raise ValueError("out must be contiguous and have the gradients' shapes and device")
-        out_ptrs = array("Q", [o.data_ptr() for o in outs])
-    numels = array("q", [g.numel() for g in grads])
+        if not (all(map(T.is_contiguous, outs)) and set(map(T.get_device, outs)) == {index}
+                and [g.shape for g in grads] == [o.shape for o in outs]):
+            raise ValueError("out must be contiguous and have the gradients' shapes and device")
+        out_ptrs = array("Q", map(T.data_ptr, outs))
+    numels = array("q", map(T.numel, grads))
     if norm is None:
         norm = torch.empty(1, dtype=torch.float32, device=dev)
     else:

@@ -37,14 +37,18 @@ struct List {
   int log_chunk;
 };
 
+// The tensor that a chunk belongs to.  The last 32 candidates are compared at
+// once, a lane each: a bisection to the end is a chain of first-time loads of
+// the argument, 18 tensors took five of them in a row.
 template <int N>
 __device__ __forceinline__ int tensor_of(const List<N>& l, int chunk) {
   int lo = 0, hi = l.n;
-  while (hi - lo > 1) {
+  while (hi - lo > 32) {
     const int mid = (lo + hi) >> 1;
     if (l.first[mid] <= chunk) lo = mid; else hi = mid;
   }
-  return lo;
+  const int i = lo + (threadIdx.x & 31);
+  return lo + __popc(__ballot_sync(0xffffffffu, i < hi && l.first[i] <= chunk)) - 1;
 }
 
 // A running sum of squares: hi + lo in fp32, exact to about 2^-48 (each group's
@@ -152,6 +156,7 @@ template <int N>
 __global__ void __launch_bounds__(kThreads)
 grad_squares_kernel(const __grid_constant__ List<N> l, double* partial) {
   __shared__ double sm[kThreads / 32];
+  launch_dependents();
   Squares acc;
   for (int k = blockIdx.x; k < l.n_chunks; k += gridDim.x) {
     const int t = tensor_of(l, k);
@@ -177,6 +182,7 @@ __device__ __forceinline__ float norm_of(const double* partial, int n, double* s
 __global__ void __launch_bounds__(kThreads)
 grad_norm_kernel(const double* partial, int n, float* norm) {
   __shared__ double sm[kThreads / 32];
+  wait_for_launch_before();
   const float v = norm_of(partial, n, sm);
   if (threadIdx.x == 0) *norm = v;
 }
@@ -228,12 +234,15 @@ __global__ void __launch_bounds__(kThreads)
 grad_clip_kernel(const __grid_constant__ List<N> l, const double* partial, int n_partial,
                  float* norm, float max_norm) {
   __shared__ double sm[kThreads / 32];
+  // the first chunk's tensor is looked up while the norm is on its way
+  int k = l.n_chunks - 1 - blockIdx.x;
+  int t = tensor_of(l, k);
+  wait_for_launch_before();
   const float v = norm_of(partial, n_partial, sm);
   if (blockIdx.x == 0 && threadIdx.x == 0) *norm = v;
   const float c = isfinite(v) ? fminf(1.f, max_norm / (v + 1e-6f)) : 1.f;
   // from the last chunk down: what the norm read last is still in L2
-  for (int k = l.n_chunks - 1 - blockIdx.x; k >= 0; k -= gridDim.x) {
-    const int t = tensor_of(l, k);
+  for (; k >= 0; k -= gridDim.x, t = k >= 0 ? tensor_of(l, k) : 0) {
     if (c == 1.f && l.in[t] == l.out[t]) continue;   // in place: nothing changes
     const long long off = static_cast<long long>(k - l.first[t]) << l.log_chunk;
     const long long left = l.numel[t] - off;
@@ -303,14 +312,16 @@ cudaError_t launch_lists(const ClipTensor* t, int n, bool clip, float max_norm, 
     grad_squares_kernel<N><<<g, kThreads, 0, s>>>(l, partial + np);
     np += g;
   }
-  if (!clip || np == 0) {
-    grad_norm_kernel<<<1, kThreads, 0, s>>>(partial, np, norm);
-    return cudaGetLastError();
-  }
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  if (!clip || np == 0)
+    return launch_overlapped(grad_norm_kernel, dim3(1), dim3(kThreads), 0, s, partial, np, norm);
   for (int at = 0; at < n;) {
     at = fill(l, t, n, at, lc);
     if (l.n_chunks == 0) continue;
-    grad_clip_kernel<N><<<ctas(l.n_chunks, num_sms), kThreads, 0, s>>>(l, partial, np, norm, max_norm);
+    e = launch_overlapped(grad_clip_kernel<N>, dim3(ctas(l.n_chunks, num_sms)), dim3(kThreads), 0, s,
+                          l, partial, np, norm, max_norm);
+    if (e != cudaSuccess) return e;
   }
   return cudaGetLastError();
 }

@@ -729,6 +729,7 @@ rmsnorm_dw_kernel(const float* __restrict__ partial, int n, int H, float* __rest
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
   float acc = 0.f;
+  wait_for_launch_before();
   if (c < H) {
 #pragma unroll 8
     for (int i = warp; i < n; i += kDwWarps) acc += partial[static_cast<long long>(i) * H + c];
@@ -900,8 +901,8 @@ cudaError_t launch_rmsnorm_bwd(const RmsNormBwdArgs& a, int is_bf16, int num_sms
 }
 
 cudaError_t launch_rmsnorm_dw(const float* partial, int n, int H, float* dw, cudaStream_t s) {
-  rmsnorm_dw_kernel<<<(H + 31) / 32, 32 * kDwWarps, 0, s>>>(partial, n, H, dw);
-  return cudaGetLastError();
+  return launch_overlapped(rmsnorm_dw_kernel, dim3((H + 31) / 32), dim3(32 * kDwWarps), 0, s, partial,
+                           n, H, dw);
 }
 
 }  // namespace eas
