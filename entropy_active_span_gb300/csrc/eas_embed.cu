@@ -56,7 +56,7 @@ embed_fwd_kernel(const EmbedFwdArgs p) {
     src[r] = id >= 0 && id < p.V ? static_cast<const T*>(p.table) + static_cast<long long>(id) * p.H : nullptr;
   }
   T* dst = static_cast<T*>(p.out) + t0 * p.H;
-#pragma unroll 2
+#pragma unroll 4
   for (int c = threadIdx.x * VEC; c < p.H; c += blockDim.x * VEC) {
     Raw<T, VEC> raw[kRows];
 #pragma unroll
@@ -71,7 +71,9 @@ embed_fwd_kernel(const EmbedFwdArgs p) {
 #pragma unroll
         for (int i = 0; i < VEC; ++i) f[i] *= p.scale;
       }
-      store_vec<T, VEC>(dst + static_cast<long long>(r) * p.H + c, f);
+      // the table's rows come again, the output does not: 128 us against 136 at
+      // [65536, 5120] bf16 with Zipf-distributed ids
+      store_vec<T, VEC, true>(dst + static_cast<long long>(r) * p.H + c, f);
     }
   }
 }

@@ -60,23 +60,28 @@ __device__ __forceinline__ void widen(const Raw<T, VEC>& r, float (&f)[VEC]) {
   }
 }
 
-// Rounds to T (nearest-even) and stores VEC consecutive elements.
-template <typename T, int VEC>
+// Rounds to T (nearest-even) and stores VEC consecutive elements.  kStream: they
+// are the first to leave L2.
+template <typename T, int VEC, bool kStream = false>
 __device__ __forceinline__ void store_vec(T* p, const float (&f)[VEC]) {
   if constexpr (VEC == 1) {
     if constexpr (sizeof(T) == 4)
       *p = f[0];
     else
       *p = __float2bfloat16_rn(f[0]);
-  } else if constexpr (sizeof(T) == 4) {
-    *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
   } else {
     uint4 u;
-    u.x = pack_bf16x2(f[0], f[1]);
-    u.y = pack_bf16x2(f[2], f[3]);
-    u.z = pack_bf16x2(f[4], f[5]);
-    u.w = pack_bf16x2(f[6], f[7]);
-    *reinterpret_cast<uint4*>(p) = u;
+    if constexpr (sizeof(T) == 4) {
+      u = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
+                     __float_as_uint(f[3]));
+    } else {
+      u = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                     pack_bf16x2(f[6], f[7]));
+    }
+    if constexpr (kStream)
+      __stcs(reinterpret_cast<uint4*>(p), u);
+    else
+      *reinterpret_cast<uint4*>(p) = u;
   }
 }
 
