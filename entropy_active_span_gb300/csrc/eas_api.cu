@@ -1127,14 +1127,12 @@ eas_status eas_embed_bwd(const int32_t* ids, const void* dout, int64_t T, int64_
   const EmbedBwdArgs a = {ids, dout, dweight, T, static_cast<int>(V), static_cast<int>(H), scale,
                           accumulate, at<char>(ws, align_up(sizeof(DevStatus))),
                           static_cast<DevStatus*>(ws)};
-  {
+  if (embed_bwd_sorts(T)) {
     Trace tr_(kTrEmbedSort, s);
     EAS_CUDA(launch_embed_sort(a, s), "embed_sort");
   }
-  if (T > 0 || !accumulate) {
-    Trace tr_(kTrEmbedBwd, s);
-    EAS_CUDA(launch_embed_bwd(a, dtype == EAS_BF16, s), "embed_bwd");
-  }
+  Trace tr_(kTrEmbedBwd, s);
+  EAS_CUDA(launch_embed_bwd(a, dtype == EAS_BF16, s), "embed_bwd");
   return EAS_OK;
 }
 

@@ -385,6 +385,17 @@ constexpr int kSumThreads = 128;
 constexpr int kSumUnroll = 8;
 constexpr int kMaxChunk = 128;
 
+// Zeros in the n floats at p by the CTA's kSumThreads threads; p need not start on
+// a 16-byte boundary (rows of odd width).
+__device__ __forceinline__ void zero_floats(float* p, int n, int tid) {
+  int head = static_cast<int>(-(reinterpret_cast<uintptr_t>(p) >> 2) & 3);
+  if (head > n) head = n;
+  const int mid = (n - head) & ~3;
+  for (int c = tid * 4; c < mid; c += kSumThreads * 4)
+    *reinterpret_cast<float4*>(p + head + c) = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (tid < n - mid) p[tid < head ? tid : mid + tid] = 0.f;
+}
+
 // Zeros in rows [v0, v0 + p.zero_rows) of dw, but for those that a token names:
 // each row's id is looked up in the sorted list.
 __device__ __forceinline__ void zero_rows(const SumArgs& p, int block, int* skip) {
@@ -400,16 +411,8 @@ __device__ __forceinline__ void zero_rows(const SumArgs& p, int block, int* skip
     skip[tid] = v >= p.V || (lo < p.T && p.keys[lo] == v);
   }
   __syncthreads();
-  for (int r = 0; r < p.zero_rows; ++r) {
-    if (skip[r]) continue;
-    float* row = p.dw + (v0 + r) * p.H;
-    if (p.H % 4 == 0) {
-      for (int c = tid * 4; c < p.H; c += kSumThreads * 4)
-        *reinterpret_cast<float4*>(row + c) = make_float4(0.f, 0.f, 0.f, 0.f);
-    } else {
-      for (int c = tid; c < p.H; c += kSumThreads) row[c] = 0.f;
-    }
-  }
+  for (int r = 0; r < p.zero_rows; ++r)
+    if (!skip[r]) zero_floats(p.dw + (v0 + r) * p.H, p.H, tid);
 }
 
 // CTA b < p.sum_ctas: blockDim.y chunks of the sorted tokens (one where the
@@ -502,6 +505,93 @@ __global__ void __launch_bounds__(kSumThreads) embed_join_kernel(const SumArgs p
   put_row<1>(p.dw + static_cast<long long>(key) * p.H + c, a, p.scale, p.accumulate);
 }
 
+// ------------------------------------------------------------- short lists
+
+// Up to kFewTokens tokens: one launch, no sorted list.  A CTA is a token and
+// kSumThreads * VEC columns; it ends at once if an earlier token has its id, and
+// else lists the tokens that have it, in their order, and sums them.  The CTAs
+// after them fill the other rows.  CTA 0 also checks the ids and writes the
+// status word.  An id that all of 512 tokens name is one CTA's work (about 50
+// us); that is why the lists end there.
+constexpr int kFewTokens = 512;
+
+template <typename T, int VEC>
+__global__ void __launch_bounds__(kSumThreads)
+embed_few_kernel(const SumArgs p, const int* __restrict__ ids, DevStatus* st) {
+  __shared__ int list[kFewTokens];
+  __shared__ int warp_n[kSumThreads / 32];
+  __shared__ int first_bad;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int n = static_cast<int>(p.T);
+  if (blockIdx.x == 0) {
+    if (tid == 0) first_bad = n;
+    __syncthreads();
+    for (int j = tid; j < n; j += kSumThreads)
+      if (ids[j] < -1 || ids[j] >= p.V) atomicMin(&first_bad, j);
+    __syncthreads();
+    if (tid == 0) {
+      const bool bad = first_bad < n;
+      st->code = bad ? kStInvalidArg : kStOk;
+      st->where = bad ? kWhereEmbed : 0;
+      st->info = bad ? first_bad : 0;
+    }
+  }
+  if (blockIdx.x >= p.sum_ctas) {
+    if (p.accumulate) return;           // an empty list: only the status
+    const long long v0 = static_cast<long long>(blockIdx.x - p.sum_ctas) * p.zero_rows;
+    if (tid < p.zero_rows) list[tid] = v0 + tid >= p.V;
+    __syncthreads();
+    for (int j = tid; j < n; j += kSumThreads) {
+      const long long r = ids[j] - v0;
+      if (r >= 0 && r < p.zero_rows) list[r] = 1;
+    }
+    __syncthreads();
+    for (int r = 0; r < p.zero_rows; ++r)
+      if (!list[r]) zero_floats(p.dw + (v0 + r) * p.H, p.H, tid);
+    return;
+  }
+  const int slabs = (p.H + kSumThreads * VEC - 1) / (kSumThreads * VEC);
+  const int t = blockIdx.x / slabs, slab = blockIdx.x - t * slabs;
+  const int id = ids[t];
+  if (id < 0 || id >= p.V) return;
+  int count = 0;
+  for (int j0 = 0; j0 < n; j0 += kSumThreads) {
+    const int j = j0 + tid;
+    const bool same = j < n && ids[j] == id;
+    const unsigned m = __ballot_sync(0xffffffffu, same);
+    if (lane == 0) warp_n[warp] = __popc(m);
+    if (__syncthreads_or(same && j < t)) return;
+    int at = count + __popc(m & ((1u << lane) - 1));
+#pragma unroll
+    for (int w = 0; w < kSumThreads / 32; ++w) {
+      if (w < warp) at += warp_n[w];
+      count += warp_n[w];
+    }
+    if (same) list[at] = j;
+    __syncthreads();
+  }
+  const int c = (slab * kSumThreads + tid) * VEC;
+  if (c >= p.H) return;
+  const T* dout = static_cast<const T*>(p.dout) + c;
+  float acc[VEC] = {};
+  for (int i = 0; i < count; i += kSumUnroll) {
+    Raw<T, VEC> raw[kSumUnroll];
+#pragma unroll
+    for (int u = 0; u < kSumUnroll; ++u)
+      if (i + u < count) raw[u] = load_raw<T, VEC>(dout + static_cast<long long>(list[i + u]) * p.H);
+#pragma unroll
+    for (int u = 0; u < kSumUnroll; ++u) {
+      if (i + u < count) {
+        float f[VEC];
+        widen<T, VEC>(raw[u], f);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) acc[e] += f[e];
+      }
+    }
+  }
+  put_row<VEC>(p.dw + static_cast<long long>(id) * p.H + c, acc, p.scale, p.accumulate);
+}
+
 size_t up(size_t x) { return (x + 255) / 256 * 256; }
 
 long long sort_tile(long long T) {
@@ -583,6 +673,18 @@ EmbedBwdPlan embed_bwd_plan(long long T, long long H, long long V) {
   return p;
 }
 
+template <typename T, int VEC>
+static cudaError_t few_t(SumArgs s, const EmbedBwdArgs& a, cudaStream_t st) {
+  const long long slabs = (s.H + kSumThreads * VEC - 1) / (kSumThreads * VEC);
+  const long long zeros = s.accumulate ? 0 : (static_cast<long long>(s.V) + s.zero_rows - 1) / s.zero_rows;
+  s.sum_ctas = static_cast<int>(s.T * slabs);
+  const long long grid = s.sum_ctas + zeros;
+  embed_few_kernel<T, VEC><<<static_cast<unsigned>(grid > 0 ? grid : 1), kSumThreads, 0, st>>>(s, a.ids, a.status);
+  return cudaGetLastError();
+}
+
+bool embed_bwd_sorts(long long T) { return T > kFewTokens; }
+
 template <int kRounds>
 static cudaError_t cluster_sort(const ClusterSort& p, cudaStream_t s) {
   const int smem = kClusterThreads * kRounds * static_cast<int>(sizeof(int2)) +
@@ -654,6 +756,11 @@ static cudaError_t sum_t(SumArgs s, int n_chunks, cudaStream_t st) {
 cudaError_t launch_embed_bwd(const EmbedBwdArgs& a, int is_bf16, cudaStream_t st) {
   const EmbedBwdPlan pl = embed_bwd_plan(a.T, a.H, a.V);
   const SumArgs s = sum_args(a, pl, (sort_passes(a.V) - 1) & 1);
+  if (!embed_bwd_sorts(a.T)) {
+    if (a.H % (is_bf16 ? 8 : 4) == 0)
+      return is_bf16 ? few_t<__nv_bfloat16, 8>(s, a, st) : few_t<float, 4>(s, a, st);
+    return is_bf16 ? few_t<__nv_bfloat16, 1>(s, a, st) : few_t<float, 1>(s, a, st);
+  }
   const int n_chunks = static_cast<int>((a.T + pl.chunk - 1) / pl.chunk);
   const int vec16 = is_bf16 ? 8 : 4;
   cudaError_t e;

@@ -247,7 +247,9 @@ struct EmbedBwdArgs {
   char* scratch;
   DevStatus* status;
 };
-// The sort clears the status word.
+// Whether a list is long enough to be sorted; the sort clears the status word,
+// and without one launch_embed_bwd does.
+bool embed_bwd_sorts(long long T);
 cudaError_t launch_embed_sort(const EmbedBwdArgs& a, cudaStream_t s);
 cudaError_t launch_embed_bwd(const EmbedBwdArgs& a, int is_bf16, cudaStream_t s);
 

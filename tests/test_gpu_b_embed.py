@@ -54,7 +54,7 @@ def check_bwd(ids, dout, V, scale, dw, base=None):
     assert (np.abs(f64(dw) - ref) <= tol * (1 + 1e-6)).all()
 
 
-SHAPES = [(1, 64, 1), (1, 1003, 10), (5, 7, 3), (16, 4096, 1500), (300, 320, 600), (2049, 256, 511),
+SHAPES = [(1, 64, 1), (1, 1003, 10), (5, 7, 3), (16, 4096, 1500), (300, 320, 600), (512, 1003, 77), (513, 136, 77), (2049, 256, 511),
           (2048, 64, 512), (4100, 1088, 513), (9000, 136, 270000)]
 
 
