@@ -1132,7 +1132,7 @@ eas_status eas_embed_bwd(const int32_t* ids, const void* dout, int64_t T, int64_
     EAS_CUDA(launch_embed_sort(a, s), "embed_sort");
   }
   Trace tr_(kTrEmbedBwd, s);
-  EAS_CUDA(launch_embed_bwd(a, dtype == EAS_BF16, s), "embed_bwd");
+  EAS_CUDA(launch_embed_bwd(a, dtype == EAS_BF16, di.sms, s), "embed_bwd");
   return EAS_OK;
 }
 

@@ -21,6 +21,11 @@ constexpr int kWhereEmbed = 20;
 
 // ------------------------------------------------------------------ lookup
 
+// Vectors of a row that a thread holds at a time: single elements (rows of odd
+// width) go four together, so that as many loads are on their way.
+template <int VEC>
+constexpr int kCols = VEC == 1 ? 4 : 1;
+
 // CTA 0 also checks every id and writes the status word: no other launch clears
 // it.
 template <typename T, int VEC, int kRows>
@@ -56,24 +61,30 @@ embed_fwd_kernel(const EmbedFwdArgs p) {
     src[r] = id >= 0 && id < p.V ? static_cast<const T*>(p.table) + static_cast<long long>(id) * p.H : nullptr;
   }
   T* dst = static_cast<T*>(p.out) + t0 * p.H;
-#pragma unroll 4
-  for (int c = threadIdx.x * VEC; c < p.H; c += blockDim.x * VEC) {
-    Raw<T, VEC> raw[kRows];
+  const int step = blockDim.x * VEC;
+  for (int c0 = threadIdx.x * VEC; c0 < p.H; c0 += kCols<VEC> * step) {
+    Raw<T, VEC> raw[kCols<VEC>][kRows];
 #pragma unroll
-    for (int r = 0; r < kRows; ++r)
-      if (src[r]) raw[r] = load_raw<T, VEC>(src[r] + c);
+    for (int m = 0; m < kCols<VEC>; ++m)
 #pragma unroll
-    for (int r = 0; r < kRows; ++r) {
-      if (t0 + r >= p.T) break;
-      float f[VEC] = {};
-      if (src[r]) {
-        widen<T, VEC>(raw[r], f);
+      for (int r = 0; r < kRows; ++r)
+        if (src[r] && c0 + m * step < p.H) raw[m][r] = load_const<T, VEC>(src[r] + c0 + m * step);
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) f[i] *= p.scale;
+    for (int m = 0; m < kCols<VEC>; ++m) {
+      const int c = c0 + m * step;
+#pragma unroll
+      for (int r = 0; r < kRows; ++r) {
+        if (t0 + r >= p.T || c >= p.H) break;
+        float f[VEC] = {};
+        if (src[r]) {
+          widen<T, VEC>(raw[m][r], f);
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) f[i] *= p.scale;
+        }
+        // the table's rows come again, the output does not: 128 us against 136 at
+        // [65536, 5120] bf16 with Zipf-distributed ids
+        store_vec<T, VEC, true>(dst + static_cast<long long>(r) * p.H + c, f);
       }
-      // the table's rows come again, the output does not: 128 us against 136 at
-      // [65536, 5120] bf16 with Zipf-distributed ids
-      store_vec<T, VEC, true>(dst + static_cast<long long>(r) * p.H + c, f);
     }
   }
 }
@@ -90,6 +101,11 @@ constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kSortRounds = 4;
 constexpr int kSortSub = kSortThreads * kSortRounds;
 constexpr int kSortTiles = 128;
+
+// The number of runs that cross chunks stands behind the status word; the sort
+// clears both.
+constexpr size_t kClearBytes = sizeof(DevStatus) + sizeof(int);
+__host__ __device__ __forceinline__ int* run_count(DevStatus* st) { return reinterpret_cast<int*>(st + 1); }
 
 struct SortPass {
   const int* ids;         // first pass: the token ids; later: null
@@ -140,6 +156,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_scatter_kernel(const SortPa
 
   // where this tile's tokens of digit `tid` start
   int before = 0, total = 0;
+#pragma unroll 32
   for (int t = 0; t < p.n_tiles; ++t) {
     const int n = p.hist[t * kSortBins + tid];
     if (t < blockIdx.x) before += n;
@@ -255,6 +272,7 @@ cluster_sort_kernel(const ClusterSort p) {
   if (rank == 0 && tid == 0) {
     p.status->code = kStOk;
     p.status->where = p.status->info = 0;
+    *run_count(p.status) = 0;
   }
   cluster_sync();                       // the status is clear, and every CTA runs
   int key[kRounds], pos[kRounds];
@@ -363,6 +381,9 @@ struct SumArgs {
   int accumulate;
   int sum_ctas;
   int zero_rows;          // rows of dw a zeroing CTA looks after
+  int* n_runs;            // runs that cross chunks: how many,
+  int* runs;              // and the chunk in which each starts
+  int n_chunks;
 };
 
 template <int VEC>
@@ -370,7 +391,7 @@ __device__ __forceinline__ void put_row(float* dst, const float (&acc)[VEC], flo
   float o[VEC];
 #pragma unroll
   for (int i = 0; i < VEC; ++i) o[i] = acc[i] * scale;
-  constexpr int W = VEC == 1 ? 1 : 4;
+  constexpr int W = VEC < 4 ? 1 : 4;
 #pragma unroll
   for (int h = 0; h < VEC; h += W) {
     float v[W];
@@ -382,23 +403,32 @@ __device__ __forceinline__ void put_row(float* dst, const float (&acc)[VEC], flo
 }
 
 constexpr int kSumThreads = 128;
-constexpr int kSumUnroll = 8;
+template <int VEC>
+constexpr int kSumUnroll = VEC == 1 ? 4 : 8;   // tokens on their way
 constexpr int kMaxChunk = 128;
 
-// Zeros in the n floats at p by the CTA's kSumThreads threads; p need not start on
-// a 16-byte boundary (rows of odd width).
-__device__ __forceinline__ void zero_floats(float* p, int n, int tid) {
+// Zeros in the n floats at p by a warp; p need not start on a 16-byte boundary
+// (rows of odd width).
+__device__ __forceinline__ void zero_floats(float* p, int n, int lane) {
   int head = static_cast<int>(-(reinterpret_cast<uintptr_t>(p) >> 2) & 3);
   if (head > n) head = n;
   const int mid = (n - head) & ~3;
-  for (int c = tid * 4; c < mid; c += kSumThreads * 4)
+#pragma unroll 4
+  for (int c = lane * 4; c < mid; c += 128)
     *reinterpret_cast<float4*>(p + head + c) = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (tid < n - mid) p[tid < head ? tid : mid + tid] = 0.f;
+  if (lane < n - mid) p[lane < head ? lane : mid + lane] = 0.f;
 }
 
-// Zeros in rows [v0, v0 + p.zero_rows) of dw, but for those that a token names:
-// each row's id is looked up in the sorted list.
-__device__ __forceinline__ void zero_rows(const SumArgs& p, int block, int* skip) {
+// Zeros in those of the CTA's rows of dw (from v0) whose skip[] is 0, a warp a row.
+__device__ __forceinline__ void zero_rows(const SumArgs& p, long long v0, const int* skip, int tid) {
+#pragma unroll 2
+  for (int r = tid >> 5; r < p.zero_rows; r += kSumThreads / 32)
+    if (!skip[r]) zero_floats(p.dw + (v0 + r) * p.H, p.H, tid & 31);
+}
+
+// The rows that no token names, for one CTA: each row's id is looked up in the
+// sorted list.
+__device__ __forceinline__ void zero_unnamed(const SumArgs& p, int block, int* skip) {
   const long long v0 = static_cast<long long>(block) * p.zero_rows;
   const int tid = threadIdx.y * blockDim.x + threadIdx.x;
   if (tid < p.zero_rows) {
@@ -411,8 +441,17 @@ __device__ __forceinline__ void zero_rows(const SumArgs& p, int block, int* skip
     skip[tid] = v >= p.V || (lo < p.T && p.keys[lo] == v);
   }
   __syncthreads();
-  for (int r = 0; r < p.zero_rows; ++r)
-    if (!skip[r]) zero_floats(p.dw + (v0 + r) * p.H, p.H, tid);
+  zero_rows(p, v0, skip, tid);
+}
+
+// The first index from `from` on whose key is not `key`, at most `limit`; a warp.
+__device__ __forceinline__ int run_end(const int* keys, int from, int limit, int key) {
+  const int lane = threadIdx.x & 31;
+  for (int i = from; i < limit; i += 32) {
+    const unsigned m = __ballot_sync(0xffffffffu, i + lane < limit && keys[i + lane] == key);
+    if (m != 0xffffffffu) return i + __popc(m);
+  }
+  return limit;
 }
 
 // CTA b < p.sum_ctas: blockDim.y chunks of the sorted tokens (one where the
@@ -420,108 +459,159 @@ __device__ __forceinline__ void zero_rows(const SumArgs& p, int block, int* skip
 // their stores run beside the others' loads.
 template <typename T, int VEC>
 __global__ void __launch_bounds__(kSumThreads) embed_sum_kernel(const SumArgs p) {
-  __shared__ int key_store[4][kMaxChunk + 2];
-  __shared__ int pos_store[4][kMaxChunk];
+  __shared__ int key_store[4][2 * kMaxChunk + 2];
+  __shared__ int pos_store[4][2 * kMaxChunk];
   wait_for_launch_before();
   if (blockIdx.x >= p.sum_ctas) {
-    zero_rows(p, blockIdx.x - p.sum_ctas, key_store[0]);
+    zero_unnamed(p, blockIdx.x - p.sum_ctas, key_store[0]);
     return;
   }
-  int* keys = key_store[threadIdx.y];   // [0]: the key before the chunk, [n + 1]: the one after
+  int* keys = key_store[threadIdx.y];   // [0]: the key before the chunk; then two chunks and one more
   int* pos = pos_store[threadIdx.y];
-  const int slabs = (p.H + blockDim.x * VEC - 1) / (blockDim.x * VEC);
+  const int step = blockDim.x * VEC, width = kCols<VEC> * step;
+  const int slabs = (p.H + width - 1) / width;
   const int group = blockIdx.x / slabs, slab = blockIdx.x - group * slabs;
   const int chunk = group * blockDim.y + threadIdx.y;
   const long long i0 = static_cast<long long>(chunk) * p.chunk;
   const long long left = p.T - i0;
   const int n = static_cast<int>(left < 0 ? 0 : left < p.chunk ? left : p.chunk);
-  for (int i = threadIdx.x; i < n + 2; i += blockDim.x) {
+  const int seen = static_cast<int>(left < 0 ? 0 : left < 2 * p.chunk ? left : 2 * p.chunk);
+  for (int i = threadIdx.x; i < 2 * p.chunk + 2; i += blockDim.x) {
     const long long k = i0 + i - 1;
     keys[i] = k >= 0 && k < p.T ? p.keys[k] : -1;
-    if (i < n) pos[i] = p.pos[i0 + i];
+    if (i < seen) pos[i] = p.pos[i0 + i];
   }
+  // A run of at most two chunks is the work of the chunk in which it starts: it
+  // goes on into the next one (to `stop`), which leaves those tokens out (to
+  // `begin`).
+  const bool came = n > 0 && i0 > 0 && p.keys[i0 - 1] == p.keys[i0];
+  const bool came_far = came && i0 > p.chunk && p.keys[i0 - p.chunk - 1] == p.keys[i0];
   __syncthreads();
-  const int c = (slab * blockDim.x + threadIdx.x) * VEC;
+  int begin = 0, stop = n;
+  const bool through = came && keys[n + 1] == keys[1];       // and goes on past the chunk
+  if (came && !came_far && !through) begin = run_end(keys + 1, 0, n, keys[1]);
+  if (n == p.chunk && keys[n + 1] == keys[n] && !through && keys[2 * p.chunk + 1] != keys[n])
+    stop = run_end(keys + 1, n, seen, keys[n]);
+  const int c = slab * width + threadIdx.x * VEC;
   if (c >= p.H) return;
   const T* dout = static_cast<const T*>(p.dout) + c;
-  float acc[VEC] = {};
-  int start = 0;                        // where the current run starts in the chunk
-  for (int i = 0; i < n; i += kSumUnroll) {
+  constexpr int U = kSumUnroll<VEC>, M = kCols<VEC>;
+  float acc[M][VEC] = {};
+  bool piece = came && begin == 0;      // the current run started in an earlier chunk
+  for (int i = begin; i < stop; i += U) {
     if (keys[i + 1] == p.V) break;      // the padding, after every token
-    Raw<T, VEC> raw[kSumUnroll];
+    Raw<T, VEC> raw[U][M];
 #pragma unroll
-    for (int u = 0; u < kSumUnroll; ++u)
-      if (i + u < n && keys[i + u + 1] != p.V)
-        raw[u] = load_raw<T, VEC>(dout + static_cast<long long>(pos[i + u]) * p.H);
+    for (int u = 0; u < U; ++u)
 #pragma unroll
-    for (int u = 0; u < kSumUnroll; ++u) {
+      for (int m = 0; m < M; ++m)
+        if (i + u < stop && keys[i + u + 1] != p.V && c + m * step < p.H)
+          raw[u][m] = load_const<T, VEC>(dout + static_cast<long long>(pos[i + u]) * p.H + m * step);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
       const int k = i + u;
-      if (k < n && keys[k + 1] != p.V) {
-        float f[VEC];
-        widen<T, VEC>(raw[u], f);
+      if (k < stop && keys[k + 1] != p.V) {
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) acc[e] += f[e];
+        for (int m = 0; m < M; ++m) {
+          float f[VEC];
+          widen<T, VEC>(raw[u][m], f);
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) acc[m][e] += f[e];
+        }
         const int key = keys[k + 1];
-        if (k + 1 == n || keys[k + 2] != key) {   // the run ends here, or the chunk does
-          const bool from_before = start == 0 && keys[0] == key;
-          const bool goes_on = keys[k + 2] == key;
-          if (!from_before && !goes_on) {
-            put_row<VEC>(p.dw + static_cast<long long>(key) * p.H + c, acc, p.scale, p.accumulate);
-          } else {
-            float* q = p.partial + (2ll * chunk + (from_before ? 0 : 1)) * p.H + c;
-            put_row<VEC>(q, acc, 1.f, 0);
-          }
-          start = k + 1;
+        const bool goes_on = keys[k + 2] == key;
+        if (!goes_on || k + 1 == stop) {          // the run ends here, or the chunk does
+          const bool done = !piece && !goes_on;
+          if (goes_on && !piece && threadIdx.x == 0 && slab == 0)
+            p.runs[atomicAdd(p.n_runs, 1)] = chunk;
+          float* to = done ? p.dw + static_cast<long long>(key) * p.H + c
+                           : p.partial + (2ll * chunk + (piece ? 0 : 1)) * p.H + c;
 #pragma unroll
-          for (int e = 0; e < VEC; ++e) acc[e] = 0.f;
+          for (int m = 0; m < M; ++m) {
+            if (c + m * step < p.H) put_row<VEC>(to + m * step, acc[m], done ? p.scale : 1.f, done && p.accumulate);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) acc[m][e] = 0.f;
+          }
+          piece = false;
         }
       }
     }
   }
 }
 
-// Adds up the runs that cross chunks: the CTAs of the chunk in which a run
-// starts walk the chunks it covers.
-__global__ void __launch_bounds__(kSumThreads) embed_join_kernel(const SumArgs p, int n_chunks) {
+// Adds up the runs of three chunks or more.  The sums have listed them (in any order:
+// each is added up by itself, in the order of its chunks).  A CTA takes a run
+// and 32 W columns; its kJoinParts warps each add a stretch of the run's pieces,
+// and the first warp the stretches.
+constexpr int kJoinParts = 8;
+template <int W>
+__global__ void __launch_bounds__(32 * kJoinParts) embed_join_kernel(const SumArgs p) {
+  __shared__ float sums[kJoinParts][32 * W];
   wait_for_launch_before();
-  const long long end = static_cast<long long>(blockIdx.x + 1) * p.chunk;
-  if (end >= p.T) return;
-  const int key = p.keys[end - 1];
-  if (key == p.V || p.keys[end] != key) return;                      // no run goes on
-  const long long begin = end - p.chunk;
-  if (p.keys[begin] == key && begin > 0 && p.keys[begin - 1] == key) return;   // nor starts here
-  // the last chunk of the run: the last that begins with its id
-  int last = blockIdx.x + 1, hi = n_chunks;
-  while (hi - last > 1) {
-    const int mid = last + (hi - last) / 2;
-    if (p.keys[static_cast<long long>(mid) * p.chunk] == key) last = mid; else hi = mid;
-  }
-  const int c = blockIdx.y * kSumThreads + threadIdx.x;
-  if (c >= p.H) return;
-  float acc = p.partial[(2ll * blockIdx.x + 1) * p.H + c];
+  const int lane = threadIdx.x & 31, part = threadIdx.x >> 5;
+  const int slabs = (p.H + 32 * W - 1) / (32 * W);
+  const long long items = static_cast<long long>(*p.n_runs) * slabs;
+  for (long long item = blockIdx.x; item < items; item += gridDim.x) {
+    const int run = static_cast<int>(item / slabs);
+    const int c = (static_cast<int>(item - static_cast<long long>(run) * slabs) * 32 + lane) * W;
+    const int first = p.runs[run];
+    const int key = p.keys[(static_cast<long long>(first) + 1) * p.chunk - 1];
+    // the run's last chunk: the last that begins with its id
+    int last = first + 1, end = p.n_chunks;
+    while (end - last > 1) {
+      const int step = (end - last + 31) / 32;
+      const long long probe = last + (lane + 1ll) * step;
+      const bool in = probe < end && p.keys[probe * p.chunk] == key;
+      last += __popc(__ballot_sync(0xffffffffu, in)) * step;
+      end = end < last + step ? end : last + step;
+    }
+    const int pieces = last - first + 1;
+    const int per = (pieces + kJoinParts - 1) / kJoinParts;
+    const int to = (part + 1) * per < pieces ? (part + 1) * per : pieces;
+    float acc[W] = {};
+    if (c < p.H) {
 #pragma unroll 8
-  for (int k = blockIdx.x + 1; k <= last; ++k) acc += p.partial[2ll * k * p.H + c];
-  const float a[1] = {acc};
-  put_row<1>(p.dw + static_cast<long long>(key) * p.H + c, a, p.scale, p.accumulate);
+      for (int q = part * per; q < to; ++q) {
+        const float* from = p.partial + (q == 0 ? 2ll * first + 1 : 2ll * (first + q)) * p.H + c;
+        float f[W];
+        widen<float, W>(load_const<float, W>(from), f);
+#pragma unroll
+        for (int i = 0; i < W; ++i) acc[i] += f[i];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < W; ++i) sums[part][lane * W + i] = acc[i];
+    __syncthreads();
+    if (part == 0 && c < p.H) {
+      for (int q = 1; q < kJoinParts; ++q)
+#pragma unroll
+        for (int i = 0; i < W; ++i) acc[i] += sums[q][lane * W + i];
+      put_row<W>(p.dw + static_cast<long long>(key) * p.H + c, acc, p.scale, p.accumulate);
+    }
+    __syncthreads();
+  }
 }
 
 // ------------------------------------------------------------- short lists
 
-// Up to kFewTokens tokens: one launch, no sorted list.  A CTA is a token and
-// kSumThreads * VEC columns; it ends at once if an earlier token has its id, and
-// else lists the tokens that have it, in their order, and sums them.  The CTAs
+// Up to kFewTokens tokens: one launch, no sorted list.  A CTA is a token and a
+// stretch of columns; it ends at once if an earlier token has its id, and else
+// lists the tokens that have it, in their order, and sums them (blockDim.y
+// stretches of the list where the columns leave threads for that).  The CTAs
 // after them fill the other rows.  CTA 0 also checks the ids and writes the
-// status word.  An id that all of 512 tokens name is one CTA's work (about 50
-// us); that is why the lists end there.
+// status word.  An id that all tokens name is one CTA's work; that is why the
+// lists end at 512.
 constexpr int kFewTokens = 512;
 
 template <typename T, int VEC>
 __global__ void __launch_bounds__(kSumThreads)
 embed_few_kernel(const SumArgs p, const int* __restrict__ ids, DevStatus* st) {
+  constexpr int U = 2 * kSumUnroll<VEC>, M = kCols<VEC>;
   __shared__ int list[kFewTokens];
   __shared__ int warp_n[kSumThreads / 32];
   __shared__ int first_bad;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  __shared__ float sums[kSumThreads * VEC * M];
+  const int tid = threadIdx.y * blockDim.x + threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int n = static_cast<int>(p.T);
   if (blockIdx.x == 0) {
     if (tid == 0) first_bad = n;
@@ -546,11 +636,11 @@ embed_few_kernel(const SumArgs p, const int* __restrict__ ids, DevStatus* st) {
       if (r >= 0 && r < p.zero_rows) list[r] = 1;
     }
     __syncthreads();
-    for (int r = 0; r < p.zero_rows; ++r)
-      if (!list[r]) zero_floats(p.dw + (v0 + r) * p.H, p.H, tid);
+    zero_rows(p, v0, list, tid);
     return;
   }
-  const int slabs = (p.H + kSumThreads * VEC - 1) / (kSumThreads * VEC);
+  const int step = blockDim.x * VEC, width = M * step;
+  const int slabs = (p.H + width - 1) / width;
   const int t = blockIdx.x / slabs, slab = blockIdx.x - t * slabs;
   const int id = ids[t];
   if (id < 0 || id >= p.V) return;
@@ -570,26 +660,49 @@ embed_few_kernel(const SumArgs p, const int* __restrict__ ids, DevStatus* st) {
     if (same) list[at] = j;
     __syncthreads();
   }
-  const int c = (slab * kSumThreads + tid) * VEC;
-  if (c >= p.H) return;
-  const T* dout = static_cast<const T*>(p.dout) + c;
-  float acc[VEC] = {};
-  for (int i = 0; i < count; i += kSumUnroll) {
-    Raw<T, VEC> raw[kSumUnroll];
+  const int c = slab * width + threadIdx.x * VEC;
+  const int per = (count + blockDim.y - 1) / blockDim.y;
+  const int to = static_cast<int>(threadIdx.y + 1) * per < count ? (threadIdx.y + 1) * per : count;
+  float acc[M][VEC] = {};
+  if (c < p.H) {
+    const T* dout = static_cast<const T*>(p.dout) + c;
+    for (int i = threadIdx.y * per; i < to; i += U) {
+      Raw<T, VEC> raw[U][M];
 #pragma unroll
-    for (int u = 0; u < kSumUnroll; ++u)
-      if (i + u < count) raw[u] = load_raw<T, VEC>(dout + static_cast<long long>(list[i + u]) * p.H);
+      for (int u = 0; u < U; ++u)
 #pragma unroll
-    for (int u = 0; u < kSumUnroll; ++u) {
-      if (i + u < count) {
-        float f[VEC];
-        widen<T, VEC>(raw[u], f);
+        for (int m = 0; m < M; ++m)
+          if (i + u < to && c + m * step < p.H)
+            raw[u][m] = load_const<T, VEC>(dout + static_cast<long long>(list[i + u]) * p.H + m * step);
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) acc[e] += f[e];
-      }
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int m = 0; m < M; ++m)
+          if (i + u < to && c + m * step < p.H) {
+            float f[VEC];
+            widen<T, VEC>(raw[u][m], f);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) acc[m][e] += f[e];
+          }
     }
   }
-  put_row<VEC>(p.dw + static_cast<long long>(id) * p.H + c, acc, p.scale, p.accumulate);
+  if (blockDim.y > 1) {
+#pragma unroll
+    for (int m = 0; m < M; ++m)
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) sums[(m * VEC + e) * kSumThreads + tid] = acc[m][e];
+    __syncthreads();
+    if (threadIdx.y > 0) return;
+    for (int y = 1; y < static_cast<int>(blockDim.y); ++y)
+#pragma unroll
+      for (int m = 0; m < M; ++m)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) acc[m][e] += sums[(m * VEC + e) * kSumThreads + y * blockDim.x + tid];
+  }
+#pragma unroll
+  for (int m = 0; m < M; ++m)
+    if (c + m * step < p.H)
+      put_row<VEC>(p.dw + static_cast<long long>(id) * p.H + c + m * step, acc[m], p.scale, p.accumulate);
 }
 
 size_t up(size_t x) { return (x + 255) / 256 * 256; }
@@ -613,7 +726,12 @@ SumArgs sum_args(const EmbedBwdArgs& a, const EmbedBwdPlan& pl, int buf) {
   s.scale = a.scale;
   s.accumulate = a.accumulate;
   s.sum_ctas = 0;
-  const long long rows = 32768 / (a.H > 0 ? a.H : 1);   // 128 KB of dw
+  s.n_runs = run_count(a.status);
+  s.runs = reinterpret_cast<int*>(a.scratch + pl.runs);
+  s.n_chunks = static_cast<int>((a.T + pl.chunk - 1) / pl.chunk);
+  // 128 KB of dw a CTA, less where that would leave the machine idle
+  long long rows = 32768 / a.H;
+  if (rows > a.V / 1024) rows = a.V / 1024;
   s.zero_rows = static_cast<int>(rows < 4 ? 4 : rows > kSumThreads ? kSumThreads : rows);
   return s;
 }
@@ -669,17 +787,35 @@ EmbedBwdPlan embed_bwd_plan(long long T, long long H, long long V) {
   p.partial = o;
   const size_t chunks = (n + p.chunk - 1) / p.chunk;
   if (chunks > 1) o = up(o + chunks * 2 * 4 * static_cast<size_t>(H));
+  p.runs = o; o = up(o + 4 * chunks);
   p.total = o;
   return p;
 }
 
+// Threads of a row and rows (or stretches) of a CTA of kSumThreads.
+template <int VEC>
+static dim3 sum_block(int H, int least) {
+  int tx = least;
+  while (tx < kSumThreads && tx * VEC * kCols<VEC> < H) tx *= 2;
+  return dim3(tx, kSumThreads / tx);
+}
+
+template <int VEC>
+static long long sum_slabs(int H, const dim3& block) {
+  const long long width = static_cast<long long>(block.x) * VEC * kCols<VEC>;
+  return (H + width - 1) / width;
+}
+
+static long long zero_ctas(const SumArgs& s) {
+  return s.accumulate ? 0 : (static_cast<long long>(s.V) + s.zero_rows - 1) / s.zero_rows;
+}
+
 template <typename T, int VEC>
 static cudaError_t few_t(SumArgs s, const EmbedBwdArgs& a, cudaStream_t st) {
-  const long long slabs = (s.H + kSumThreads * VEC - 1) / (kSumThreads * VEC);
-  const long long zeros = s.accumulate ? 0 : (static_cast<long long>(s.V) + s.zero_rows - 1) / s.zero_rows;
-  s.sum_ctas = static_cast<int>(s.T * slabs);
-  const long long grid = s.sum_ctas + zeros;
-  embed_few_kernel<T, VEC><<<static_cast<unsigned>(grid > 0 ? grid : 1), kSumThreads, 0, st>>>(s, a.ids, a.status);
+  const dim3 block = sum_block<VEC>(s.H, 16);
+  s.sum_ctas = static_cast<int>(s.T * sum_slabs<VEC>(s.H, block));
+  const long long grid = s.sum_ctas + zero_ctas(s);
+  embed_few_kernel<T, VEC><<<static_cast<unsigned>(grid > 0 ? grid : 1), block, 0, st>>>(s, a.ids, a.status);
   return cudaGetLastError();
 }
 
@@ -712,7 +848,7 @@ cudaError_t launch_embed_sort(const EmbedBwdArgs& a, cudaStream_t s) {
     return a.T <= per ? cluster_sort<1>(p, s)
                       : a.T <= 2 * per ? cluster_sort<2>(p, s) : cluster_sort<4>(p, s);
   }
-  cudaError_t e = cudaMemsetAsync(a.status, 0, sizeof(DevStatus), s);
+  cudaError_t e = cudaMemsetAsync(a.status, 0, kClearBytes, s);
   if (e != cudaSuccess) return e;
   for (int i = 0; i < passes; ++i) {
     SortPass p;
@@ -742,36 +878,31 @@ cudaError_t launch_embed_sort(const EmbedBwdArgs& a, cudaStream_t s) {
 }
 
 template <typename T, int VEC>
-static cudaError_t sum_t(SumArgs s, int n_chunks, cudaStream_t st) {
-  int tx = 32;
-  while (tx < kSumThreads && tx * VEC < s.H) tx *= 2;
-  const dim3 block(tx, kSumThreads / tx);
-  const long long slabs = (s.H + tx * VEC - 1) / (tx * VEC);
-  const long long zeros = s.accumulate ? 0 : (static_cast<long long>(s.V) + s.zero_rows - 1) / s.zero_rows;
-  s.sum_ctas = static_cast<int>((n_chunks + block.y - 1) / block.y * slabs);
-  return launch_overlapped(embed_sum_kernel<T, VEC>, dim3(static_cast<unsigned>(s.sum_ctas + zeros)),
-                           block, 0, st, s);
+static cudaError_t sum_t(SumArgs s, cudaStream_t st) {
+  const dim3 block = sum_block<VEC>(s.H, 32);
+  s.sum_ctas = static_cast<int>((s.n_chunks + block.y - 1) / block.y * sum_slabs<VEC>(s.H, block));
+  return launch_overlapped(embed_sum_kernel<T, VEC>,
+                           dim3(static_cast<unsigned>(s.sum_ctas + zero_ctas(s))), block, 0, st, s);
 }
 
-cudaError_t launch_embed_bwd(const EmbedBwdArgs& a, int is_bf16, cudaStream_t st) {
+cudaError_t launch_embed_bwd(const EmbedBwdArgs& a, int is_bf16, int num_sms, cudaStream_t st) {
   const EmbedBwdPlan pl = embed_bwd_plan(a.T, a.H, a.V);
   const SumArgs s = sum_args(a, pl, (sort_passes(a.V) - 1) & 1);
+  const bool aligned = a.H % (is_bf16 ? 8 : 4) == 0;
   if (!embed_bwd_sorts(a.T)) {
-    if (a.H % (is_bf16 ? 8 : 4) == 0)
-      return is_bf16 ? few_t<__nv_bfloat16, 8>(s, a, st) : few_t<float, 4>(s, a, st);
-    return is_bf16 ? few_t<__nv_bfloat16, 1>(s, a, st) : few_t<float, 1>(s, a, st);
+    if (is_bf16) return aligned ? few_t<__nv_bfloat16, 8>(s, a, st) : few_t<__nv_bfloat16, 1>(s, a, st);
+    return aligned ? few_t<float, 4>(s, a, st) : few_t<float, 1>(s, a, st);
   }
-  const int n_chunks = static_cast<int>((a.T + pl.chunk - 1) / pl.chunk);
-  const int vec16 = is_bf16 ? 8 : 4;
   cudaError_t e;
-  if (a.H % vec16 == 0)
-    e = is_bf16 ? sum_t<__nv_bfloat16, 8>(s, n_chunks, st) : sum_t<float, 4>(s, n_chunks, st);
-  else
-    e = is_bf16 ? sum_t<__nv_bfloat16, 1>(s, n_chunks, st) : sum_t<float, 1>(s, n_chunks, st);
-  if (e != cudaSuccess || n_chunks <= 1) return e;
-  return launch_overlapped(embed_join_kernel,
-                           dim3(n_chunks, (a.H + kSumThreads - 1) / kSumThreads), dim3(kSumThreads),
-                           0, st, s, n_chunks);
+  if (is_bf16) e = aligned ? sum_t<__nv_bfloat16, 8>(s, st) : sum_t<__nv_bfloat16, 1>(s, st);
+  else e = aligned ? sum_t<float, 4>(s, st) : sum_t<float, 1>(s, st);
+  if (e != cudaSuccess || s.n_chunks <= 1) return e;
+  const int w = a.H % 4 == 0 ? 4 : 1;
+  const long long most = static_cast<long long>(s.n_chunks) * ((a.H + 32 * w - 1) / (32 * w));
+  // an item is a chain of latencies, so as many at a time as there may be
+  const dim3 grid(static_cast<unsigned>(most < 64LL * num_sms ? most : 64LL * num_sms));
+  return w == 4 ? launch_overlapped(embed_join_kernel<4>, grid, dim3(32 * kJoinParts), 0, st, s)
+                : launch_overlapped(embed_join_kernel<1>, grid, dim3(32 * kJoinParts), 0, st, s);
 }
 
 }  // namespace eas

@@ -232,6 +232,7 @@ struct EmbedBwdPlan {     // sizes of the backward's scratch, in bytes from its 
   size_t keys[2], pos[2]; // the sort's two buffers of (id, token)
   size_t hist;            // digit counts of the sort's tiles
   size_t partial;         // sums of the pieces of rows that several workers share
+  size_t runs;            // where those rows' tokens start in the sorted list
   size_t total;
   int chunk;              // sorted tokens a worker
 };
@@ -251,7 +252,7 @@ struct EmbedBwdArgs {
 // and without one launch_embed_bwd does.
 bool embed_bwd_sorts(long long T);
 cudaError_t launch_embed_sort(const EmbedBwdArgs& a, cudaStream_t s);
-cudaError_t launch_embed_bwd(const EmbedBwdArgs& a, int is_bf16, cudaStream_t s);
+cudaError_t launch_embed_bwd(const EmbedBwdArgs& a, int is_bf16, int num_sms, cudaStream_t s);
 
 // ---- gradient norm and clipping (eas_clip.cu) ----
 struct ClipTensor {

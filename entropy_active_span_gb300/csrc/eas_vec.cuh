@@ -43,6 +43,18 @@ __device__ __forceinline__ Raw<T, VEC> load_raw(const T* p) {
   return r;
 }
 
+// The same from memory that the kernel does not write: the load may move ahead
+// of the kernel's stores.
+template <typename T, int VEC>
+__device__ __forceinline__ Raw<T, VEC> load_const(const T* p) {
+  Raw<T, VEC> r;
+  if constexpr (VEC == 1)
+    r.v = __ldg(p);
+  else
+    r.v = __ldg(reinterpret_cast<const uint4*>(p));
+  return r;
+}
+
 template <typename T, int VEC>
 __device__ __forceinline__ void widen(const Raw<T, VEC>& r, float (&f)[VEC]) {
   if constexpr (VEC == 1) {
