@@ -108,6 +108,25 @@ def test_a_run_across_many_chunks():
     check_bwd(ids, dout, V, 1.0, dw)
 
 
+@pytest.mark.parametrize("accumulate", [False, True])
+@pytest.mark.parametrize("V", [40, 400])
+def test_runs_around_chunk_boundaries(V, accumulate):
+    """Runs that start, end and lie across the workers' chunks (16 tokens at this
+    size, and powers of two above it) at every offset; small integers, so exact."""
+    rng = np.random.default_rng(V)
+    lens = rng.choice([1, 2, 15, 16, 17, 31, 32, 33, 47, 48, 49, 64, 80], V)
+    lens[0], lens[1] = 16, 16
+    ids = np.repeat(np.arange(V), lens).astype(np.int32)
+    assert len(ids) > 600
+    order = rng.permutation(len(ids))
+    for these in (ids, ids[order], np.concatenate([ids, np.full(100, -1, np.int32)])):
+        T, H = len(these), 72
+        dout = torch.from_numpy(rng.integers(-4, 5, (T, H)).astype(np.float32)).bfloat16().cuda()
+        base = torch.zeros(V, H, device="cuda")
+        dw = eas.embed_bwd(torch.from_numpy(these).cuda(), dout, V, 1.0, accumulate, dweight=base)
+        assert np.array_equal(f64(dw), oracle.embed_grad(these, f64(dout), V, 1.0))
+
+
 @pytest.mark.parametrize("T", [8192, 8193, 20000, 50001, 131072, 131073, 262144 + 77, 600000])
 def test_large_sorts(T):
     """The sort in one launch at each of its sizes, and beyond them over several:
