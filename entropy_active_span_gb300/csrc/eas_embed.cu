@@ -26,31 +26,9 @@ constexpr int kWhereEmbed = 20;
 template <int VEC>
 constexpr int kCols = VEC == 1 ? 4 : 1;
 
-// CTA 0 also checks every id and writes the status word: no other launch clears
-// it.
 template <typename T, int VEC, int kRows>
 __global__ void __launch_bounds__(256)
 embed_fwd_kernel(const EmbedFwdArgs p) {
-  if (p.status && blockIdx.x == 0) {
-    __shared__ unsigned long long first_bad;
-    const int tid = threadIdx.y * blockDim.x + threadIdx.x;
-    if (tid == 0) first_bad = ~0ull;
-    __syncthreads();
-    for (long long t = tid; t < p.T; t += 256) {
-      const int id = p.ids[t];
-      if (id < -1 || id >= p.V) {
-        atomicMin(&first_bad, static_cast<unsigned long long>(t));
-        break;
-      }
-    }
-    __syncthreads();
-    if (tid == 0) {
-      const bool bad = first_bad != ~0ull;
-      p.status->code = bad ? kStInvalidArg : kStOk;
-      p.status->where = bad ? kWhereEmbed : 0;
-      p.status->info = bad ? static_cast<int>(first_bad) : 0;
-    }
-  }
   // kRows rows a thread: their ids come in one latency and their loads leave
   // together
   const long long t0 = (static_cast<long long>(blockIdx.x) * blockDim.y + threadIdx.y) * kRows;
@@ -59,6 +37,8 @@ embed_fwd_kernel(const EmbedFwdArgs p) {
   for (int r = 0; r < kRows; ++r) {
     const int id = t0 + r < p.T ? p.ids[t0 + r] : -1;
     src[r] = id >= 0 && id < p.V ? static_cast<const T*>(p.table) + static_cast<long long>(id) * p.H : nullptr;
+    if (p.status && id != -1 && !src[r] && threadIdx.x == 0)
+      report(p.status, kStInvalidArg, kWhereEmbed, static_cast<int>(t0 + r));
   }
   T* dst = static_cast<T*>(p.out) + t0 * p.H;
   const int step = blockDim.x * VEC;
@@ -746,6 +726,10 @@ int sort_passes(int V) {
 
 template <typename T, int VEC>
 static cudaError_t embed_fwd_t(const EmbedFwdArgs& a, int num_sms, cudaStream_t s) {
+  if (a.status) {
+    const cudaError_t e = cudaMemsetAsync(a.status, 0, sizeof(DevStatus), s);
+    if (e != cudaSuccess || a.T == 0) return e;
+  }
   int tx = 32;
   while (tx < 256 && tx * VEC < a.H) tx *= 2;
   const dim3 block(tx, 256 / tx);
@@ -755,7 +739,7 @@ static cudaError_t embed_fwd_t(const EmbedFwdArgs& a, int num_sms, cudaStream_t 
   if (groups >= 8LL * num_sms) {
     embed_fwd_kernel<T, VEC, 4><<<static_cast<unsigned>(groups), block, 0, s>>>(a);
   } else {
-    const long long grid = a.T > 0 ? (a.T + block.y - 1) / block.y : 1;
+    const long long grid = (a.T + block.y - 1) / block.y;
     embed_fwd_kernel<T, VEC, 1><<<static_cast<unsigned>(grid), block, 0, s>>>(a);
   }
   return cudaGetLastError();
