@@ -1033,7 +1033,7 @@ eas_status eas_rmsnorm_fwd(const void* x, const void* residual, const void* weig
 }
 
 static size_t norm_bwd_rstd_offset(long long R, long long H) {
-  return align_up(4 * static_cast<size_t>(rmsnorm_bwd_partials(R, H)) * static_cast<size_t>(H));
+  return align_up(sizeof(DevStatus)) + align_up(4 * static_cast<size_t>(rmsnorm_bwd_partials(R, H)) * static_cast<size_t>(H));
 }
 
 size_t eas_rmsnorm_bwd_workspace_size(int64_t R, int64_t H) {
@@ -1060,7 +1060,7 @@ eas_status eas_rmsnorm_bwd(const void* dy, const void* sum, const void* weight, 
   st = device_info(&di);
   if (st != EAS_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const RmsNormBwdArgs a = {dy, sum, weight, ds, mask, dx, at<float>(ws, 0),
+  const RmsNormBwdArgs a = {dy, sum, weight, ds, mask, dx, at<float>(ws, align_up(sizeof(DevStatus))),
                             at<float>(ws, norm_bwd_rstd_offset(R, H)), R, static_cast<int>(H), eps};
   int n = 0;
   {
@@ -1069,7 +1069,7 @@ eas_status eas_rmsnorm_bwd(const void* dy, const void* sum, const void* weight, 
   }
   {
     Trace tr_(kTrNormDw, s);
-    EAS_CUDA(launch_rmsnorm_dw(a.partial, n, a.H, dweight, s), "rmsnorm_dweight");
+    EAS_CUDA(launch_rmsnorm_dw(a.partial, n, a.H, dweight, static_cast<DevStatus*>(ws), s), "rmsnorm_dweight");
   }
   return EAS_OK;
 }
@@ -1138,7 +1138,7 @@ eas_status eas_embed_bwd(const int32_t* ids, const void* dout, int64_t T, int64_
 
 size_t eas_clip_grad_norm_workspace_size(int32_t n) {
   if (n < 0) return 0;
-  return clip_workspace_bytes(n);
+  return align_up(sizeof(DevStatus)) + clip_workspace_bytes(n);
 }
 
 eas_status eas_clip_grad_norm(const void* const* grads, void* const* outs, const int64_t* numels,
@@ -1151,8 +1151,8 @@ eas_status eas_clip_grad_norm(const void* const* grads, void* const* outs, const
   if (outs && !(max_norm >= 0.f)) return fail(EAS_ERR_INVALID_ARG, "max_norm must be >= 0");
   if (!aligned(norm, 4) || !aligned(ws, 256))
     return fail(EAS_ERR_INVALID_ARG, "ws must be 256-byte aligned");
-  if (ws_bytes < clip_workspace_bytes(n))
-    return fail(EAS_ERR_WORKSPACE, "workspace %zu < %zu", ws_bytes, clip_workspace_bytes(n));
+  const size_t need = eas_clip_grad_norm_workspace_size(n);
+  if (ws_bytes < need) return fail(EAS_ERR_WORKSPACE, "workspace %zu < %zu", ws_bytes, need);
   try {
     std::vector<ClipTensor> list(static_cast<size_t>(n));
     // every buffer that is written, and every one that is read, by address
@@ -1202,7 +1202,8 @@ eas_status eas_clip_grad_norm(const void* const* grads, void* const* outs, const
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     Trace tr_(outs ? kTrGradClip : kTrGradNorm, s);
     EAS_CUDA(launch_clip_grad_norm(list.data(), n, outs != nullptr, max_norm,
-                                   static_cast<double*>(ws), norm, di.sms, s),
+                                   at<double>(ws, align_up(sizeof(DevStatus))), norm,
+                                   static_cast<DevStatus*>(ws), di.sms, s),
              "clip_grad_norm");
     return EAS_OK;
   } catch (const std::bad_alloc&) {

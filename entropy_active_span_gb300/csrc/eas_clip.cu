@@ -56,7 +56,7 @@ __device__ __forceinline__ int tensor_of(const List<N>& l, int chunk) {
 // leaves the range in which that holds.  fp64 sums from each 16-byte load on
 // were built first: this part's fp64 rate is far below its fp32 rate, and the
 // norm and clipping of 1.33 G gradients (0.53 G fp32, 0.81 G bf16, into bf16)
-// took 3370 us; this way 1482, which is the time of reading everything twice
+// took 3370 us; this way 1472, which is the time of reading everything twice
 // and writing it once (10.1 GB at 6.8 TB/s).
 struct Squares {
   float hi = 0.f, lo = 0.f;
@@ -180,11 +180,14 @@ __device__ __forceinline__ float norm_of(const double* partial, int n, double* s
 }
 
 __global__ void __launch_bounds__(kThreads)
-grad_norm_kernel(const double* partial, int n, float* norm) {
+grad_norm_kernel(const double* partial, int n, float* norm, DevStatus* st) {
   __shared__ double sm[kThreads / 32];
   wait_for_launch_before();
   const float v = norm_of(partial, n, sm);
-  if (threadIdx.x == 0) *norm = v;
+  if (threadIdx.x == 0) {
+    *norm = v;
+    *st = DevStatus{};   // nothing here can fail on the device
+  }
 }
 
 template <typename I, typename O>
@@ -232,14 +235,17 @@ __device__ __forceinline__ void scale_chunk(const I* in, O* out, int n, float c)
 template <int N>
 __global__ void __launch_bounds__(kThreads)
 grad_clip_kernel(const __grid_constant__ List<N> l, const double* partial, int n_partial,
-                 float* norm, float max_norm) {
+                 float* norm, float max_norm, DevStatus* st) {
   __shared__ double sm[kThreads / 32];
   // the first chunk's tensor is looked up while the norm is on its way
   int k = l.n_chunks - 1 - blockIdx.x;
   int t = tensor_of(l, k);
   wait_for_launch_before();
   const float v = norm_of(partial, n_partial, sm);
-  if (blockIdx.x == 0 && threadIdx.x == 0) *norm = v;
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    *norm = v;
+    *st = DevStatus{};
+  }
   const float c = isfinite(v) ? fminf(1.f, max_norm / (v + 1e-6f)) : 1.f;
   // from the last chunk down: what the norm read last is still in L2
   for (; k >= 0; k -= gridDim.x, t = k >= 0 ? tensor_of(l, k) : 0) {
@@ -301,7 +307,7 @@ int ctas(int chunks, int num_sms) {
 
 template <int N>
 cudaError_t launch_lists(const ClipTensor* t, int n, bool clip, float max_norm, double* partial,
-                         float* norm, int num_sms, cudaStream_t s) {
+                         float* norm, DevStatus* st, int num_sms, cudaStream_t s) {
   const int lc = log_chunk_of(t, n, num_sms);
   List<N> l;
   int np = 0;
@@ -315,12 +321,13 @@ cudaError_t launch_lists(const ClipTensor* t, int n, bool clip, float max_norm, 
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   if (!clip || np == 0)
-    return launch_overlapped(grad_norm_kernel, dim3(1), dim3(kThreads), 0, s, partial, np, norm);
+    return launch_overlapped(grad_norm_kernel, dim3(1), dim3(kThreads), 0, s, partial, np, norm,
+                             st);
   for (int at = 0; at < n;) {
     at = fill(l, t, n, at, lc);
     if (l.n_chunks == 0) continue;
     e = launch_overlapped(grad_clip_kernel<N>, dim3(ctas(l.n_chunks, num_sms)), dim3(kThreads), 0, s,
-                          l, partial, np, norm, max_norm);
+                          l, partial, np, norm, max_norm, st);
     if (e != cudaSuccess) return e;
   }
   return cudaGetLastError();
@@ -334,10 +341,11 @@ size_t clip_workspace_bytes(long long n) {
 }
 
 cudaError_t launch_clip_grad_norm(const ClipTensor* t, int n, bool clip, float max_norm,
-                                  double* partial, float* norm, int num_sms, cudaStream_t s) {
+                                  double* partial, float* norm, DevStatus* st, int num_sms,
+                                  cudaStream_t s) {
   return n <= kSmallList
-             ? launch_lists<kSmallList>(t, n, clip, max_norm, partial, norm, num_sms, s)
-             : launch_lists<kLargeList>(t, n, clip, max_norm, partial, norm, num_sms, s);
+             ? launch_lists<kSmallList>(t, n, clip, max_norm, partial, norm, st, num_sms, s)
+             : launch_lists<kLargeList>(t, n, clip, max_norm, partial, norm, st, num_sms, s);
 }
 
 }  // namespace eas

@@ -6,9 +6,14 @@
 // The gradient sorts the tokens by id (stable radix sort, so the tokens of a
 // row stay in their order), cuts the sorted list into chunks of equal length
 // and sums each chunk's runs of equal ids in fp32 registers.  A run that lies
-// in one chunk is written to its row of dE at once; the pieces of a run that
-// crosses chunks go to scratch and are added in order by a second kernel.  No
-// floating-point atomics: results repeat to the bit.
+// in two chunks at most is written to its row of dE at once; the pieces of a
+// longer one go to scratch and are added in order by a second kernel.  Lists of
+// up to 512 tokens need no sort.  No floating-point atomics: results repeat to
+// the bit.
+//
+// All of it is bound by bytes: dout is read once, dE written once.  16384 tokens
+// into [128256, 4096] take 329 us and 131072 Zipf-distributed ones into [129280,
+// 7168] 785 us, both 6.8 TB/s; the plain copy rate is 6.8.
 #include "eas_device.cuh"
 #include "eas_kernels.h"
 #include "eas_vec.cuh"
@@ -201,7 +206,9 @@ __global__ void __launch_bounds__(kSortThreads) sort_scatter_kernel(const SortPa
 // a pass ranks every warp's run of digits, adds the counts up over warps and
 // (through distributed shared memory) over CTAs, and moves each pair to its
 // place in whichever CTA holds that.  A thread keeps its pairs in registers
-// meanwhile, so one buffer is enough.
+// meanwhile, so one buffer is enough.  A call with 16384 tokens of 64 columns
+// takes 28 us this way; at 131072 tokens the eight CTAs sorted for 75 us against
+// 33 of the launches above, which is why the lists end at 32768.
 constexpr int kClusterCtas = 8;
 constexpr int kClusterThreads = 1024;
 constexpr int kClusterWarps = kClusterThreads / 32;
@@ -554,7 +561,7 @@ __global__ void __launch_bounds__(32 * kJoinParts) embed_join_kernel(const SumAr
       for (int q = part * per; q < to; ++q) {
         const float* from = p.partial + (q == 0 ? 2ll * first + 1 : 2ll * (first + q)) * p.H + c;
         float f[W];
-        widen<float, W>(load_const<float, W>(from), f);
+        widen<float, W>(load_raw<float, W>(from), f);   // written by the launch before
 #pragma unroll
         for (int i = 0; i < W; ++i) acc[i] += f[i];
       }

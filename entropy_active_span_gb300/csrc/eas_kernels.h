@@ -214,7 +214,9 @@ long long rmsnorm_bwd_partials(long long R, long long H);
 // Writes dx and *n_partials rows of partial; launch_rmsnorm_dw sums them.
 cudaError_t launch_rmsnorm_bwd(const RmsNormBwdArgs& a, int is_bf16, int num_sms, int* n_partials,
                                cudaStream_t s);
-cudaError_t launch_rmsnorm_dw(const float* partial, int n, int H, float* dw, cudaStream_t s);
+// Also clears the status word.
+cudaError_t launch_rmsnorm_dw(const float* partial, int n, int H, float* dw, DevStatus* st,
+                              cudaStream_t s);
 
 // ---- embedding (eas_embed.cu) ----
 struct EmbedFwdArgs {
@@ -262,9 +264,10 @@ struct ClipTensor {
   int in_bf16, out_bf16;
 };
 size_t clip_workspace_bytes(long long n_tensors);
-// The norm, and with `clip` the scaled tensors too.
+// The norm, and with `clip` the scaled tensors too; clears the status word.
 cudaError_t launch_clip_grad_norm(const ClipTensor* t, int n, bool clip, float max_norm,
-                                  double* partial, float* norm, int num_sms, cudaStream_t s);
+                                  double* partial, float* norm, DevStatus* st, int num_sms,
+                                  cudaStream_t s);
 
 // ---- helpers the C-ABI translation units share (eas_api.cu) ----
 size_t lmhead_fwd_workspace_bytes(long long T, long long H, long long V, int dtype);

@@ -14,7 +14,8 @@
 // All of it is bound by bytes: about 10 operations an element.  What it takes is
 // to have enough of them on their way all the time, which a row held by threads
 // that load, reduce and store in turn does not: [65536, 5120] bf16 backward took
-// 737 us that way and takes 397 with the ring below (6.8 TB/s).
+// 737 us that way and takes 395 with the ring below (6.8 TB/s), and [262144,
+// 8192] forward with residual, mask and codes 3023 us and 2780 (6.9 TB/s).
 #include <cuda_fp8.h>
 
 #include "eas_device.cuh"
@@ -418,7 +419,7 @@ rmsnorm_fwd_long_kernel(const RmsNormFwdArgs p) {
 // CTA's row of `partial` at the end.  The number of partial rows and the order
 // of every sum depend on the shape and the machine only, so results repeat to
 // the bit.  Whether there is a ds and a mask is compiled in for the longer
-// rows: [65536, 5120] bf16 with ds took 447 us deciding in the loop and 397
+// rows: [65536, 5120] bf16 with ds took 447 us deciding in the loop and 395
 // without.
 template <typename T, int NV, int kStages, bool kShort, bool kOdd, bool kDs, bool kMask>
 __global__ void __launch_bounds__(kShort ? 256 : 512, kShort ? 2 : 1)
@@ -724,12 +725,13 @@ rmsnorm_dw_long_kernel(const RmsNormBwdArgs p) {
 // warps take every kDwWarps-th partial row, then the warps' sums in order.
 constexpr int kDwWarps = 16;
 __global__ void __launch_bounds__(32 * kDwWarps)
-rmsnorm_dw_kernel(const float* __restrict__ partial, int n, int H, float* __restrict__ dw) {
+rmsnorm_dw_kernel(const float* partial, int n, int H, float* dw, DevStatus* st) {
   __shared__ float sm[kDwWarps][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
   float acc = 0.f;
   wait_for_launch_before();
+  if (blockIdx.x == 0 && threadIdx.x == 0) *st = DevStatus{};   // nothing here can fail on the device
   if (c < H) {
 #pragma unroll 8
     for (int i = warp; i < n; i += kDwWarps) acc += partial[static_cast<long long>(i) * H + c];
@@ -845,8 +847,7 @@ cudaError_t bwd_kind(const RmsNormBwdArgs& a, const RingShape& r, unsigned g, cu
 
 template <typename T, bool kOdd>
 cudaError_t bwd_rows(const RmsNormBwdArgs& a, const RingShape& r, unsigned g, cudaStream_t s) {
-  if (r.nv == 2)
-    return r.stages == 2 ? bwd_kind<T, 2, 2, kOdd>(a, r, g, s) : bwd_kind<T, 2, 3, kOdd>(a, r, g, s);
+  if (r.nv == 2) return bwd_kind<T, 2, 3, kOdd>(a, r, g, s);   // 512 threads an SM: always three deep
   return r.stages == 2 ? bwd_kind<T, 4, 2, kOdd>(a, r, g, s) : bwd_kind<T, 4, 3, kOdd>(a, r, g, s);
 }
 
@@ -900,9 +901,10 @@ cudaError_t launch_rmsnorm_bwd(const RmsNormBwdArgs& a, int is_bf16, int num_sms
                  : bwd_t<float>(a, num_sms, n_partials, s);
 }
 
-cudaError_t launch_rmsnorm_dw(const float* partial, int n, int H, float* dw, cudaStream_t s) {
+cudaError_t launch_rmsnorm_dw(const float* partial, int n, int H, float* dw, DevStatus* st,
+                              cudaStream_t s) {
   return launch_overlapped(rmsnorm_dw_kernel, dim3((H + 31) / 32), dim3(32 * kDwWarps), 0, s, partial,
-                           n, H, dw);
+                           n, H, dw, st);
 }
 
 }  // namespace eas

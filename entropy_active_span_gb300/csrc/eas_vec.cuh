@@ -43,8 +43,8 @@ __device__ __forceinline__ Raw<T, VEC> load_raw(const T* p) {
   return r;
 }
 
-// The same from memory that the kernel does not write: the load may move ahead
-// of the kernel's stores.
+// The same from memory that neither the kernel nor an overlapped launch before it
+// writes: the load may move ahead of stores and waits.
 template <typename T, int VEC>
 __device__ __forceinline__ Raw<T, VEC> load_const(const T* p) {
   Raw<T, VEC> r;

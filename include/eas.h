@@ -399,7 +399,7 @@ eas_status eas_rmsnorm_fwd(const void* x, const void* residual, const void* weig
  *   mask     as in the forward: inactive rows' dy and s are not read, their dx
  *            is ds or 0, and they add nothing to dweight
  *   dx       [R, H] out in dtype; dweight [H] fp32 out; both overwritten
- *   ws       eas_rmsnorm_bwd_workspace_size(R, H) bytes
+ *   ws       eas_rmsnorm_bwd_workspace_size(R, H) bytes; holds the status word
  * Sums are taken in a fixed order: results repeat to the bit.
  */
 size_t eas_rmsnorm_bwd_workspace_size(int64_t R, int64_t H);
@@ -455,7 +455,7 @@ eas_status eas_embed_bwd(const int32_t* ids, const void* dout, int64_t T, int64_
  *            place) or another buffer, which no other entry may overlap.  outs
  *            NULL: only the norm is computed (max_norm is not used).
  *   norm     [1] fp32 device, out: the norm before clipping
- *   ws       eas_clip_grad_norm_workspace_size(n) bytes
+ *   ws       eas_clip_grad_norm_workspace_size(n) bytes; holds the status word
  */
 size_t eas_clip_grad_norm_workspace_size(int32_t n);
 

@@ -197,6 +197,14 @@ def test_outputs_are_optional():
     assert b[1] is None and torch.equal(b[0], y) and torch.equal(b[3], s)
 
 
+@pytest.mark.parametrize("R,H", [(4, 64), (0, 64), (3, 1003), (2, 40001)])
+def test_status_word_is_cleared(R, H):
+    x, w, _, _ = problem(max(R, 1), H, "bf16", False, None)
+    ws = torch.full((eas.rmsnorm_bwd_workspace_size(R, H),), 255, dtype=torch.uint8, device="cuda")
+    eas.rmsnorm_bwd(x[:R], x[:R], w, ws=ws)
+    assert eas.read_device_status(ws) == 0
+
+
 def test_refusals():
     x, w, r, m = problem(4, 64, "bf16", True, "some")
     with pytest.raises(ValueError):

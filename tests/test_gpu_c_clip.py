@@ -106,6 +106,16 @@ def test_non_finite_gradients_are_left_alone(bad, at):
         assert not torch.isfinite(eas.clip_grad_norm([z], None)).any()
 
 
+def test_status_word_is_cleared():
+    g = rand(1000, "fp32", 0)
+    ws = torch.full((eas.clip_grad_norm_workspace_size(1),), 255, dtype=torch.uint8, device="cuda")
+    eas.clip_grad_norm([g], 1.0, ws=ws)
+    assert eas.read_device_status(ws) == 0
+    ws.fill_(255)
+    eas.clip_grad_norm([g], None, ws=ws)
+    assert eas.read_device_status(ws) == 0
+
+
 def test_zeros_and_empty_tensors():
     z = [torch.zeros(1000, device="cuda"), torch.empty(0, device="cuda", dtype=torch.bfloat16)]
     assert float(eas.clip_grad_norm(z, 1.0)) == 0 and (z[0] == 0).all()
