@@ -27,6 +27,7 @@ import ctypes
 from array import array
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import _lib
 from ._lib import (EAS_BF16, EAS_DEFAULT_VOCAB_CHUNK, EAS_E4M3, EAS_FP32, EAS_REUSE_FWD_ROWS,
@@ -702,6 +703,7 @@ class FusedRMSNorm(torch.autograd.Function):
         return y, (s if residual is not None else None), q, scale
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, g_y, g_s, _q, _scale):
         s, weight, mask = ctx.saved_tensors
         if g_y is None:
@@ -731,6 +733,7 @@ class FusedEmbedding(torch.autograd.Function):
         return embed_fwd(ids, table, scale)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, g):
         ids, = ctx.saved_tensors
         return None, embed_bwd(ids, _grad_rows(g), ctx.V, ctx.scale).to(ctx.dtype), None

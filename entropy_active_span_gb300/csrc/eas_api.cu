@@ -14,6 +14,7 @@
 #include <cstdlib>
 #include <cstring>
 #include <deque>
+#include <initializer_list>
 #include <mutex>
 #include <new>
 #include <vector>
@@ -996,8 +997,17 @@ eas_status eas_selftest_wait_timeout(int64_t budget_cycles, void* ws, size_t ws_
 
 // ------------------------------------------------ operators around the LM head
 
-// Shape and type of the row operators: any H (odd ones take element-wide
-// accesses).
+// Whether [a, a + na) and [b, b + nb) share a byte (null shares none).
+static bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x && y && na && nb && x < y + nb && y < x + na;
+}
+
+// The same for two buffers of n bytes of which one may replace the other.
+static bool overlap_partly(const void* a, const void* b, size_t n) { return a != b && overlap(a, n, b, n); }
+
+// Shape and type of the row operators: any H (odd ones keep their vectors on
+// 16-byte boundaries in memory).
 static eas_status check_rows(long long R, long long H, eas_dtype dt) {
   if (R < 0 || R > 0x7fffff00LL) return fail(EAS_ERR_INVALID_ARG, "rows=%lld out of range", R);
   if (H < 1 || H > (1LL << 20)) return fail(EAS_ERR_INVALID_ARG, "H=%lld out of range", H);
@@ -1019,8 +1029,13 @@ eas_status eas_rmsnorm_fwd(const void* x, const void* residual, const void* weig
   if (!aligned(x, 16) || !aligned(residual, 16) || !aligned(weight, 16) || !aligned(sum_out, 16) ||
       !aligned(y, 16) || !aligned(y_e4m3, 16) || !aligned(y_scale, 4))
     return fail(EAS_ERR_INVALID_ARG, "tensors must be 16-byte aligned");
-  if (R > 0 && y && (y == x || y == residual || y == sum_out))
-    return fail(EAS_ERR_INVALID_ARG, "y must not be x, residual or sum_out");
+  const size_t codes = static_cast<size_t>(R) * static_cast<size_t>(H), rows = codes * elem_size(dtype);
+  for (const void* in : {x, residual, static_cast<const void*>(sum_out)})
+    if (overlap(y, rows, in, rows) || overlap(y_e4m3, codes, in, rows))
+      return fail(EAS_ERR_INVALID_ARG, "y and y_e4m3 must not overlap x, residual or sum_out");
+  if (overlap(y, rows, y_e4m3, codes) || overlap_partly(sum_out, x, rows) ||
+      overlap_partly(sum_out, residual, rows))
+    return fail(EAS_ERR_INVALID_ARG, "an output overlaps another buffer");
   DevInfo di;
   st = device_info(&di);
   if (st != EAS_OK) return st;
@@ -1052,8 +1067,9 @@ eas_status eas_rmsnorm_bwd(const void* dy, const void* sum, const void* weight, 
   if (!aligned(dy, 16) || !aligned(sum, 16) || !aligned(weight, 16) || !aligned(ds, 16) ||
       !aligned(dx, 16) || !aligned(dweight, 16) || !aligned(ws, 256))
     return fail(EAS_ERR_INVALID_ARG, "tensors must be 16-byte and ws 256-byte aligned");
-  if (R > 0 && (dx == dy || dx == sum))
-    return fail(EAS_ERR_INVALID_ARG, "dx must not be dy or s");
+  const size_t rows = static_cast<size_t>(R) * static_cast<size_t>(H) * elem_size(dtype);
+  if (overlap(dx, rows, dy, rows) || overlap(dx, rows, sum, rows) || overlap_partly(dx, ds, rows))
+    return fail(EAS_ERR_INVALID_ARG, "dx must not overlap dy or s, nor ds in part");
   const size_t need = eas_rmsnorm_bwd_workspace_size(R, H);
   if (ws_bytes < need) return fail(EAS_ERR_WORKSPACE, "workspace %zu < %zu", ws_bytes, need);
   DevInfo di;
@@ -1090,7 +1106,9 @@ eas_status eas_embed_fwd(const int32_t* ids, const void* table, int64_t T, int64
   if (!table || (T > 0 && (!ids || !out))) return fail(EAS_ERR_INVALID_ARG, "null pointer");
   if (!aligned(ids, 4) || !aligned(table, 16) || !aligned(out, 16) || !aligned(ws, 16))
     return fail(EAS_ERR_INVALID_ARG, "table, out and ws must be 16-byte aligned");
-  if (T > 0 && out == table) return fail(EAS_ERR_INVALID_ARG, "out must not be the table");
+  const size_t row = static_cast<size_t>(H) * elem_size(dtype);
+  if (overlap(out, row * static_cast<size_t>(T), table, row * static_cast<size_t>(V)))
+    return fail(EAS_ERR_INVALID_ARG, "out must not overlap the table");
   if (ws && ws_bytes < sizeof(DevStatus)) return fail(EAS_ERR_WORKSPACE, "workspace too small");
   DevInfo di;
   st = device_info(&di);
@@ -1118,6 +1136,9 @@ eas_status eas_embed_bwd(const int32_t* ids, const void* dout, int64_t T, int64_
   if (!dweight || !ws || (T > 0 && (!ids || !dout))) return fail(EAS_ERR_INVALID_ARG, "null pointer");
   if (!aligned(ids, 4) || !aligned(dout, 16) || !aligned(dweight, 16) || !aligned(ws, 256))
     return fail(EAS_ERR_INVALID_ARG, "dout and dweight must be 16-byte and ws 256-byte aligned");
+  if (overlap(dweight, 4 * static_cast<size_t>(V) * static_cast<size_t>(H), dout,
+              static_cast<size_t>(T) * static_cast<size_t>(H) * elem_size(dtype)))
+    return fail(EAS_ERR_INVALID_ARG, "dweight must not overlap dout");
   const size_t need = eas_embed_bwd_workspace_size(T, H, V);
   if (ws_bytes < need) return fail(EAS_ERR_WORKSPACE, "workspace %zu < %zu", ws_bytes, need);
   DevInfo di;

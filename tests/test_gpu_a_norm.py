@@ -269,6 +269,15 @@ def test_autograd():
     assert (x3.grad == 1).all()
 
 
+def test_second_derivatives_are_refused():
+    x, w, _, _ = problem(3, 64, "fp32", False, None)
+    x.requires_grad_()
+    y, _, _, _ = eas.fused_rmsnorm(x, w)
+    g, = torch.autograd.grad(y.square().sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError, match="once_differentiable"):
+        g.sum().backward()
+
+
 def test_other_stream_and_graph():
     x, w, r, m = problem(64, 1024, "bf16", True, "some", seed=8)
     want = eas.rmsnorm_fwd(x, w, EPS, r, m, want_e4m3=True)

@@ -9,35 +9,38 @@ import torch
 import entropy_active_span_gb300 as eas
 from entropy_active_span_gb300 import _lib
 
-P = 256          # a fake, aligned address
+P = 256          # a fake, aligned address, and others far from it
+A, B, C, D, E, F = (P + (i << 20) for i in range(1, 7))
 BIG = 1 << 40
 INVALID, WORKSPACE = _lib.EAS_ERR_INVALID_ARG, _lib.EAS_ERR_WORKSPACE
 
 
-def norm_fwd(lib, x=P, r=P, w=P, mask=P, R=4, H=64, dtype=_lib.EAS_BF16, eps=1e-6, s=P, y=2 * P,
-             q=P, scale=P):
+def norm_fwd(lib, x=A, r=B, w=P, mask=P, R=4, H=64, dtype=_lib.EAS_BF16, eps=1e-6, s=C, y=D,
+             q=E, scale=F):
     return lib.eas_rmsnorm_fwd(x, r, w, mask, R, H, dtype, eps, s, y, q, scale, None)
 
 
 @pytest.mark.parametrize("bad", [
     dict(R=-1), dict(H=0), dict(H=(1 << 20) + 1), dict(dtype=_lib.EAS_E4M3), dict(eps=0.0),
     dict(eps=-1.0), dict(eps=float("nan")), dict(eps=float("inf")), dict(x=None), dict(w=None),
-    dict(q=None), dict(scale=None), dict(r=None), dict(x=P + 8), dict(r=P + 2), dict(w=P + 4),
-    dict(y=P + 8), dict(q=P + 1), dict(s=P + 8), dict(y=P), dict(s=None, y=None, q=None, scale=None),
+    dict(q=None), dict(scale=None), dict(r=None), dict(x=A + 8), dict(r=B + 2), dict(w=P + 4),
+    dict(y=D + 8), dict(q=E + 1), dict(s=C + 8), dict(s=None, y=None, q=None, scale=None),
+    dict(y=A), dict(y=B + 16), dict(y=C), dict(q=A + 496), dict(q=C), dict(q=D + 16),
+    dict(s=A + 64), dict(s=B - 64),
 ])
 def test_rmsnorm_fwd_refuses(libeas, bad):
     assert norm_fwd(libeas, **bad) == INVALID
 
 
-def norm_bwd(lib, dy=P, s=P, w=P, ds=P, mask=P, R=4, H=64, dtype=_lib.EAS_BF16, eps=1e-6,
-             dx=2 * P, dw=P, ws=P, ws_bytes=BIG):
+def norm_bwd(lib, dy=A, s=B, w=P, ds=C, mask=P, R=4, H=64, dtype=_lib.EAS_BF16, eps=1e-6,
+             dx=D, dw=E, ws=F, ws_bytes=BIG):
     return lib.eas_rmsnorm_bwd(dy, s, w, ds, mask, R, H, dtype, eps, dx, dw, ws, ws_bytes, None)
 
 
 @pytest.mark.parametrize("bad", [
     dict(R=-1), dict(H=0), dict(dtype=7), dict(eps=0.0), dict(dy=None), dict(s=None), dict(w=None),
-    dict(dx=None), dict(dw=None), dict(ws=None), dict(dy=P + 8), dict(s=P + 4), dict(ds=P + 8),
-    dict(dx=P + 8), dict(dw=P + 4), dict(ws=P + 16), dict(dx=P),
+    dict(dx=None), dict(dw=None), dict(ws=None), dict(dy=A + 8), dict(s=B + 4), dict(ds=C + 8),
+    dict(dx=D + 8), dict(dw=E + 4), dict(ws=F + 16), dict(dx=A), dict(dx=B + 64), dict(dx=C + 64),
 ])
 def test_rmsnorm_bwd_refuses(libeas, bad):
     assert norm_bwd(libeas, **bad) == INVALID
@@ -45,30 +48,30 @@ def test_rmsnorm_bwd_refuses(libeas, bad):
     assert norm_bwd(libeas, ws_bytes=need - 1) == WORKSPACE
 
 
-def embed_fwd(lib, ids=P, table=P, T=4, H=64, V=10, dtype=_lib.EAS_BF16, scale=1.0, out=2 * P,
-              ws=P, ws_bytes=64):
+def embed_fwd(lib, ids=P, table=A, T=4, H=64, V=10, dtype=_lib.EAS_BF16, scale=1.0, out=B,
+              ws=C, ws_bytes=64):
     return lib.eas_embed_fwd(ids, table, T, H, V, dtype, scale, out, ws, ws_bytes, None)
 
 
 @pytest.mark.parametrize("bad", [
     dict(T=-1), dict(H=0), dict(V=0), dict(V=1 << 31), dict(dtype=_lib.EAS_E4M3),
     dict(scale=float("nan")), dict(ids=None), dict(table=None), dict(out=None), dict(ids=P + 2),
-    dict(table=P + 8), dict(out=P + 8), dict(ws=P + 8), dict(out=P),
+    dict(table=A + 8), dict(out=B + 8), dict(ws=C + 8), dict(out=A), dict(out=A + 1264),
 ])
 def test_embed_fwd_refuses(libeas, bad):
     assert embed_fwd(libeas, **bad) == INVALID
     assert embed_fwd(libeas, ws_bytes=8) == WORKSPACE
 
 
-def embed_bwd(lib, ids=P, dout=P, T=4, H=64, V=10, dtype=_lib.EAS_BF16, scale=1.0, accumulate=0,
-              dw=P, ws=P, ws_bytes=BIG):
+def embed_bwd(lib, ids=P, dout=A, T=4, H=64, V=10, dtype=_lib.EAS_BF16, scale=1.0, accumulate=0,
+              dw=B, ws=C, ws_bytes=BIG):
     return lib.eas_embed_bwd(ids, dout, T, H, V, dtype, scale, accumulate, dw, ws, ws_bytes, None)
 
 
 @pytest.mark.parametrize("bad", [
     dict(T=-1), dict(H=0), dict(V=0), dict(dtype=_lib.EAS_E4M3), dict(scale=float("inf")),
     dict(accumulate=2), dict(ids=None), dict(dout=None), dict(dw=None), dict(ws=None),
-    dict(ids=P + 1), dict(dout=P + 8), dict(dw=P + 8), dict(ws=P + 16),
+    dict(ids=P + 1), dict(dout=A + 8), dict(dw=B + 8), dict(ws=C + 16), dict(dw=A + 496),
 ])
 def test_embed_bwd_refuses(libeas, bad):
     assert embed_bwd(libeas, **bad) == INVALID
