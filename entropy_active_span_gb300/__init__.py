@@ -639,7 +639,7 @@ def clip_grad_norm(grads, max_norm: float | None, out=None, ws=None, norm=None):
     2-norm over all of them, and returns norm (fp32 [1], on the device).
 
     grads: contiguous bf16 or fp32 tensors.  out: None scales in place; else one
-    tensor for each gradient, of its shape, bf16 or fp32 (an fp32 gradient
+    tensor for each gradient, of its size, bf16 or fp32 (an fp32 gradient
     clipped into the bf16 one that an optimiser reads).  max_norm None computes
     the norm alone.  Where the norm is not finite nothing is scaled."""
     grads = list(grads)
@@ -656,15 +656,14 @@ def clip_grad_norm(grads, max_norm: float | None, out=None, ws=None, norm=None):
     dev, index = grads[0].device, grads[0].get_device()
     if not (all(map(T.is_contiguous, grads)) and set(map(T.get_device, grads)) == {index}):
         raise ValueError(f"gradients must be contiguous and on one device ({dev})")
-    ptrs = array("Q", map(T.data_ptr, grads))
+    ptrs, numels = array("Q", map(T.data_ptr, grads)), array("q", map(T.numel, grads))
     out_codes, out_ptrs = codes, ptrs
     if out is not None:
         out_codes = _row_codes(outs, "out")
         if not (all(map(T.is_contiguous, outs)) and set(map(T.get_device, outs)) == {index}
-                and [g.shape for g in grads] == [o.shape for o in outs]):
-            raise ValueError("out must be contiguous and have the gradients' shapes and device")
+                and numels == array("q", map(T.numel, outs))):
+            raise ValueError("out must be contiguous and have the gradients' sizes and device")
         out_ptrs = array("Q", map(T.data_ptr, outs))
-    numels = array("q", map(T.numel, grads))
     if norm is None:
         norm = torch.empty(1, dtype=torch.float32, device=dev)
     else:

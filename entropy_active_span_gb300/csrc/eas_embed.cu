@@ -887,7 +887,7 @@ cudaError_t launch_embed_bwd(const EmbedBwdArgs& a, int is_bf16, int num_sms, cu
   cudaError_t e;
   if (is_bf16) e = aligned ? sum_t<__nv_bfloat16, 8>(s, st) : sum_t<__nv_bfloat16, 1>(s, st);
   else e = aligned ? sum_t<float, 4>(s, st) : sum_t<float, 1>(s, st);
-  if (e != cudaSuccess || s.n_chunks <= 1) return e;
+  if (e != cudaSuccess || s.n_chunks <= 2) return e;   // no run of three chunks
   const int w = a.H % 4 == 0 ? 4 : 1;
   const long long most = static_cast<long long>(s.n_chunks) * ((a.H + 32 * w - 1) / (32 * w));
   // an item is a chain of latencies, so as many at a time as there may be
