@@ -759,7 +759,10 @@ struct RingShape {
 // About 512 threads an SM, two or four vectors each: the backward of [65536,
 // 8192] bf16 with ds took 742 us with one row by 1024 threads of one vector and
 // 600 by 512 of two.  Three rows deep: 600 us against 630 with two and 639 with
-// four; at [65536, 4096] fp32 477 against 508 and 525.
+// four; at [65536, 4096] fp32 477 against 508 and 525.  Rows of up to 96 vectors
+// lie within warps, in lanes that they fill best: the backward of [131072, 320]
+// bf16 with ds 59 us on 16 lanes of three vectors against 76 on 32 of two; above
+// that a CTA of 64 lanes does better ([131072, 1024]: 170 against 180).
 RingShape ring_shape(int H, int esize, int arrays) {
   RingShape r = {};
   const int vec = 16 / esize;
@@ -767,9 +770,9 @@ RingShape ring_shape(int H, int esize, int arrays) {
   const int n = r.odd ? (H + 2 * vec - 2) / vec : H / vec;   // vectors that cover a row anywhere
   if (n > 2048) return r;
   r.groups = 1;
-  if (n <= 128) {                       // rows within warps
-    r.nv = n <= 64 ? 2 : 4;
-    r.lanes = n <= 16 ? 8 : n <= 32 ? 16 : 32;
+  if (n <= 96) {                        // rows within warps: the lanes that n fills best
+    r.lanes = n <= 24 ? 8 : n <= 48 ? 16 : 32;
+    r.nv = n <= 2 * r.lanes ? 2 : 3;
     r.groups = 32 * kShortWarps / r.lanes;
   } else {
     r.nv = n <= 1024 ? 2 : 4;
@@ -806,7 +809,7 @@ template <typename T, bool kOdd>
 cudaError_t fwd_rows(const RmsNormFwdArgs& a, const RingShape& r, cudaStream_t s, int batch,
                      unsigned g) {
   if (r.groups > 1)
-    return r.nv == 2 ? fwd_kind<T, 2, true, kOdd>(a, r, s, batch, g) : fwd_kind<T, 4, true, kOdd>(a, r, s, batch, g);
+    return r.nv == 2 ? fwd_kind<T, 2, true, kOdd>(a, r, s, batch, g) : fwd_kind<T, 3, true, kOdd>(a, r, s, batch, g);
   return r.nv == 2 ? fwd_kind<T, 2, false, kOdd>(a, r, s, batch, g) : fwd_kind<T, 4, false, kOdd>(a, r, s, batch, g);
 }
 
@@ -836,8 +839,6 @@ cudaError_t fwd_t(const RmsNormFwdArgs& a, int num_sms, cudaStream_t s) {
 
 template <typename T, int NV, int S, bool kOdd>
 cudaError_t bwd_kind(const RmsNormBwdArgs& a, const RingShape& r, unsigned g, cudaStream_t s) {
-  if (r.groups > 1)
-    return ring_launch(rmsnorm_bwd_ring_kernel<T, NV, S, true, kOdd, false, false>, r, g, s, a);
   if (a.ds)
     return a.mask ? ring_launch(rmsnorm_bwd_ring_kernel<T, NV, S, false, kOdd, true, true>, r, g, s, a)
                   : ring_launch(rmsnorm_bwd_ring_kernel<T, NV, S, false, kOdd, true, false>, r, g, s, a);
@@ -845,8 +846,17 @@ cudaError_t bwd_kind(const RmsNormBwdArgs& a, const RingShape& r, unsigned g, cu
                 : ring_launch(rmsnorm_bwd_ring_kernel<T, NV, S, false, kOdd, false, false>, r, g, s, a);
 }
 
+template <typename T, int NV, int S, bool kOdd>
+cudaError_t bwd_short(const RmsNormBwdArgs& a, const RingShape& r, unsigned g, cudaStream_t s) {
+  return ring_launch(rmsnorm_bwd_ring_kernel<T, NV, S, true, kOdd, false, false>, r, g, s, a);
+}
+
 template <typename T, bool kOdd>
 cudaError_t bwd_rows(const RmsNormBwdArgs& a, const RingShape& r, unsigned g, cudaStream_t s) {
+  if (r.groups > 1) {
+    if (r.nv == 2) return bwd_short<T, 2, 3, kOdd>(a, r, g, s);
+    return r.stages == 2 ? bwd_short<T, 3, 2, kOdd>(a, r, g, s) : bwd_short<T, 3, 3, kOdd>(a, r, g, s);
+  }
   if (r.nv == 2) return bwd_kind<T, 2, 3, kOdd>(a, r, g, s);   // 512 threads an SM: always three deep
   return r.stages == 2 ? bwd_kind<T, 4, 2, kOdd>(a, r, g, s) : bwd_kind<T, 4, 3, kOdd>(a, r, g, s);
 }
