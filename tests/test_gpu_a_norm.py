@@ -74,7 +74,8 @@ def check_fwd(x, w, r, m, y, q, scale, s):
 
 SHAPES = [(1, 1), (3, 7), (1, 128), (5, 128), (2, 320), (37, 1003), (9, 1088), (130, 4096),
           (3, 8192), (2, 8191), (3, 16384), (2, 32768), (2, 32776), (1, 40001),
-          (1300, 100), (1300, 101), (700, 2047), (650, 2052), (320, 8189), (20000, 33), (9000, 128)]
+          (1300, 100), (1300, 101), (700, 2047), (650, 2052), (320, 8189), (20000, 33), (9000, 128),
+          (900, 150), (700, 333), (1100, 601), (800, 192)]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
