@@ -16,6 +16,7 @@
 // 7168] 785 us, both 6.8 TB/s; the plain copy rate is 6.8.
 #include "eas_device.cuh"
 #include "eas_kernels.h"
+#include "eas_launch.cuh"
 #include "eas_vec.cuh"
 
 namespace eas {
@@ -816,8 +817,7 @@ template <int kRounds>
 static cudaError_t cluster_sort(const ClusterSort& p, cudaStream_t s) {
   const int smem = kClusterThreads * kRounds * static_cast<int>(sizeof(int2)) +
                    kClusterWarps * kSortBins * static_cast<int>(sizeof(short));
-  const cudaError_t e = cudaFuncSetAttribute(cluster_sort_kernel<kRounds>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  const cudaError_t e = allow_smem<cluster_sort_kernel<kRounds>>(smem);
   if (e != cudaSuccess) return e;
   cluster_sort_kernel<kRounds><<<kClusterCtas, kClusterThreads, smem, s>>>(p);
   return cudaGetLastError();

@@ -20,6 +20,7 @@
 
 #include "eas_device.cuh"
 #include "eas_kernels.h"
+#include "eas_launch.cuh"
 #include "eas_vec.cuh"
 
 namespace eas {
@@ -786,12 +787,16 @@ RingShape ring_shape(int H, int esize, int arrays) {
   return r;
 }
 
-template <typename K, typename... A>
-cudaError_t ring_launch(K kernel, const RingShape& r, unsigned grid, cudaStream_t s, A... args) {
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             static_cast<int>(r.smem));
+// The most shared memory that ring_shape asks for: three stages fit 200 KB on all
+// of an SM's CTAs, and two of the largest (three arrays of 2048 vectors) take 192.
+constexpr int kRingBytes = 200 << 10;
+
+template <auto kKernel, typename... A>
+cudaError_t ring_launch(const RingShape& r, unsigned grid, cudaStream_t s, A... args) {
+  if (r.smem > kRingBytes) return cudaErrorInvalidValue;
+  const cudaError_t e = allow_smem<kKernel>(kRingBytes);
   if (e != cudaSuccess) return e;
-  kernel<<<grid, dim3(r.lanes, r.groups), r.smem, s>>>(args...);
+  kKernel<<<grid, dim3(r.lanes, r.groups), r.smem, s>>>(args...);
   return cudaGetLastError();
 }
 
@@ -799,10 +804,10 @@ template <typename T, int NV, bool kShort, bool kOdd>
 cudaError_t fwd_kind(const RmsNormFwdArgs& a, const RingShape& r, cudaStream_t s, int batch,
                      unsigned g) {
   if (a.r)
-    return a.mask ? ring_launch(rmsnorm_fwd_ring_kernel<T, NV, 3, kShort, kOdd, true, true>, r, g, s, a, batch)
-                  : ring_launch(rmsnorm_fwd_ring_kernel<T, NV, 3, kShort, kOdd, true, false>, r, g, s, a, batch);
-  return a.mask ? ring_launch(rmsnorm_fwd_ring_kernel<T, NV, 3, kShort, kOdd, false, true>, r, g, s, a, batch)
-                : ring_launch(rmsnorm_fwd_ring_kernel<T, NV, 3, kShort, kOdd, false, false>, r, g, s, a, batch);
+    return a.mask ? ring_launch<rmsnorm_fwd_ring_kernel<T, NV, 3, kShort, kOdd, true, true>>(r, g, s, a, batch)
+                  : ring_launch<rmsnorm_fwd_ring_kernel<T, NV, 3, kShort, kOdd, true, false>>(r, g, s, a, batch);
+  return a.mask ? ring_launch<rmsnorm_fwd_ring_kernel<T, NV, 3, kShort, kOdd, false, true>>(r, g, s, a, batch)
+                : ring_launch<rmsnorm_fwd_ring_kernel<T, NV, 3, kShort, kOdd, false, false>>(r, g, s, a, batch);
 }
 
 template <typename T, bool kOdd>
@@ -840,15 +845,15 @@ cudaError_t fwd_t(const RmsNormFwdArgs& a, int num_sms, cudaStream_t s) {
 template <typename T, int NV, int S, bool kOdd>
 cudaError_t bwd_kind(const RmsNormBwdArgs& a, const RingShape& r, unsigned g, cudaStream_t s) {
   if (a.ds)
-    return a.mask ? ring_launch(rmsnorm_bwd_ring_kernel<T, NV, S, false, kOdd, true, true>, r, g, s, a)
-                  : ring_launch(rmsnorm_bwd_ring_kernel<T, NV, S, false, kOdd, true, false>, r, g, s, a);
-  return a.mask ? ring_launch(rmsnorm_bwd_ring_kernel<T, NV, S, false, kOdd, false, true>, r, g, s, a)
-                : ring_launch(rmsnorm_bwd_ring_kernel<T, NV, S, false, kOdd, false, false>, r, g, s, a);
+    return a.mask ? ring_launch<rmsnorm_bwd_ring_kernel<T, NV, S, false, kOdd, true, true>>(r, g, s, a)
+                  : ring_launch<rmsnorm_bwd_ring_kernel<T, NV, S, false, kOdd, true, false>>(r, g, s, a);
+  return a.mask ? ring_launch<rmsnorm_bwd_ring_kernel<T, NV, S, false, kOdd, false, true>>(r, g, s, a)
+                : ring_launch<rmsnorm_bwd_ring_kernel<T, NV, S, false, kOdd, false, false>>(r, g, s, a);
 }
 
 template <typename T, int NV, int S, bool kOdd>
 cudaError_t bwd_short(const RmsNormBwdArgs& a, const RingShape& r, unsigned g, cudaStream_t s) {
-  return ring_launch(rmsnorm_bwd_ring_kernel<T, NV, S, true, kOdd, false, false>, r, g, s, a);
+  return ring_launch<rmsnorm_bwd_ring_kernel<T, NV, S, true, kOdd, false, false>>(r, g, s, a);
 }
 
 template <typename T, bool kOdd>
