@@ -172,20 +172,20 @@ grad_squares_kernel(const __grid_constant__ List<N> l, double* partial) {
   if (threadIdx.x == 0) partial[blockIdx.x] = sum;
 }
 
-// The norm from the partial sums, the same to the bit in whatever CTA asks.
-__device__ __forceinline__ float norm_of(const double* partial, int n, double* sm) {
+// The sum of squares from the partial sums, the same to the bit in whatever CTA asks.
+__device__ __forceinline__ double squares_of(const double* partial, int n, double* sm) {
   double acc = 0.0;
   for (int i = threadIdx.x; i < n; i += kThreads) acc += partial[i];
-  return static_cast<float>(sqrt(block_sum(acc, sm)));
+  return block_sum(acc, sm);
 }
 
 __global__ void __launch_bounds__(kThreads)
 grad_norm_kernel(const double* partial, int n, float* norm, DevStatus* st) {
   __shared__ double sm[kThreads / 32];
   wait_for_launch_before();
-  const float v = norm_of(partial, n, sm);
+  const double sum = squares_of(partial, n, sm);
   if (threadIdx.x == 0) {
-    *norm = v;
+    *norm = static_cast<float>(sqrt(sum));
     *st = DevStatus{};   // nothing here can fail on the device
   }
 }
@@ -237,16 +237,25 @@ __global__ void __launch_bounds__(kThreads)
 grad_clip_kernel(const __grid_constant__ List<N> l, const double* partial, int n_partial,
                  float* norm, float max_norm, DevStatus* st) {
   __shared__ double sm[kThreads / 32];
+  __shared__ float factor;
   // the first chunk's tensor is looked up while the norm is on its way
   int k = l.n_chunks - 1 - blockIdx.x;
   int t = tensor_of(l, k);
   wait_for_launch_before();
-  const float v = norm_of(partial, n_partial, sm);
-  if (blockIdx.x == 0 && threadIdx.x == 0) {
-    *norm = v;
-    *st = DevStatus{};
+  const double sum = squares_of(partial, n_partial, sm);
+  if (threadIdx.x == 0) {
+    // norm and factor in 64 bits, each rounded once: an error in the factor would
+    // be every gradient's
+    const double v = sqrt(sum);
+    const float rounded = static_cast<float>(v);
+    factor = isfinite(rounded) ? static_cast<float>(fmin(1.0, max_norm / (v + 1e-6))) : 1.f;
+    if (blockIdx.x == 0) {
+      *norm = rounded;
+      *st = DevStatus{};
+    }
   }
-  const float c = isfinite(v) ? fminf(1.f, max_norm / (v + 1e-6f)) : 1.f;
+  __syncthreads();
+  const float c = factor;
   // from the last chunk down: what the norm read last is still in L2
   for (; k >= 0; k -= gridDim.x, t = k >= 0 ? tensor_of(l, k) : 0) {
     if (c == 1.f && l.in[t] == l.out[t]) continue;   // in place: nothing changes

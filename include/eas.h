@@ -446,7 +446,8 @@ eas_status eas_embed_bwd(const int32_t* ids, const void* dout, int64_t T, int64_
  *   norm = sqrt(sum over all tensors of g^2),
  *   c = min(1, max_norm / (norm + 1e-6)),  out = c * g.
  * Where the norm is not finite, c = 1: the caller sees the norm and skips its
- * step.  Squares are added in fp32 over 32 elements and in about 48 bits beyond
+ * step.  norm and c are each rounded to fp32 once; squares are added in fp32 over
+ * 32 elements and in about 48 bits beyond
  * (fp64 where they leave fp32's range), in a fixed order.
  *
  *   grads, outs, numels, dtypes, out_dtypes : HOST arrays of n entries, copied
