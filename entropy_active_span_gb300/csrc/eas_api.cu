@@ -6,81 +6,21 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
-#include <algorithm>
-#include <atomic>
-#include <cmath>
-#include <cstdarg>
-#include <cstdio>
 #include <cstdlib>
 #include <cstring>
-#include <deque>
-#include <initializer_list>
 #include <mutex>
-#include <new>
-#include <vector>
 
 #include "../../include/eas.h"
 #include "eas_device.cuh"
+#include "eas_host.h"
 #include "eas_kernels.h"
 
 using namespace eas;
 
 namespace {
 
-thread_local char g_err[512] = "";
-
-eas_status fail(eas_status s, const char* fmt, ...) {
-  va_list ap;
-  va_start(ap, fmt);
-  vsnprintf(g_err, sizeof(g_err), fmt, ap);
-  va_end(ap);
-  return s;
-}
-
-eas_status cuda_fail(cudaError_t e, const char* what) {
-  return fail(EAS_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
-}
-
-#define EAS_CUDA(call, what)                  \
-  do {                                        \
-    cudaError_t e_ = (call);                  \
-    if (e_ != cudaSuccess) return cuda_fail(e_, what); \
-  } while (0)
-
 inline long long round_up(long long x, long long m) { return (x + m - 1) / m * m; }
 inline long long cdiv(long long x, long long m) { return (x + m - 1) / m; }
-
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-// ------------------------------------------------------------ device info
-
-struct DevInfo {
-  int sms = 0;
-  int major = 0, minor = 0;
-};
-
-eas_status device_info(DevInfo* out) {
-  static std::mutex mu;
-  static DevInfo cache[64];
-  static bool have[64] = {};
-  int dev = 0;
-  EAS_CUDA(cudaGetDevice(&dev), "cudaGetDevice");
-  if (dev < 0 || dev >= 64) return fail(EAS_ERR_UNSUPPORTED, "device ordinal %d", dev);
-  std::lock_guard<std::mutex> lk(mu);
-  if (!have[dev]) {
-    DevInfo d;
-    EAS_CUDA(cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev), "sm count");
-    EAS_CUDA(cudaDeviceGetAttribute(&d.major, cudaDevAttrComputeCapabilityMajor, dev), "cc");
-    EAS_CUDA(cudaDeviceGetAttribute(&d.minor, cudaDevAttrComputeCapabilityMinor, dev), "cc");
-    cache[dev] = d;
-    have[dev] = true;
-  }
-  *out = cache[dev];
-  if (out->major != 10 || out->minor != 3)
-    return fail(EAS_ERR_UNSUPPORTED, "built for sm_103a; device is sm_%d%d", out->major,
-                out->minor);
-  return EAS_OK;
-}
 
 long long wait_budget() {
   static long long b = [] {
@@ -90,72 +30,6 @@ long long wait_budget() {
   }();
   return b;
 }
-
-// ------------------------------------------------------------ tracing
-//
-// When enabled, every kernel launch of the library is bracketed by a pair of
-// CUDA events on its stream, tagged with the kernel's kind; eas_trace_read()
-// returns the durations.  Off by default; meant for eager (not captured)
-// launches.  Backward tensor-core launches are named by their jobs:
-// dlogits_gemm_tc (d-logits of chunk 0), bwd_chunk_gemm_tc (dW and dHidden of
-// chunk c-1 with the d-logits of chunk c), dproj_gemm_tc (dW and dHidden of
-// the last chunk); the e4m3 backward runs dlogits_gemm_tc_e4m3 (d-logits of a
-// chunk) and dproj_gemm_tc (dW and dHidden of that chunk) per chunk.
-
-enum TraceKind : int {
-  kTrSpans = 0, kTrRowmap, kTrGather, kTrFwdGemm, kTrCombine, kTrZeroRows,
-  kTrDLogitsGemm, kTrDProjGemm, kTrUnused, kTrSimtFwd, kTrSimtDLogits,
-  kTrSimtDHidden, kTrSimtDWeight, kTrMemset, kTrBwdChunkGemm, kTrDLogitsFp8Gemm,
-  kTrNormFwd, kTrNormBwd, kTrNormDw, kTrEmbedFwd, kTrEmbedSort, kTrEmbedBwd, kTrGradNorm,
-  kTrGradClip, kTrCount
-};
-
-const char* const kTraceNames[kTrCount] = {
-    "spans_build", "rowmap", "gather_rows", "fwd_gemm_tc", "combine", "zero_rows",
-    "dlogits_gemm_tc", "dproj_gemm_tc", "unused", "fwd_gemm_simt",
-    "dlogits_gemm_simt", "dhidden_gemm_simt", "dweight_gemm_simt", "memset",
-    "bwd_chunk_gemm_tc", "dlogits_gemm_tc_e4m3",
-    "rmsnorm_fwd", "rmsnorm_bwd", "rmsnorm_dweight", "embed_fwd", "embed_sort", "embed_bwd",
-    "grad_norm", "clip_grad_norm"};
-
-struct TraceRec {
-  int kind;
-  cudaEvent_t a, b;
-};
-
-std::mutex g_trace_mu;
-std::atomic<bool> g_trace_on{false};   // read unlocked on every launch
-std::deque<TraceRec> g_trace_pool;    // events are created once and reused; a deque
-                                      // keeps records in place as it grows
-size_t g_trace_used = 0;
-
-class Trace {
- public:
-  Trace(int kind, cudaStream_t s) : s_(s) {
-    if (!g_trace_on.load(std::memory_order_relaxed)) return;
-    std::lock_guard<std::mutex> lk(g_trace_mu);
-    if (!g_trace_on.load(std::memory_order_relaxed)) return;
-    if (g_trace_used == g_trace_pool.size()) {
-      TraceRec r{kind, nullptr, nullptr};
-      if (cudaEventCreate(&r.a) != cudaSuccess) return;
-      if (cudaEventCreate(&r.b) != cudaSuccess) {
-        cudaEventDestroy(r.a);
-        return;
-      }
-      g_trace_pool.push_back(r);
-    }
-    rec_ = &g_trace_pool[g_trace_used++];
-    rec_->kind = kind;
-    cudaEventRecord(rec_->a, s_);
-  }
-  ~Trace() {
-    if (rec_) cudaEventRecord(rec_->b, s_);
-  }
-
- private:
-  cudaStream_t s_;
-  TraceRec* rec_ = nullptr;
-};
 
 // ------------------------------------------------------------ tensor maps
 
@@ -235,8 +109,6 @@ eas_status make_map_u8(CUtensorMap* m, const void* base, long long cols, long lo
   return make_map_2d(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, base, cols, rows, ld, box_rows);
 }
 
-size_t elem_size(eas_dtype dt) { return dt == EAS_BF16 ? 2 : dt == EAS_E4M3 ? 1 : 4; }
-
 // ---------------------------------------------------------- workspace layout
 
 struct Layout {
@@ -252,8 +124,6 @@ struct Layout {
   size_t dz, dz2, acc, counters;                  // backward part (two staging buffers)
   size_t fwd_end, bwd_end, total;
 };
-
-size_t align_up(size_t x) { return (x + 1023) / 1024 * 1024; }
 
 Layout layout(long long T, long long H, long long V, eas_dtype dt, long long chunk) {
   Layout L;
@@ -307,11 +177,6 @@ struct Fp8Operands {
   const uint8_t* weight;   // [V, H] codes
   const float* wscale;     // [V]
 };
-
-template <typename T>
-T* at(void* ws, size_t off) {
-  return reinterpret_cast<T*>(static_cast<char*>(ws) + off);
-}
 
 eas_status check_shape(long long T, long long H, long long V, eas_dtype dt) {
   if (T < 0 || T > 0x7fffff00LL) return fail(EAS_ERR_INVALID_ARG, "T=%lld out of range", T);
@@ -995,298 +860,6 @@ eas_status eas_selftest_wait_timeout(int64_t budget_cycles, void* ws, size_t ws_
   return EAS_OK;
 }
 
-// ------------------------------------------------ operators around the LM head
-
-// Whether [a, a + na) and [b, b + nb) share a byte (null shares none).
-static bool overlap(const void* a, size_t na, const void* b, size_t nb) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return x && y && na && nb && x < y + nb && y < x + na;
-}
-
-// The same for two buffers of n bytes of which one may replace the other.
-static bool overlap_partly(const void* a, const void* b, size_t n) { return a != b && overlap(a, n, b, n); }
-
-// Shape and type of the row operators: any H (odd ones keep their vectors on
-// 16-byte boundaries in memory).
-static eas_status check_rows(long long R, long long H, eas_dtype dt) {
-  if (R < 0 || R > 0x7fffff00LL) return fail(EAS_ERR_INVALID_ARG, "rows=%lld out of range", R);
-  if (H < 1 || H > (1LL << 20)) return fail(EAS_ERR_INVALID_ARG, "H=%lld out of range", H);
-  if (dt != EAS_BF16 && dt != EAS_FP32) return fail(EAS_ERR_INVALID_ARG, "dtype %d", (int)dt);
-  return EAS_OK;
-}
-
-eas_status eas_rmsnorm_fwd(const void* x, const void* residual, const void* weight,
-                           const uint8_t* mask, int64_t R, int64_t H, eas_dtype dtype, float eps,
-                           void* sum_out, void* y, uint8_t* y_e4m3, float* y_scale, void* stream) {
-  eas_status st = check_rows(R, H, dtype);
-  if (st != EAS_OK) return st;
-  if (!(eps > 0.f) || !std::isfinite(eps)) return fail(EAS_ERR_INVALID_ARG, "eps must be positive");
-  if (!weight || (R > 0 && !x)) return fail(EAS_ERR_INVALID_ARG, "null pointer");
-  if ((y_e4m3 == nullptr) != (y_scale == nullptr))
-    return fail(EAS_ERR_INVALID_ARG, "y_e4m3 and y_scale come together");
-  if (sum_out && !residual) return fail(EAS_ERR_INVALID_ARG, "sum_out needs a residual");
-  if (R > 0 && !y && !y_e4m3 && !sum_out) return fail(EAS_ERR_INVALID_ARG, "no output");
-  if (!aligned(x, 16) || !aligned(residual, 16) || !aligned(weight, 16) || !aligned(sum_out, 16) ||
-      !aligned(y, 16) || !aligned(y_e4m3, 16) || !aligned(y_scale, 4))
-    return fail(EAS_ERR_INVALID_ARG, "tensors must be 16-byte aligned");
-  const size_t codes = static_cast<size_t>(R) * static_cast<size_t>(H), rows = codes * elem_size(dtype);
-  for (const void* in : {x, residual, static_cast<const void*>(sum_out)})
-    if (overlap(y, rows, in, rows) || overlap(y_e4m3, codes, in, rows))
-      return fail(EAS_ERR_INVALID_ARG, "y and y_e4m3 must not overlap x, residual or sum_out");
-  if (overlap(y, rows, y_e4m3, codes) || overlap_partly(sum_out, x, rows) ||
-      overlap_partly(sum_out, residual, rows))
-    return fail(EAS_ERR_INVALID_ARG, "an output overlaps another buffer");
-  DevInfo di;
-  st = device_info(&di);
-  if (st != EAS_OK) return st;
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const RmsNormFwdArgs a = {x, residual, weight, mask, sum_out, y, y_e4m3, y_scale,
-                            R, static_cast<int>(H), eps};
-  Trace tr_(kTrNormFwd, s);
-  EAS_CUDA(launch_rmsnorm_fwd(a, dtype == EAS_BF16, di.sms, s), "rmsnorm_fwd");
-  return EAS_OK;
-}
-
-static size_t norm_bwd_rstd_offset(long long R, long long H) {
-  return align_up(sizeof(DevStatus)) + align_up(4 * static_cast<size_t>(rmsnorm_bwd_partials(R, H)) * static_cast<size_t>(H));
-}
-
-size_t eas_rmsnorm_bwd_workspace_size(int64_t R, int64_t H) {
-  if (R < 0 || H < 1) return 0;
-  return norm_bwd_rstd_offset(R, H) + align_up(4 * static_cast<size_t>(R));
-}
-
-eas_status eas_rmsnorm_bwd(const void* dy, const void* sum, const void* weight, const void* ds,
-                           const uint8_t* mask, int64_t R, int64_t H, eas_dtype dtype, float eps,
-                           void* dx, float* dweight, void* ws, size_t ws_bytes, void* stream) {
-  eas_status st = check_rows(R, H, dtype);
-  if (st != EAS_OK) return st;
-  if (!(eps > 0.f) || !std::isfinite(eps)) return fail(EAS_ERR_INVALID_ARG, "eps must be positive");
-  if (!weight || !dweight || !ws || (R > 0 && (!dy || !sum || !dx)))
-    return fail(EAS_ERR_INVALID_ARG, "null pointer");
-  if (!aligned(dy, 16) || !aligned(sum, 16) || !aligned(weight, 16) || !aligned(ds, 16) ||
-      !aligned(dx, 16) || !aligned(dweight, 16) || !aligned(ws, 256))
-    return fail(EAS_ERR_INVALID_ARG, "tensors must be 16-byte and ws 256-byte aligned");
-  const size_t rows = static_cast<size_t>(R) * static_cast<size_t>(H) * elem_size(dtype);
-  if (overlap(dx, rows, dy, rows) || overlap(dx, rows, sum, rows) || overlap_partly(dx, ds, rows))
-    return fail(EAS_ERR_INVALID_ARG, "dx must not overlap dy or s, nor ds in part");
-  const size_t need = eas_rmsnorm_bwd_workspace_size(R, H);
-  if (ws_bytes < need) return fail(EAS_ERR_WORKSPACE, "workspace %zu < %zu", ws_bytes, need);
-  DevInfo di;
-  st = device_info(&di);
-  if (st != EAS_OK) return st;
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const RmsNormBwdArgs a = {dy, sum, weight, ds, mask, dx, at<float>(ws, align_up(sizeof(DevStatus))),
-                            at<float>(ws, norm_bwd_rstd_offset(R, H)), R, static_cast<int>(H), eps};
-  int n = 0;
-  {
-    Trace tr_(kTrNormBwd, s);
-    EAS_CUDA(launch_rmsnorm_bwd(a, dtype == EAS_BF16, di.sms, &n, s), "rmsnorm_bwd");
-  }
-  {
-    Trace tr_(kTrNormDw, s);
-    EAS_CUDA(launch_rmsnorm_dw(a.partial, n, a.H, dweight, static_cast<DevStatus*>(ws), s), "rmsnorm_dweight");
-  }
-  return EAS_OK;
-}
-
-static eas_status check_embed(long long T, long long H, long long V, eas_dtype dt, float scale) {
-  eas_status st = check_rows(T, H, dt);
-  if (st != EAS_OK) return st;
-  if (V < 1 || V > 0x7fffff00LL) return fail(EAS_ERR_INVALID_ARG, "V=%lld out of range", V);
-  if (!std::isfinite(scale)) return fail(EAS_ERR_INVALID_ARG, "scale must be finite");
-  return EAS_OK;
-}
-
-eas_status eas_embed_fwd(const int32_t* ids, const void* table, int64_t T, int64_t H, int64_t V,
-                         eas_dtype dtype, float scale, void* out, void* ws, size_t ws_bytes,
-                         void* stream) {
-  eas_status st = check_embed(T, H, V, dtype, scale);
-  if (st != EAS_OK) return st;
-  if (!table || (T > 0 && (!ids || !out))) return fail(EAS_ERR_INVALID_ARG, "null pointer");
-  if (!aligned(ids, 4) || !aligned(table, 16) || !aligned(out, 16) || !aligned(ws, 16))
-    return fail(EAS_ERR_INVALID_ARG, "table, out and ws must be 16-byte aligned");
-  const size_t row = static_cast<size_t>(H) * elem_size(dtype);
-  if (overlap(out, row * static_cast<size_t>(T), table, row * static_cast<size_t>(V)))
-    return fail(EAS_ERR_INVALID_ARG, "out must not overlap the table");
-  if (ws && ws_bytes < sizeof(DevStatus)) return fail(EAS_ERR_WORKSPACE, "workspace too small");
-  DevInfo di;
-  st = device_info(&di);
-  if (st != EAS_OK) return st;
-  if (T == 0 && !ws) return EAS_OK;
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const EmbedFwdArgs a = {ids, table, out, T, static_cast<int>(V), static_cast<int>(H), scale,
-                          static_cast<DevStatus*>(ws)};
-  Trace tr_(kTrEmbedFwd, s);
-  EAS_CUDA(launch_embed_fwd(a, dtype == EAS_BF16, di.sms, s), "embed_fwd");
-  return EAS_OK;
-}
-
-size_t eas_embed_bwd_workspace_size(int64_t T, int64_t H, int64_t V) {
-  if (T < 0 || H < 1 || V < 1) return 0;
-  return align_up(sizeof(DevStatus)) + embed_bwd_plan(T, H, V).total;
-}
-
-eas_status eas_embed_bwd(const int32_t* ids, const void* dout, int64_t T, int64_t H, int64_t V,
-                         eas_dtype dtype, float scale, int32_t accumulate, float* dweight,
-                         void* ws, size_t ws_bytes, void* stream) {
-  eas_status st = check_embed(T, H, V, dtype, scale);
-  if (st != EAS_OK) return st;
-  if (accumulate != 0 && accumulate != 1) return fail(EAS_ERR_INVALID_ARG, "accumulate must be 0 or 1");
-  if (!dweight || !ws || (T > 0 && (!ids || !dout))) return fail(EAS_ERR_INVALID_ARG, "null pointer");
-  if (!aligned(ids, 4) || !aligned(dout, 16) || !aligned(dweight, 16) || !aligned(ws, 256))
-    return fail(EAS_ERR_INVALID_ARG, "dout and dweight must be 16-byte and ws 256-byte aligned");
-  if (overlap(dweight, 4 * static_cast<size_t>(V) * static_cast<size_t>(H), dout,
-              static_cast<size_t>(T) * static_cast<size_t>(H) * elem_size(dtype)))
-    return fail(EAS_ERR_INVALID_ARG, "dweight must not overlap dout");
-  const size_t need = eas_embed_bwd_workspace_size(T, H, V);
-  if (ws_bytes < need) return fail(EAS_ERR_WORKSPACE, "workspace %zu < %zu", ws_bytes, need);
-  DevInfo di;
-  st = device_info(&di);
-  if (st != EAS_OK) return st;
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const EmbedBwdArgs a = {ids, dout, dweight, T, static_cast<int>(V), static_cast<int>(H), scale,
-                          accumulate, at<char>(ws, align_up(sizeof(DevStatus))),
-                          static_cast<DevStatus*>(ws)};
-  if (embed_bwd_sorts(T)) {
-    Trace tr_(kTrEmbedSort, s);
-    EAS_CUDA(launch_embed_sort(a, s), "embed_sort");
-  }
-  Trace tr_(kTrEmbedBwd, s);
-  EAS_CUDA(launch_embed_bwd(a, dtype == EAS_BF16, di.sms, s), "embed_bwd");
-  return EAS_OK;
-}
-
-size_t eas_clip_grad_norm_workspace_size(int32_t n) {
-  if (n < 0) return 0;
-  return align_up(sizeof(DevStatus)) + clip_workspace_bytes(n);
-}
-
-eas_status eas_clip_grad_norm(const void* const* grads, void* const* outs, const int64_t* numels,
-                              const int32_t* dtypes, const int32_t* out_dtypes, int32_t n,
-                              float max_norm, float* norm, void* ws, size_t ws_bytes,
-                              void* stream) {
-  if (n < 0 || n > (1 << 20)) return fail(EAS_ERR_INVALID_ARG, "n=%d out of range", n);
-  if (!norm || !ws || (n > 0 && (!grads || !numels || !dtypes)) || (n > 0 && outs && !out_dtypes))
-    return fail(EAS_ERR_INVALID_ARG, "null pointer");
-  if (outs && !(max_norm >= 0.f)) return fail(EAS_ERR_INVALID_ARG, "max_norm must be >= 0");
-  if (!aligned(norm, 4) || !aligned(ws, 256))
-    return fail(EAS_ERR_INVALID_ARG, "ws must be 256-byte aligned");
-  const size_t need = eas_clip_grad_norm_workspace_size(n);
-  if (ws_bytes < need) return fail(EAS_ERR_WORKSPACE, "workspace %zu < %zu", ws_bytes, need);
-  try {
-    std::vector<ClipTensor> list(static_cast<size_t>(n));
-    // every buffer that is written, and every one that is read, by address
-    struct Range {
-      uintptr_t lo, hi;
-      int tensor;
-      bool written;
-    };
-    std::vector<Range> ranges;
-    ranges.reserve(2 * static_cast<size_t>(n));
-    for (int i = 0; i < n; ++i) {
-      ClipTensor& t = list[i];
-      t.in = grads[i];
-      t.out = outs ? outs[i] : nullptr;
-      t.numel = numels[i];
-      const int id = dtypes[i], od = outs ? out_dtypes[i] : id;
-      if ((id != EAS_BF16 && id != EAS_FP32) || (od != EAS_BF16 && od != EAS_FP32))
-        return fail(EAS_ERR_INVALID_ARG, "tensor %d: dtype %d / %d", i, id, od);
-      t.in_bf16 = id == EAS_BF16;
-      t.out_bf16 = od == EAS_BF16;
-      if (t.numel < 0 || t.numel > (1LL << 40))
-        return fail(EAS_ERR_INVALID_ARG, "tensor %d: numel %lld", i, t.numel);
-      if (t.numel == 0) continue;
-      if (!t.in || (outs && !t.out)) return fail(EAS_ERR_INVALID_ARG, "tensor %d: null pointer", i);
-      const size_t ie = t.in_bf16 ? 2 : 4, oe = t.out_bf16 ? 2 : 4;
-      if (!aligned(t.in, ie) || (outs && !aligned(t.out, oe)))
-        return fail(EAS_ERR_INVALID_ARG, "tensor %d: not aligned to its element", i);
-      if (!outs) continue;
-      const uintptr_t ip = reinterpret_cast<uintptr_t>(t.in), op = reinterpret_cast<uintptr_t>(t.out);
-      if (ip == op && ie != oe)
-        return fail(EAS_ERR_INVALID_ARG, "tensor %d: in place with another dtype", i);
-      ranges.push_back({op, op + oe * static_cast<size_t>(t.numel), i, true});
-      if (ip != op) ranges.push_back({ip, ip + ie * static_cast<size_t>(t.numel), i, false});
-    }
-    // no written buffer may share a byte with another entry's or its own input
-    std::sort(ranges.begin(), ranges.end(), [](const Range& a, const Range& b) { return a.lo < b.lo; });
-    uintptr_t end = 0, written_end = 0;
-    for (const Range& r : ranges) {
-      if (r.lo < (r.written ? end : written_end))
-        return fail(EAS_ERR_INVALID_ARG, "tensor %d overlaps another", r.tensor);
-      end = r.hi > end ? r.hi : end;
-      if (r.written) written_end = r.hi > written_end ? r.hi : written_end;
-    }
-    DevInfo di;
-    eas_status st = device_info(&di);
-    if (st != EAS_OK) return st;
-    cudaStream_t s = static_cast<cudaStream_t>(stream);
-    Trace tr_(outs ? kTrGradClip : kTrGradNorm, s);
-    EAS_CUDA(launch_clip_grad_norm(list.data(), n, outs != nullptr, max_norm,
-                                   at<double>(ws, align_up(sizeof(DevStatus))), norm,
-                                   static_cast<DevStatus*>(ws), di.sms, s),
-             "clip_grad_norm");
-    return EAS_OK;
-  } catch (const std::bad_alloc&) {
-    return fail(EAS_ERR_CUDA, "out of host memory");
-  }
-}
-
-eas_status eas_read_device_status(const void* ws, void* stream) {
-  if (!ws) return fail(EAS_ERR_INVALID_ARG, "null workspace");
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  DevStatus h;
-  EAS_CUDA(cudaMemcpyAsync(&h, ws, sizeof(h), cudaMemcpyDeviceToHost, s), "read status");
-  EAS_CUDA(cudaStreamSynchronize(s), "stream sync");
-  if (h.code != 0)
-    return fail(static_cast<eas_status>(h.code), "device status %d (where %d, info %d)", h.code,
-                h.where, h.info);
-  return EAS_OK;
-}
-
-void eas_trace_enable(int32_t on) {
-  std::lock_guard<std::mutex> lk(g_trace_mu);
-  g_trace_on.store(on != 0, std::memory_order_relaxed);
-  if (on != 0) g_trace_used = 0;
-}
-
-int32_t eas_trace_read(int32_t* kinds, float* ms, int32_t cap) {
-  std::lock_guard<std::mutex> lk(g_trace_mu);
-  const int32_t n = static_cast<int32_t>(g_trace_used);
-  for (int32_t i = 0; i < n && i < cap; ++i) {
-    const TraceRec& r = g_trace_pool[i];
-    float t = -1.f;
-    if (cudaEventSynchronize(r.b) != cudaSuccess || cudaEventElapsedTime(&t, r.a, r.b) != cudaSuccess)
-      t = -1.f;
-    if (kinds) kinds[i] = r.kind;
-    if (ms) ms[i] = t;
-  }
-  return n;
-}
-
-const char* eas_kernel_name(int32_t kind) {
-  return (kind >= 0 && kind < kTrCount) ? kTraceNames[kind] : "unknown";
-}
-
-const char* eas_last_error(void) { return g_err; }
-
-const char* eas_status_string(eas_status s) {
-  switch (s) {
-    case EAS_OK: return "EAS_OK";
-    case EAS_ERR_INVALID_ARG: return "EAS_ERR_INVALID_ARG";
-    case EAS_ERR_INVALID_SPANS: return "EAS_ERR_INVALID_SPANS";
-    case EAS_ERR_UNSUPPORTED: return "EAS_ERR_UNSUPPORTED";
-    case EAS_ERR_WORKSPACE: return "EAS_ERR_WORKSPACE";
-    case EAS_ERR_CUDA: return "EAS_ERR_CUDA";
-    case EAS_ERR_TIMEOUT: return "EAS_ERR_TIMEOUT";
-    case EAS_ERR_SPAN_CAPACITY: return "EAS_ERR_SPAN_CAPACITY";
-    case EAS_ERR_INVALID_LAYOUT: return "EAS_ERR_INVALID_LAYOUT";
-  }
-  return "EAS_UNKNOWN";
-}
-
-int32_t eas_version(void) { return 100; }
-
 }  // extern "C"
 
 namespace eas {
@@ -1296,8 +869,5 @@ size_t lmhead_fwd_workspace_bytes(long long T, long long H, long long V, int dty
   if (T < 0 || H < 1 || V < 1) return 0;
   return layout(T, H, V, static_cast<eas_dtype>(dtype), 0).fwd_end;
 }
-
-// Replaces this thread's eas_last_error() message.
-void set_last_error(const char* msg) { snprintf(g_err, sizeof(g_err), "%s", msg); }
 
 }  // namespace eas

@@ -11,7 +11,8 @@
 // partials up themselves, in one order, so the norm needs no launch of its own
 // and results repeat to the bit.
 #include "eas_device.cuh"
-#include "eas_kernels.h"
+#include "eas_launch.cuh"
+#include "eas_ops.h"
 #include "eas_vec.cuh"
 
 namespace eas {

@@ -51,19 +51,6 @@ __device__ __forceinline__ void report(DevStatus* st, int code, int where, int i
   }
 }
 
-// ------------------------------------------------- dependent launches --
-
-// Lets the next launch on the stream begin, if it was launched to overlap
-// (launch_overlapped); what this grid writes is not visible to it yet.
-__device__ __forceinline__ void launch_dependents() {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
-
-// Waits until the launch before has ended and its writes are visible.
-__device__ __forceinline__ void wait_for_launch_before() {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-}
-
 // ----------------------------------------------------------- shared mem --
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {

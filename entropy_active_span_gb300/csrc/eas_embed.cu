@@ -15,8 +15,8 @@
 // into [128256, 4096] take 329 us and 131072 Zipf-distributed ones into [129280,
 // 7168] 785 us, both 6.8 TB/s; the plain copy rate is 6.8.
 #include "eas_device.cuh"
-#include "eas_kernels.h"
 #include "eas_launch.cuh"
+#include "eas_ops.h"
 #include "eas_vec.cuh"
 
 namespace eas {

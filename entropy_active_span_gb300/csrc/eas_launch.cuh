@@ -1,4 +1,5 @@
-// Host-side launch helpers of the operators around the LM head.
+// Launches of the operators around the LM head: shared memory, and launches that
+// overlap (programmatic dependent launch).
 #pragma once
 
 #include <atomic>
@@ -6,6 +7,36 @@
 #include <stdint.h>
 
 namespace eas {
+
+// Lets the next launch on the stream begin, if it was launched to overlap
+// (launch_overlapped); what this grid writes is not visible to it yet.
+__device__ __forceinline__ void launch_dependents() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+// Waits until the launch before has ended and its writes are visible.
+__device__ __forceinline__ void wait_for_launch_before() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+// Launches a kernel that may begin before the launch in front of it on the
+// stream has ended; it calls wait_for_launch_before() ahead of its first use of
+// that launch's results, or at its end.
+template <typename... P, typename... A>
+cudaError_t launch_overlapped(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem,
+                              cudaStream_t s, A... args) {
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
 
 // Lets kKernel's launches have up to `bytes` of dynamic shared memory: opted into
 // once per device and instantiation (one bit per device ordinal; a repeated opt-in

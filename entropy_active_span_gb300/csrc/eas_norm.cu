@@ -19,8 +19,8 @@
 #include <cuda_fp8.h>
 
 #include "eas_device.cuh"
-#include "eas_kernels.h"
 #include "eas_launch.cuh"
+#include "eas_ops.h"
 #include "eas_vec.cuh"
 
 namespace eas {
