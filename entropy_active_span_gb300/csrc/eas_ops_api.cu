@@ -16,14 +16,30 @@ using namespace eas;
 
 namespace {
 
-// Whether [a, a + na) and [b, b + nb) share a byte (null shares none).
-bool overlap(const void* a, size_t na, const void* b, size_t nb) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return x && y && na && nb && x < y + nb && y < x + na;
+// A buffer of a call.  `shared`: a written one may replace, whole, a read one that
+// is also marked so.
+struct Buf {
+  const void* p;
+  size_t n;
+  bool shared = false;
+};
+
+// Whether no written buffer shares a byte with another buffer (null shares none).
+bool disjoint(std::initializer_list<Buf> written, std::initializer_list<Buf> read) {
+  auto overlap = [](const Buf& a, const Buf& b) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+    return x && y && a.n && b.n && x < y + b.n && y < x + a.n;
+  };
+  for (const Buf* w = written.begin(); w != written.end(); ++w) {
+    for (const Buf* v = w + 1; v != written.end(); ++v)
+      if (overlap(*w, *v)) return false;
+    for (const Buf& r : read)
+      if (!(w->shared && r.shared && w->p == r.p && w->n == r.n) && overlap(*w, r)) return false;
+  }
+  return true;
 }
 
-// The same for two buffers of n bytes of which one may replace the other.
-bool overlap_partly(const void* a, const void* b, size_t n) { return a != b && overlap(a, n, b, n); }
+eas_status overlap_error() { return fail(EAS_ERR_INVALID_ARG, "an output or the workspace overlaps another buffer"); }
 
 // Shape and type of the row operators: any H (odd ones keep their vectors on
 // 16-byte boundaries in memory).
@@ -65,12 +81,10 @@ eas_status eas_rmsnorm_fwd(const void* x, const void* residual, const void* weig
       !aligned(y, 16) || !aligned(y_e4m3, 16) || !aligned(y_scale, 4))
     return fail(EAS_ERR_INVALID_ARG, "tensors must be 16-byte aligned");
   const size_t codes = static_cast<size_t>(R) * static_cast<size_t>(H), rows = codes * elem_size(dtype);
-  for (const void* in : {x, residual, static_cast<const void*>(sum_out)})
-    if (overlap(y, rows, in, rows) || overlap(y_e4m3, codes, in, rows))
-      return fail(EAS_ERR_INVALID_ARG, "y and y_e4m3 must not overlap x, residual or sum_out");
-  if (overlap(y, rows, y_e4m3, codes) || overlap_partly(sum_out, x, rows) ||
-      overlap_partly(sum_out, residual, rows))
-    return fail(EAS_ERR_INVALID_ARG, "an output overlaps another buffer");
+  if (!disjoint({{sum_out, rows, true}, {y, rows}, {y_e4m3, codes}, {y_scale, 4 * static_cast<size_t>(R)}},
+                {{x, rows, true}, {residual, rows, true}, {weight, static_cast<size_t>(H) * elem_size(dtype)},
+                 {mask, static_cast<size_t>(R)}}))
+    return overlap_error();
   DevInfo di;
   st = device_info(&di);
   if (st != EAS_OK) return st;
@@ -98,11 +112,12 @@ eas_status eas_rmsnorm_bwd(const void* dy, const void* sum, const void* weight, 
   if (!aligned(dy, 16) || !aligned(sum, 16) || !aligned(weight, 16) || !aligned(ds, 16) ||
       !aligned(dx, 16) || !aligned(dweight, 16) || !aligned(ws, 256))
     return fail(EAS_ERR_INVALID_ARG, "tensors must be 16-byte and ws 256-byte aligned");
-  const size_t rows = static_cast<size_t>(R) * static_cast<size_t>(H) * elem_size(dtype);
-  if (overlap(dx, rows, dy, rows) || overlap(dx, rows, sum, rows) || overlap_partly(dx, ds, rows))
-    return fail(EAS_ERR_INVALID_ARG, "dx must not overlap dy or s, nor ds in part");
   const size_t need = eas_rmsnorm_bwd_workspace_size(R, H);
   if (ws_bytes < need) return fail(EAS_ERR_WORKSPACE, "workspace %zu < %zu", ws_bytes, need);
+  const size_t row = static_cast<size_t>(H) * elem_size(dtype), rows = static_cast<size_t>(R) * row;
+  if (!disjoint({{dx, rows, true}, {dweight, 4 * static_cast<size_t>(H)}, {ws, need}},
+                {{dy, rows}, {sum, rows}, {weight, row}, {ds, rows, true}, {mask, static_cast<size_t>(R)}}))
+    return overlap_error();
   DevInfo di;
   st = device_info(&di);
   if (st != EAS_OK) return st;
@@ -129,10 +144,10 @@ eas_status eas_embed_fwd(const int32_t* ids, const void* table, int64_t T, int64
   if (!table || (T > 0 && (!ids || !out))) return fail(EAS_ERR_INVALID_ARG, "null pointer");
   if (!aligned(ids, 4) || !aligned(table, 16) || !aligned(out, 16) || !aligned(ws, 16))
     return fail(EAS_ERR_INVALID_ARG, "table, out and ws must be 16-byte aligned");
-  const size_t row = static_cast<size_t>(H) * elem_size(dtype);
-  if (overlap(out, row * static_cast<size_t>(T), table, row * static_cast<size_t>(V)))
-    return fail(EAS_ERR_INVALID_ARG, "out must not overlap the table");
   if (ws && ws_bytes < sizeof(DevStatus)) return fail(EAS_ERR_WORKSPACE, "workspace too small");
+  const size_t row = static_cast<size_t>(H) * elem_size(dtype), n = static_cast<size_t>(T);
+  if (!disjoint({{out, row * n}, {ws, sizeof(DevStatus)}}, {{ids, 4 * n}, {table, row * static_cast<size_t>(V)}}))
+    return overlap_error();
   DevInfo di;
   st = device_info(&di);
   if (st != EAS_OK) return st;
@@ -159,11 +174,11 @@ eas_status eas_embed_bwd(const int32_t* ids, const void* dout, int64_t T, int64_
   if (!dweight || !ws || (T > 0 && (!ids || !dout))) return fail(EAS_ERR_INVALID_ARG, "null pointer");
   if (!aligned(ids, 4) || !aligned(dout, 16) || !aligned(dweight, 16) || !aligned(ws, 256))
     return fail(EAS_ERR_INVALID_ARG, "dout and dweight must be 16-byte and ws 256-byte aligned");
-  if (overlap(dweight, 4 * static_cast<size_t>(V) * static_cast<size_t>(H), dout,
-              static_cast<size_t>(T) * static_cast<size_t>(H) * elem_size(dtype)))
-    return fail(EAS_ERR_INVALID_ARG, "dweight must not overlap dout");
   const size_t need = eas_embed_bwd_workspace_size(T, H, V);
   if (ws_bytes < need) return fail(EAS_ERR_WORKSPACE, "workspace %zu < %zu", ws_bytes, need);
+  const size_t n = static_cast<size_t>(T), h = static_cast<size_t>(H);
+  if (!disjoint({{dweight, 4 * static_cast<size_t>(V) * h}, {ws, need}}, {{ids, 4 * n}, {dout, n * h * elem_size(dtype)}}))
+    return overlap_error();
   DevInfo di;
   st = device_info(&di);
   if (st != EAS_OK) return st;
@@ -199,14 +214,18 @@ eas_status eas_clip_grad_norm(const void* const* grads, void* const* outs, const
   if (ws_bytes < need) return fail(EAS_ERR_WORKSPACE, "workspace %zu < %zu", ws_bytes, need);
   try {
     std::vector<ClipTensor> list(static_cast<size_t>(n));
-    // every buffer that is written, and every one that is read, by address
+    // every buffer that is written, and every one that is read, by address (tensor
+    // -1: the norm and the workspace)
     struct Range {
       uintptr_t lo, hi;
       int tensor;
       bool written;
     };
     std::vector<Range> ranges;
-    ranges.reserve(2 * static_cast<size_t>(n));
+    ranges.reserve(2 * static_cast<size_t>(n) + 2);
+    const uintptr_t np = reinterpret_cast<uintptr_t>(norm), wp = reinterpret_cast<uintptr_t>(ws);
+    ranges.push_back({np, np + sizeof(float), -1, true});
+    ranges.push_back({wp, wp + need, -1, true});
     for (int i = 0; i < n; ++i) {
       ClipTensor& t = list[i];
       t.in = grads[i];
@@ -224,19 +243,20 @@ eas_status eas_clip_grad_norm(const void* const* grads, void* const* outs, const
       const size_t ie = t.in_bf16 ? 2 : 4, oe = t.out_bf16 ? 2 : 4;
       if (!aligned(t.in, ie) || (outs && !aligned(t.out, oe)))
         return fail(EAS_ERR_INVALID_ARG, "tensor %d: not aligned to its element", i);
-      if (!outs) continue;
       const uintptr_t ip = reinterpret_cast<uintptr_t>(t.in), op = reinterpret_cast<uintptr_t>(t.out);
       if (ip == op && ie != oe)
         return fail(EAS_ERR_INVALID_ARG, "tensor %d: in place with another dtype", i);
-      ranges.push_back({op, op + oe * static_cast<size_t>(t.numel), i, true});
+      if (outs) ranges.push_back({op, op + oe * static_cast<size_t>(t.numel), i, true});
       if (ip != op) ranges.push_back({ip, ip + ie * static_cast<size_t>(t.numel), i, false});
     }
-    // no written buffer may share a byte with another entry's or its own input
+    // no written buffer may share a byte with another entry's, with its own input
+    // or with the norm or the workspace
     std::sort(ranges.begin(), ranges.end(), [](const Range& a, const Range& b) { return a.lo < b.lo; });
     uintptr_t end = 0, written_end = 0;
     for (const Range& r : ranges) {
       if (r.lo < (r.written ? end : written_end))
-        return fail(EAS_ERR_INVALID_ARG, "tensor %d overlaps another", r.tensor);
+        return r.tensor < 0 ? overlap_error()
+                            : fail(EAS_ERR_INVALID_ARG, "tensor %d overlaps another buffer", r.tensor);
       end = r.hi > end ? r.hi : end;
       if (r.written) written_end = r.hi > written_end ? r.hi : written_end;
     }

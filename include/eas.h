@@ -360,6 +360,12 @@ eas_status eas_lmhead_fwd_noalloc(const void* hidden, const void* weight,
                                   uint32_t flags, float* logprob, float* entropy, float* lse,
                                   void* stream);
 
+/*
+ * In the calls from here to eas_clip_grad_norm no output and no workspace may
+ * share a byte with another buffer of the call, except where an argument says
+ * that it may replace another (EAS_ERR_INVALID_ARG).
+ */
+
 /* --------------------------------------------- norm before the LM head */
 
 /*
@@ -380,8 +386,7 @@ eas_status eas_lmhead_fwd_noalloc(const void* hidden, const void* weight,
  *            residual itself.
  *   y        [R, H] out in dtype, or NULL
  *   y_e4m3, y_scale : [R, H] uint8 and [R] fp32 out, or both NULL
- * y and y_e4m3 must not overlap an input.  1 <= H <= 2^20, eps > 0, mean(s^2)
- * within fp32.
+ * 1 <= H <= 2^20, eps > 0, mean(s^2) within fp32.
  */
 eas_status eas_rmsnorm_fwd(const void* x, const void* residual, const void* weight,
                            const uint8_t* mask, int64_t R, int64_t H, eas_dtype dtype, float eps,
