@@ -474,6 +474,17 @@ def _need_shape(t: torch.Tensor, name: str, dtype: torch.dtype, device, shape) -
     raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
+def _ws_args(ws, device) -> tuple[int, int]:
+    """Address and bytes of a workspace; refuses one that the kernels cannot write."""
+    if not isinstance(ws, torch.Tensor):
+        raise TypeError("ws must be a tensor")
+    if ws.device != device:
+        raise ValueError(f"ws is on {ws.device}, expected {device}")
+    if not ws.is_contiguous():
+        raise ValueError("ws must be contiguous")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
 def rmsnorm_fwd(x, weight, eps: float = 1e-6, residual=None, mask=None, want_y: bool = True,
                 want_e4m3: bool = False, want_sum: bool = True, out=None):
     """RMS norm of x + residual ([R, H], bf16 or fp32) times weight [H].
@@ -570,7 +581,7 @@ def rmsnorm_bwd(dy, s, weight, eps: float = 1e-6, ds=None, mask=None, ws=None, d
         ws = workspace(rmsnorm_bwd_workspace_size(R, H), dev)
     _lib.check(_lib.load().eas_rmsnorm_bwd(
         _ptr(dy), _ptr(s), _ptr(weight), _ptr(ds), _ptr(mask), R, H, code, eps, _ptr(dx),
-        _ptr(dweight), _ptr(ws), ws.numel(), _stream(dev)))
+        _ptr(dweight), *_ws_args(ws, dev), _stream(dev)))
     return dx, dweight
 
 
@@ -592,8 +603,8 @@ def embed_fwd(ids, table, scale: float = 1.0, ws=None, out=None):
     else:
         _need_shape(out, "out", dt, dev, (T, H))
     _lib.check(_lib.load().eas_embed_fwd(
-        _ptr(ids), _ptr(table), T, H, V, code, scale, _ptr(out), _ptr(ws),
-        0 if ws is None else ws.numel(), _stream(dev)))
+        _ptr(ids), _ptr(table), T, H, V, code, scale, _ptr(out),
+        *((None, 0) if ws is None else _ws_args(ws, dev)), _stream(dev)))
     return out
 
 
@@ -626,7 +637,7 @@ def embed_bwd(ids, dout, V: int, scale: float = 1.0, accumulate: bool = False, w
         ws = workspace(embed_bwd_workspace_size(T, H, V), dev)
     _lib.check(_lib.load().eas_embed_bwd(
         _ptr(ids), _ptr(dout), T, H, V, code, scale, 1 if accumulate else 0, _ptr(dweight),
-        _ptr(ws), ws.numel(), _stream(dev)))
+        *_ws_args(ws, dev), _stream(dev)))
     return dweight
 
 
@@ -674,7 +685,7 @@ def clip_grad_norm(grads, max_norm: float | None, out=None, ws=None, norm=None):
     _lib.check(_lib.load().eas_clip_grad_norm(
         ptrs.buffer_info()[0], out_ptrs.buffer_info()[0] if clip else None,
         numels.buffer_info()[0], codes.buffer_info()[0], out_codes.buffer_info()[0], n,
-        max_norm if clip else 0.0, norm.data_ptr(), ws.data_ptr(), ws.numel(), _stream(dev)))
+        max_norm if clip else 0.0, norm.data_ptr(), *_ws_args(ws, dev), _stream(dev)))
     return norm
 
 
