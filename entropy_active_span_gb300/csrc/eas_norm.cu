@@ -171,8 +171,8 @@ __device__ __forceinline__ void store_row_e4m3(uint8_t* p, int c, int H, const f
   }
 }
 
-// Combines (a, b) over the threads of a row: a by sum, b by sum or maximum.
-// `red` alternates with the row's parity, so one barrier a row is enough.
+// Combines (a, b) over the threads of a row that a CTA (of two warps or more) holds:
+// a by sum, b by sum or maximum.  `red` alternates with the row's parity, so one barrier a row is enough.
 template <bool kMaxB>
 __device__ __forceinline__ void reduce_pair(float& a, float& b, float2* red, int warps) {
 #pragma unroll
@@ -181,7 +181,6 @@ __device__ __forceinline__ void reduce_pair(float& a, float& b, float2* red, int
     const float t = __shfl_xor_sync(0xffffffffu, b, o);
     b = kMaxB ? fmaxf(b, t) : b + t;
   }
-  if (warps == 1) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (lane == 0) red[warp] = make_float2(a, b);
   __syncthreads();
