@@ -386,7 +386,7 @@ eas_status eas_lmhead_fwd_noalloc(const void* hidden, const void* weight,
  *            residual itself.
  *   y        [R, H] out in dtype, or NULL
  *   y_e4m3, y_scale : [R, H] uint8 and [R] fp32 out, or both NULL
- * 1 <= H <= 2^20, eps > 0, mean(s^2) within fp32.
+ * 1 <= H <= 2^20, eps > 0; a row's sum of s^2, and s * weight, within fp32.
  */
 eas_status eas_rmsnorm_fwd(const void* x, const void* residual, const void* weight,
                            const uint8_t* mask, int64_t R, int64_t H, eas_dtype dtype, float eps,
