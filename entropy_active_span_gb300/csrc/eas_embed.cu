@@ -67,7 +67,7 @@ embed_fwd_kernel(const EmbedFwdArgs p) {
 #pragma unroll
           for (int i = 0; i < VEC; ++i) f[i] *= p.scale;
         }
-        // the table's rows come again, the output does not: 128 us against 136 at
+        // the table's rows come again, the output does not: 130 us against 134 at
         // [65536, 5120] bf16 with Zipf-distributed ids
         store_vec<T, VEC, true>(dst + static_cast<long long>(r) * p.H + c, f);
       }
@@ -741,8 +741,8 @@ static cudaError_t embed_fwd_t(const EmbedFwdArgs& a, int num_sms, cudaStream_t 
   int tx = 32;
   while (tx < 256 && tx * VEC < a.H) tx *= 2;
   const dim3 block(tx, 256 / tx);
-  // four rows a thread once that still fills the machine ([65536, 5120] bf16:
-  // 133 us against 139 with one)
+  // four rows a thread once that still fills the machine ([65536, 5120] bf16,
+  // Zipf-distributed ids: 130 us against 139 with one)
   const long long groups = (a.T + 4 * block.y - 1) / (4 * block.y);
   if (groups >= 8LL * num_sms) {
     embed_fwd_kernel<T, VEC, 4><<<static_cast<unsigned>(groups), block, 0, s>>>(a);
@@ -760,9 +760,10 @@ cudaError_t launch_embed_fwd(const EmbedFwdArgs& a, int is_bf16, int num_sms, cu
   return a.H % 4 == 0 ? embed_fwd_t<float, 4>(a, num_sms, s) : embed_fwd_t<float, 1>(a, num_sms, s);
 }
 
-// A worker's chunk is as long as 4096 workers allow (a worker is a chunk and
-// 512 columns), 16 to 128 tokens: short chunks keep small calls parallel, long
-// ones keep the pieces of runs few.
+// A chunk is as long as leaves 4096 pairs of a chunk and 512 columns, 16 to 128
+// tokens: short chunks keep small calls parallel, long ones keep the pieces of runs
+// few.  (A CTA of the sums takes 512 columns in fp32 and in rows of odd width, 1024
+// in bf16: half as many CTAs there.)
 EmbedBwdPlan embed_bwd_plan(long long T, long long H, long long V) {
   (void)V;
   EmbedBwdPlan p;
