@@ -30,8 +30,8 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import _lib
-from ._lib import (EAS_BF16, EAS_DEFAULT_VOCAB_CHUNK, EAS_E4M3, EAS_FP32, EAS_REUSE_FWD_ROWS,
-                   EAS_ROWS_ACTIVE, EAS_ROWS_SPAN, EasError)
+from ._lib import (EAS_BF16, EAS_DEFAULT_VOCAB_CHUNK, EAS_E4M3, EAS_FP32, EAS_MAX_TOKENS, EAS_MAX_TOP,
+                   EAS_REUSE_FWD_ROWS, EAS_ROWS_ACTIVE, EAS_ROWS_SPAN, EasError)
 
 __all__ = [
     "build_active_spans", "lmhead_fwd", "lmhead_bwd", "lmhead_workspace_size",
@@ -44,6 +44,8 @@ __all__ = [
     "rmsnorm_fwd", "rmsnorm_bwd", "rmsnorm_bwd_workspace_size", "FusedRMSNorm", "fused_rmsnorm",
     "embed_fwd", "embed_bwd", "embed_bwd_workspace_size", "FusedEmbedding", "fused_embedding",
     "clip_grad_norm", "clip_grad_norm_workspace_size",
+    "EAS_MAX_TOKENS", "EAS_MAX_TOP", "token_logprobs_fwd", "token_logprobs_bwd",
+    "FusedTokenLogprobs", "fused_token_logprobs",
 ]
 
 
@@ -689,6 +691,104 @@ def clip_grad_norm(grads, max_norm: float | None, out=None, ws=None, norm=None):
     return norm
 
 
+def _rows_of(t: torch.Tensor, name: str) -> int:
+    """Row pitch of a matrix whose rows are dense (a slice of wider rows, say)."""
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be [N, V]")
+    N, V = t.shape
+    if V > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have dense rows")
+    if N <= 1:
+        return V
+    if t.stride(0) < V:
+        raise ValueError(f"{name} must not have rows that overlap")
+    return t.stride(0)
+
+
+def _token_list(tokens, N: int, device) -> int:
+    """Tokens a row of a [N] or [N, M] list."""
+    if tokens is None:
+        return 0
+    _need(tokens, "tokens", torch.int32, device)
+    if tokens.dim() not in (1, 2) or tokens.shape[0] != N:
+        raise ValueError(f"tokens must be [N] or [N, M] with N = {N}, got {tuple(tokens.shape)}")
+    return 1 if tokens.dim() == 1 else tokens.shape[1]
+
+
+def token_logprobs_fwd(logits, tokens=None, top_k: int = 0, scale: float = 1.0, mask=None, ws=None,
+                       out=None):
+    """Scores of existing logits ([N, V], bf16 or fp32, rows dense but any pitch).
+
+    Returns (logprob, entropy, lse, top_logprob, top_ids) of softmax(scale * logits):
+    the log probabilities of tokens ([N] or [N, M] int32; -1: none, 0), the entropy
+    and log-sum-exp of each row, and the top_k likeliest tokens of each row with
+    their log probabilities, ties by ascending id.  logprob is None without tokens,
+    the last two without top_k.  Rows whose mask byte is 0 are not read and get
+    zeros (top_ids -1).  Tokens outside the vocabulary get 0 and, where ws (16
+    bytes or more) is passed, EAS_ERR_INVALID_ARG in its status word.  out: buffers
+    for the five, None where one is to be allocated."""
+    code = _row_code(logits, "logits")
+    dev = logits.device
+    ld = _rows_of(logits, "logits")
+    N, V = logits.shape
+    M = _token_list(tokens, N, dev)
+    if mask is not None:
+        _need_shape(mask, "mask", torch.uint8, dev, (N,))
+    wanted = [(None if tokens is None else tokens.shape, torch.float32, "logprob"),
+              ((N,), torch.float32, "entropy"), ((N,), torch.float32, "lse"),
+              ((N, top_k) if top_k else None, torch.float32, "top_logprob"),
+              ((N, top_k) if top_k else None, torch.int32, "top_ids")]
+    res = list(out) if out is not None else [None] * 5
+    for i, (shape, dt, name) in enumerate(wanted):
+        if shape is None:
+            res[i] = None
+        elif res[i] is None:
+            res[i] = torch.empty(shape, dtype=dt, device=dev)
+        else:
+            _need_shape(res[i], name, dt, dev, shape)
+    lp, ent, lse, top, ids = res
+    _lib.check(_lib.load().eas_token_logprobs_fwd(
+        _ptr(logits), ld, _ptr(tokens), _ptr(mask), N, V, M, top_k, code, scale, _ptr(lp),
+        _ptr(ent), _ptr(lse), _ptr(top), _ptr(ids),
+        *((None, 0) if ws is None else _ws_args(ws, dev)), _stream(dev)))
+    return lp, ent, lse, top, ids
+
+
+def token_logprobs_bwd(g_logprob, g_entropy, logits, tokens, lse, entropy, scale: float = 1.0,
+                       mask=None, ws=None, out=None):
+    """Gradient of token_logprobs_fwd's logprob and entropy at the logits, in their dtype.
+
+    g_logprob has the shape of tokens (both None: no given tokens), g_entropy is [N]
+    or None.  lse and entropy are the forward's.  top_logprob's gradient is that of
+    tokens: append top_ids to them.  out may be logits itself."""
+    code = _row_code(logits, "logits")
+    dev = logits.device
+    ld = _rows_of(logits, "logits")
+    N, V = logits.shape
+    M = _token_list(tokens, N, dev)
+    if (tokens is None) != (g_logprob is None):
+        raise ValueError("tokens and g_logprob come together")
+    if tokens is not None:
+        _need_shape(g_logprob, "g_logprob", torch.float32, dev, tokens.shape)
+    if g_entropy is not None:
+        _need_shape(g_entropy, "g_entropy", torch.float32, dev, (N,))
+    _need_shape(lse, "lse", torch.float32, dev, (N,))
+    _need_shape(entropy, "entropy", torch.float32, dev, (N,))
+    if mask is not None:
+        _need_shape(mask, "mask", torch.uint8, dev, (N,))
+    if out is None:
+        out = torch.empty((N, V), dtype=logits.dtype, device=dev)
+    elif not isinstance(out, torch.Tensor) or out.dtype != logits.dtype or out.device != dev:
+        raise TypeError(f"out must be a {logits.dtype} tensor on {dev}")
+    elif out.shape != logits.shape:
+        raise ValueError(f"out must have shape {(N, V)}, got {tuple(out.shape)}")
+    _lib.check(_lib.load().eas_token_logprobs_bwd(
+        _ptr(g_logprob), _ptr(g_entropy), _ptr(logits), ld, _ptr(tokens), _ptr(mask), _ptr(lse),
+        _ptr(entropy), N, V, M, code, scale, _ptr(out), _rows_of(out, "out"),
+        *((None, 0) if ws is None else _ws_args(ws, dev)), _stream(dev)))
+    return out
+
+
 def _grad_rows(g: torch.Tensor) -> torch.Tensor:
     """An upstream gradient as the kernels read it: dense, on a 16-byte boundary
     (autograd hands over broadcast and offset views)."""
@@ -752,3 +852,41 @@ class FusedEmbedding(torch.autograd.Function):
 def fused_embedding(ids, table, scale: float = 1.0):
     """Differentiable scale * table[ids] ([T, H]); id -1 is padding."""
     return FusedEmbedding.apply(ids, table, scale)
+
+
+class FusedTokenLogprobs(torch.autograd.Function):
+    """Autograd wrapper of token_logprobs_fwd / token_logprobs_bwd: logits ->
+    (logprob, entropy, top_logprob, top_ids).  top_logprob's gradient goes to the
+    tokens that were the top ones."""
+
+    @staticmethod
+    def forward(ctx, logits, tokens, top_k, scale, mask):
+        lp, ent, lse, top, ids = token_logprobs_fwd(logits, tokens, top_k, scale, mask)
+        ctx.save_for_backward(logits, tokens, lse, ent, ids, mask)
+        ctx.scale = scale
+        ctx.set_materialize_grads(False)
+        if ids is not None:
+            ctx.mark_non_differentiable(ids)
+        return lp, ent, top, ids
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, g_lp, g_ent, g_top, _ids):
+        logits, tokens, lse, ent, ids, mask = ctx.saved_tensors
+        given = [tuple(v if v.dim() == 2 else v[:, None] for v in (t, g.float()))
+                 for t, g in ((tokens, g_lp), (ids, g_top)) if g is not None]
+        t = g = None
+        if given:
+            t, g = (torch.cat(p, 1) for p in zip(*given))
+        if g_ent is not None:
+            g_ent = g_ent.contiguous().float()
+        return token_logprobs_bwd(g, g_ent, logits, t, lse, ent, ctx.scale, mask), None, None, None, None
+
+
+def fused_token_logprobs(logits, tokens=None, top_k: int = 0, scale: float = 1.0, mask=None):
+    """Differentiable (logprob, entropy, top_logprob, top_ids) of existing logits; see
+    token_logprobs_fwd.  Without tokens logprob is None, without top_k the last two.
+    tokens and top_k together are at most 128 a row."""
+    if _token_list(tokens, logits.shape[0], logits.device) + top_k > EAS_MAX_TOKENS:
+        raise ValueError(f"tokens and top_k together are at most {EAS_MAX_TOKENS} a row")
+    return FusedTokenLogprobs.apply(logits, tokens, top_k, scale, mask)

@@ -27,6 +27,8 @@ EAS_REUSE_FWD_ROWS = 2
 
 EAS_DEFAULT_VOCAB_CHUNK = 16384
 EAS_STATIC_SCRATCH_BYTES = 64 << 20
+EAS_MAX_TOP = 64
+EAS_MAX_TOKENS = 128
 
 # name -> (restype, argtypes), in the order of include/eas.h
 _P, _I64, _I32, _U32, _SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_uint32, ctypes.c_size_t
@@ -68,6 +70,10 @@ SIGNATURES = {
                                      _SZ, _P]),
     "eas_clip_grad_norm_workspace_size": (_SZ, [_I32]),
     "eas_clip_grad_norm": (ctypes.c_int, [_P, _P, _P, _P, _P, _I32, _F32, _P, _P, _SZ, _P]),
+    "eas_token_logprobs_fwd": (ctypes.c_int, [_P, _I64, _P, _P, _I64, _I64, _I64, _I32,
+                                              ctypes.c_int, _F32, _P, _P, _P, _P, _P, _P, _SZ, _P]),
+    "eas_token_logprobs_bwd": (ctypes.c_int, [_P, _P, _P, _I64, _P, _P, _P, _P, _I64, _I64, _I64,
+                                              ctypes.c_int, _F32, _P, _I64, _P, _SZ, _P]),
     "eas_selftest_wait_timeout": (ctypes.c_int, [_I64, _P, _SZ, _P]),
     "eas_read_device_status": (ctypes.c_int, [_P, _P]),
     "eas_trace_enable": (None, [_I32]),

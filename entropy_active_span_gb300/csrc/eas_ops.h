@@ -97,4 +97,44 @@ cudaError_t launch_clip_grad_norm(const ClipTensor* t, int n, bool clip, float m
                                   double* partial, float* norm, DevStatus* st, int num_sms,
                                   cudaStream_t s);
 
+// ---- scores of logits (eas_score.cu) ----
+constexpr int kMaxTop = 64;       // EAS_MAX_TOP
+constexpr int kMaxTokens = 128;   // EAS_MAX_TOKENS
+struct ScoreFwdArgs {
+  const void* x;          // [N] rows of V logits, ld elements apart
+  long long ld;
+  const int* tokens;      // [N][M]; -1: none
+  const uint8_t* mask;    // [N] or null: every row active
+  long long N;
+  int V, M, k;
+  float scale, c;         // c = scale log2 e
+  float* logprob;         // [N][M]
+  float* entropy;         // [N]
+  float* lse;             // [N]
+  float* top;             // [N][k]
+  int* ids;               // [N][k]
+  DevStatus* status;      // or null
+  int split;              // CTAs a row (set by the launcher)
+};
+cudaError_t launch_score_fwd(const ScoreFwdArgs& a, int is_bf16, int num_sms, cudaStream_t s);
+
+struct ScoreBwdArgs {
+  const void* x;
+  long long ld;
+  const int* tokens;
+  const uint8_t* mask;
+  const float* g_logprob; // [N][M]
+  const float* g_entropy; // [N] or null: zero
+  const float* lse;       // [N]
+  const float* entropy;   // [N]
+  void* dx;               // [N] rows, ld_dx apart; may be x itself
+  long long ld_dx;
+  long long N;
+  int V, M;
+  float scale;
+  DevStatus* status;
+  int split;
+};
+cudaError_t launch_score_bwd(const ScoreBwdArgs& a, int is_bf16, int num_sms, cudaStream_t s);
+
 }  // namespace eas

@@ -62,7 +62,24 @@ eas_status check_embed(long long T, long long H, long long V, eas_dtype dt, floa
   return EAS_OK;
 }
 
+// Bytes from the first to the last element of N rows of V elements, ld apart.
+size_t extent(long long N, long long V, long long ld, size_t e) {
+  return N > 0 ? (static_cast<size_t>(N - 1) * static_cast<size_t>(ld) + static_cast<size_t>(V)) * e : 0;
+}
+
+eas_status check_scores(long long N, long long V, long long M, long long ld, eas_dtype dt, float scale) {
+  if (N < 0 || N > (1LL << 28)) return fail(EAS_ERR_INVALID_ARG, "N=%lld out of range", N);
+  if (V < 1 || V > 0x7fffff00LL) return fail(EAS_ERR_INVALID_ARG, "V=%lld out of range", V);
+  if (M < 0 || M > EAS_MAX_TOKENS) return fail(EAS_ERR_INVALID_ARG, "M=%lld out of range", M);
+  if (ld < V || ld > (1LL << 40)) return fail(EAS_ERR_INVALID_ARG, "row pitch %lld below V or out of range", ld);
+  if (dt != EAS_BF16 && dt != EAS_FP32) return fail(EAS_ERR_INVALID_ARG, "dtype %d", (int)dt);
+  if (!(scale > 0.f) || !std::isfinite(scale)) return fail(EAS_ERR_INVALID_ARG, "scale must be positive");
+  return EAS_OK;
+}
+
 }  // namespace
+
+static_assert(EAS_MAX_TOP == kMaxTop && EAS_MAX_TOKENS == kMaxTokens, "eas.h and eas_ops.h");
 
 extern "C" {
 
@@ -273,6 +290,74 @@ eas_status eas_clip_grad_norm(const void* const* grads, void* const* outs, const
   } catch (const std::bad_alloc&) {
     return fail(EAS_ERR_CUDA, "out of host memory");
   }
+}
+
+eas_status eas_token_logprobs_fwd(const void* logits, int64_t ld, const int32_t* tokens,
+                                  const uint8_t* mask, int64_t N, int64_t V, int64_t M, int32_t k,
+                                  eas_dtype dtype, float scale, float* logprob, float* entropy,
+                                  float* lse, float* top_logprob, int32_t* top_ids, void* ws,
+                                  size_t ws_bytes, void* stream) {
+  eas_status st = check_scores(N, V, M, ld, dtype, scale);
+  if (st != EAS_OK) return st;
+  if (k < 0 || k > EAS_MAX_TOP || k > V) return fail(EAS_ERR_INVALID_ARG, "k=%d out of range", k);
+  if (N > 0 && (!logits || !entropy || !lse || (M > 0 && (!tokens || !logprob)) ||
+                (k > 0 && (!top_logprob || !top_ids))))
+    return fail(EAS_ERR_INVALID_ARG, "null pointer");
+  const size_t e = elem_size(dtype);
+  if (!aligned(logits, e) || !aligned(tokens, 4) || !aligned(logprob, 4) || !aligned(entropy, 4) ||
+      !aligned(lse, 4) || !aligned(top_logprob, 4) || !aligned(top_ids, 4) || !aligned(ws, 16))
+    return fail(EAS_ERR_INVALID_ARG, "tensors must be aligned to their elements and ws to 16 bytes");
+  if (ws && ws_bytes < sizeof(DevStatus)) return fail(EAS_ERR_WORKSPACE, "workspace too small");
+  const size_t n = static_cast<size_t>(N), mb = 4 * n * static_cast<size_t>(M), kb = 4 * n * static_cast<size_t>(k);
+  if (!disjoint({{logprob, mb}, {entropy, 4 * n}, {lse, 4 * n}, {top_logprob, kb}, {top_ids, kb}, {ws, sizeof(DevStatus)}},
+                {{logits, extent(N, V, ld, e)}, {tokens, mb}, {mask, n}}))
+    return overlap_error();
+  DevInfo di;
+  st = device_info(&di);
+  if (st != EAS_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (ws) EAS_CUDA(cudaMemsetAsync(ws, 0, sizeof(DevStatus), s), "clear status");
+  const ScoreFwdArgs a = {logits, ld, tokens, mask, N, static_cast<int>(V), static_cast<int>(M), k,
+                          scale, scale * kLog2e, logprob, entropy, lse, top_logprob, top_ids,
+                          static_cast<DevStatus*>(ws), 1};
+  Trace tr_(kTrScoreFwd, s);
+  EAS_CUDA(launch_score_fwd(a, dtype == EAS_BF16, di.sms, s), "token_logprobs_fwd");
+  return EAS_OK;
+}
+
+eas_status eas_token_logprobs_bwd(const float* g_logprob, const float* g_entropy,
+                                  const void* logits, int64_t ld, const int32_t* tokens,
+                                  const uint8_t* mask, const float* lse, const float* entropy,
+                                  int64_t N, int64_t V, int64_t M, eas_dtype dtype, float scale,
+                                  void* dlogits, int64_t ld_dlogits, void* ws, size_t ws_bytes,
+                                  void* stream) {
+  eas_status st = check_scores(N, V, M, ld, dtype, scale);
+  if (st != EAS_OK) return st;
+  if (ld_dlogits < V || ld_dlogits > (1LL << 40))
+    return fail(EAS_ERR_INVALID_ARG, "row pitch %lld below V or out of range", (long long)ld_dlogits);
+  if (N > 0 && (!logits || !lse || !entropy || !dlogits || (M > 0 && (!tokens || !g_logprob))))
+    return fail(EAS_ERR_INVALID_ARG, "null pointer");
+  const size_t e = elem_size(dtype);
+  if (!aligned(logits, e) || !aligned(dlogits, e) || !aligned(tokens, 4) || !aligned(g_logprob, 4) ||
+      !aligned(g_entropy, 4) || !aligned(lse, 4) || !aligned(entropy, 4) || !aligned(ws, 16))
+    return fail(EAS_ERR_INVALID_ARG, "tensors must be aligned to their elements and ws to 16 bytes");
+  if (ws && ws_bytes < sizeof(DevStatus)) return fail(EAS_ERR_WORKSPACE, "workspace too small");
+  const size_t n = static_cast<size_t>(N), mb = 4 * n * static_cast<size_t>(M);
+  if (!disjoint({{dlogits, extent(N, V, ld_dlogits, e), true}, {ws, sizeof(DevStatus)}},
+                {{logits, extent(N, V, ld, e), true}, {tokens, mb}, {mask, n}, {g_logprob, mb},
+                 {g_entropy, 4 * n}, {lse, 4 * n}, {entropy, 4 * n}}))
+    return overlap_error();
+  DevInfo di;
+  st = device_info(&di);
+  if (st != EAS_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (ws) EAS_CUDA(cudaMemsetAsync(ws, 0, sizeof(DevStatus), s), "clear status");
+  const ScoreBwdArgs a = {logits, ld, tokens, mask, g_logprob, g_entropy, lse, entropy, dlogits,
+                          ld_dlogits, N, static_cast<int>(V), static_cast<int>(M), scale,
+                          static_cast<DevStatus*>(ws), 1};
+  Trace tr_(kTrScoreBwd, s);
+  EAS_CUDA(launch_score_bwd(a, dtype == EAS_BF16, di.sms, s), "token_logprobs_bwd");
+  return EAS_OK;
 }
 
 }  // extern "C"

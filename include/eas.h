@@ -361,7 +361,7 @@ eas_status eas_lmhead_fwd_noalloc(const void* hidden, const void* weight,
                                   void* stream);
 
 /*
- * In the calls from here to eas_clip_grad_norm no output and no workspace may
+ * In the calls from here to eas_token_logprobs_bwd no output and no workspace may
  * share a byte with another buffer of the call, except where an argument says
  * that it may replace another (EAS_ERR_INVALID_ARG).
  */
@@ -469,6 +469,58 @@ eas_status eas_clip_grad_norm(const void* const* grads, void* const* outs, const
                               const int32_t* dtypes, const int32_t* out_dtypes, int32_t n,
                               float max_norm, float* norm, void* ws, size_t ws_bytes,
                               void* stream);
+
+/* ------------------------------------------------- scores of logits */
+
+/*
+ * Scores of logits that exist (a sampler's, a teacher's), z = scale * logits:
+ *   lse = log sum_v exp(z_v),  logprob_j = z[tokens_j] - lse,
+ *   entropy = lse - sum_v p_v z_v,  p = exp(z - lse)  (0 where z is -inf),
+ *   top_logprob, top_ids: z - lse and column of the k largest logits, from the
+ *   largest on; equal ones by ascending column (-0 equals 0, NaN is above all).
+ * logits are read once; sums are fp32, in a fixed order: results repeat to the bit.
+ *
+ *   logits   [N] rows of V values, ld elements apart (ld >= V; aligned to their
+ *            element), bf16 or fp32 (dtype).  -inf is a token that cannot be.  A row
+ *            with NaN or +inf, or with nothing but -inf, has NaN for its lse,
+ *            entropy and log probabilities (its top_ids are as said above).
+ *   tokens   [N, M] int32 columns, 0 <= M <= EAS_MAX_TOKENS (NULL where M = 0); the
+ *            same one may come twice.  -1: none, logprob 0.  Any other one outside
+ *            [0, V) also gives 0, and EAS_ERR_INVALID_ARG in the status word of ws.
+ *   mask     [N] uint8 or NULL (every row active).  Inactive rows are not read; they
+ *            get zeros, and -1 in top_ids.
+ *   scale    > 0, finite (the inverse of a temperature)
+ *   k        0 <= k <= min(EAS_MAX_TOP, V); 0: top_logprob and top_ids may be NULL
+ *   logprob [N, M], entropy [N], lse [N], top_logprob [N, k] fp32, top_ids [N, k]
+ *            int32 : out
+ *   ws       at least 16 bytes for the status word, or NULL: no status is kept
+ */
+#define EAS_MAX_TOP 64
+#define EAS_MAX_TOKENS 128
+
+eas_status eas_token_logprobs_fwd(const void* logits, int64_t ld, const int32_t* tokens,
+                                  const uint8_t* mask, int64_t N, int64_t V, int64_t M, int32_t k,
+                                  eas_dtype dtype, float scale, float* logprob, float* entropy,
+                                  float* lse, float* top_logprob, int32_t* top_ids, void* ws,
+                                  size_t ws_bytes, void* stream);
+
+/*
+ * Its gradient at the logits.  With G the sum of a row's g_logprob over real tokens:
+ *   dlogits_v = scale * (sum_j g_logprob_j [v == tokens_j]
+ *                        - p_v (G + g_entropy (z_v - lse + entropy))).
+ * The gradient of top_logprob is that of given tokens: pass top_ids among them.
+ *   lse, entropy : the forward's; p is taken from lse
+ *   g_logprob [N, M], g_entropy [N] fp32; g_entropy may be NULL (zero)
+ *   dlogits  [N] rows of V values, ld_dlogits apart, in dtype; may be logits itself
+ *            (same pitch).  Inactive rows get zeros, whatever logits and the
+ *            gradients hold there.  Elements between the rows are left alone.
+ */
+eas_status eas_token_logprobs_bwd(const float* g_logprob, const float* g_entropy,
+                                  const void* logits, int64_t ld, const int32_t* tokens,
+                                  const uint8_t* mask, const float* lse, const float* entropy,
+                                  int64_t N, int64_t V, int64_t M, eas_dtype dtype, float scale,
+                                  void* dlogits, int64_t ld_dlogits, void* ws, size_t ws_bytes,
+                                  void* stream);
 
 /* ------------------------------------------------------------- utilities */
 

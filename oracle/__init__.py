@@ -16,7 +16,8 @@ from .fp8 import (dequantize_rows_e4m3, dequantized_rows, e4m3_decode, e4m3_enco
                   quantize_rows_e4m3)
 from .lmhead import (lmhead_forward, lmhead_forward_rows, lmhead_dlogits_rows,
                      lmhead_backward, lmhead_backward_rows_weighted, loss_value)
-from .ops import clip_grads, embed, embed_grad, rmsnorm, rmsnorm_grad
+from .ops import (clip_grads, embed, embed_grad, momentum_update, orthogonalize, rmsnorm,
+                  rmsnorm_grad, token_scores, token_scores_grad)
 
 __all__ = [
     "active_spans", "span_rows", "cp_local_mask", "cp_local_to_global", "lmhead_forward", "lmhead_forward_rows",
@@ -24,5 +25,5 @@ __all__ = [
     "loss_value", "e4m3_decode", "e4m3_encode_rne", "quantize_rows_e4m3",
     "dequantize_rows_e4m3", "dequantized_rows", "lmhead_backward_e4m3",
     "lmhead_backward_e4m3_rows_weighted", "rmsnorm", "rmsnorm_grad", "embed", "embed_grad",
-    "clip_grads",
+    "clip_grads", "momentum_update", "orthogonalize", "token_scores", "token_scores_grad",
 ]
