@@ -46,6 +46,7 @@ __all__ = [
     "clip_grad_norm", "clip_grad_norm_workspace_size",
     "EAS_MAX_TOKENS", "EAS_MAX_TOP", "token_logprobs_fwd", "token_logprobs_bwd",
     "FusedTokenLogprobs", "fused_token_logprobs",
+    "NEWTON_SCHULZ", "orthogonalize", "muon_update", "orthogonalize_workspace_size",
 ]
 
 
@@ -890,3 +891,72 @@ def fused_token_logprobs(logits, tokens=None, top_k: int = 0, scale: float = 1.0
     if _token_list(tokens, logits.shape[0], logits.device) + top_k > EAS_MAX_TOKENS:
         raise ValueError(f"tokens and top_k together are at most {EAS_MAX_TOKENS} a row")
     return FusedTokenLogprobs.apply(logits, tokens, top_k, scale, mask)
+
+
+# Coefficients (a, b, c) of a Newton-Schulz step that raise small singular values fast
+# and bring all of them near 1 in about five steps.
+NEWTON_SCHULZ = (3.4445, -4.7750, 2.0315)
+
+
+def orthogonalize_workspace_size(L: int, rows: int, cols: int) -> int:
+    return int(_lib.load().eas_orthogonalize_workspace_size(L, rows, cols))
+
+
+def _coefficients(coeffs, steps: int) -> array:
+    flat = list(coeffs)
+    if flat and not hasattr(flat[0], "__len__"):
+        flat = [flat] * steps
+    if len(flat) != steps or any(len(c) != 3 for c in flat):
+        raise ValueError("coeffs must be one (a, b, c) or one for each step")
+    return array("f", [v for c in flat for v in c])
+
+
+def _orthogonalize(grad, momentum, new_momentum, beta, nesterov, steps, coeffs, eps, scale, ws, out):
+    code = _row_code(grad, "grad")
+    dev, shape = grad.device, grad.shape
+    if len(shape) not in (2, 3):
+        raise ValueError("grad must be [rows, cols] or [L, rows, cols]")
+    L, rows, cols = (1, *shape) if len(shape) == 2 else shape
+    _need_shape(grad, "grad", grad.dtype, dev, shape)
+    mom_code, mp, np_ = code, None, None
+    if momentum is not None:
+        mom_code = _row_code(momentum, "momentum")
+        _need_shape(momentum, "momentum", momentum.dtype, dev, shape)
+        mp = np_ = momentum.data_ptr()
+        if new_momentum is not None:
+            _need_shape(new_momentum, "new_momentum", momentum.dtype, dev, shape)
+            np_ = new_momentum.data_ptr()
+    flat = _coefficients(coeffs, steps)
+    if out is None:
+        out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+    else:
+        _need_shape(out, "out", torch.bfloat16, dev, shape)
+    if ws is None:
+        ws = workspace(orthogonalize_workspace_size(L, rows, cols), dev)
+    _lib.check(_lib.load().eas_orthogonalize(
+        grad.data_ptr(), code, mp, np_, mom_code, L, rows, cols, beta, 1 if nesterov else 0,
+        flat.buffer_info()[0], steps, eps, scale, out.data_ptr(), *_ws_args(ws, dev), _stream(dev)))
+    return out
+
+
+def orthogonalize(grad, steps: int = 5, coeffs=NEWTON_SCHULZ, eps: float = 1e-7, scale: float = 1.0,
+                  ws=None, out=None):
+    """scale times the orthogonalised matrix (or stack of matrices, [L, rows, cols]):
+    grad over its 2-norm, then `steps` Newton-Schulz products.  bf16.
+
+    coeffs: (a, b, c) of every step, or one triple for each."""
+    return _orthogonalize(grad, None, None, 0.0, False, steps, coeffs, eps, scale, ws, out)
+
+
+def muon_update(grad, momentum, beta: float = 0.95, nesterov: bool = True, steps: int = 5,
+                coeffs=NEWTON_SCHULZ, eps: float = 1e-7, scale: float = 1.0, new_momentum=None,
+                ws=None, out=None):
+    """One Muon update: momentum = beta momentum + (1 - beta) grad, in place or into
+    new_momentum; returns scale times the orthogonalised momentum (with nesterov, of
+    beta momentum + (1 - beta) grad) in bf16, for param.sub_(update, alpha=lr).
+
+    grad and momentum are [rows, cols] or a stack [L, rows, cols], each bf16 or fp32."""
+    if momentum is None:
+        raise ValueError("momentum must be a tensor (orthogonalize takes none)")
+    return _orthogonalize(grad, momentum, new_momentum, beta, nesterov, steps, coeffs, eps, scale,
+                          ws, out)

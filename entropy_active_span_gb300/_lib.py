@@ -74,6 +74,9 @@ SIGNATURES = {
                                               ctypes.c_int, _F32, _P, _P, _P, _P, _P, _P, _SZ, _P]),
     "eas_token_logprobs_bwd": (ctypes.c_int, [_P, _P, _P, _I64, _P, _P, _P, _P, _I64, _I64, _I64,
                                               ctypes.c_int, _F32, _P, _I64, _P, _SZ, _P]),
+    "eas_orthogonalize_workspace_size": (_SZ, [_I64, _I64, _I64]),
+    "eas_orthogonalize": (ctypes.c_int, [_P, ctypes.c_int, _P, _P, ctypes.c_int, _I64, _I64, _I64,
+                                         ctypes.c_double, _I32, _P, _I32, _F32, _F32, _P, _P, _SZ, _P]),
     "eas_selftest_wait_timeout": (ctypes.c_int, [_I64, _P, _SZ, _P]),
     "eas_read_device_status": (ctypes.c_int, [_P, _P]),
     "eas_trace_enable": (None, [_I32]),

@@ -23,7 +23,8 @@ const char* const kTraceNames[kTrCount] = {
     "dlogits_gemm_simt", "dhidden_gemm_simt", "dweight_gemm_simt", "memset",
     "bwd_chunk_gemm_tc", "dlogits_gemm_tc_e4m3",
     "rmsnorm_fwd", "rmsnorm_bwd", "rmsnorm_dweight", "embed_fwd", "embed_sort", "embed_bwd",
-    "grad_norm", "clip_grad_norm", "token_logprobs_fwd", "token_logprobs_bwd"};
+    "grad_norm", "clip_grad_norm", "token_logprobs_fwd", "token_logprobs_bwd",
+    "orthogonalize"};
 
 }  // namespace
 

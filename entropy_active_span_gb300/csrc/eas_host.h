@@ -52,7 +52,7 @@ enum TraceKind : int {
   kTrDLogitsGemm, kTrDProjGemm, kTrUnused, kTrSimtFwd, kTrSimtDLogits,
   kTrSimtDHidden, kTrSimtDWeight, kTrMemset, kTrBwdChunkGemm, kTrDLogitsFp8Gemm,
   kTrNormFwd, kTrNormBwd, kTrNormDw, kTrEmbedFwd, kTrEmbedSort, kTrEmbedBwd, kTrGradNorm,
-  kTrGradClip, kTrScoreFwd, kTrScoreBwd, kTrCount
+  kTrGradClip, kTrScoreFwd, kTrScoreBwd, kTrMuon, kTrCount
 };
 
 class Trace {

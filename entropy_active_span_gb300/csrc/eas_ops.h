@@ -2,6 +2,9 @@
 // ABI).
 #pragma once
 
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -136,5 +139,47 @@ struct ScoreBwdArgs {
   int split;
 };
 cudaError_t launch_score_bwd(const ScoreBwdArgs& a, int is_bf16, int num_sms, cudaStream_t s);
+
+// ---- orthogonalised update (eas_muon.cu) ----
+struct MuonPlan {         // sizes of the workspace, in bytes from its start
+  size_t partial;         // double [L][chunks]
+  size_t x[4];            // X's two pairs: hi, lo, hi, lo; u [L][rows][cols] fp32 from x[2] on
+  size_t gram, poly;
+  size_t total;
+  long long ldx, lda;     // row pitches in elements
+  long long chunk, chunks;
+};
+MuonPlan muon_plan(long long L, long long rows, long long cols);
+struct MuonPair {
+  __half* hi;
+  __half* lo;
+};
+struct MuonArgs {
+  const void* grad;       // [L][rows][cols]
+  const void* mom;        // or null
+  void* new_mom;          // may be mom
+  int mom_bf16;
+  int rows, cols, L;
+  int n, m, tall;         // X [n][m], n <= m; tall: the transpose of what came
+  float beta, rest;       // rest = 1 - beta
+  int nesterov;
+  float eps, scale;
+  const float* coeffs;    // host, [steps][3]
+  int steps;
+  __nv_bfloat16* out;     // [L][rows][cols]
+  double* partial;
+  int chunk, chunks;
+  float* u;
+  MuonPair x[2];
+  __half* gram;           // A
+  __half* poly;           // B
+  long long ldx, lda;
+  DevStatus* status;
+  long long budget;       // clocks a wait may take
+};
+typedef CUresult (*MapEncoder)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                               const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                               CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+cudaError_t launch_muon(const MuonArgs& a, int grad_bf16, MapEncoder enc, int num_sms, cudaStream_t s);
 
 }  // namespace eas

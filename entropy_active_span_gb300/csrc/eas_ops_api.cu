@@ -4,6 +4,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <cstdlib>
 #include <initializer_list>
 #include <new>
 #include <vector>
@@ -75,6 +76,32 @@ eas_status check_scores(long long N, long long V, long long M, long long ld, eas
   if (dt != EAS_BF16 && dt != EAS_FP32) return fail(EAS_ERR_INVALID_ARG, "dtype %d", (int)dt);
   if (!(scale > 0.f) || !std::isfinite(scale)) return fail(EAS_ERR_INVALID_ARG, "scale must be positive");
   return EAS_OK;
+}
+
+// Clocks that a pipeline wait may take, as in the LM head's kernels.
+long long wait_budget() {
+  static const long long b = [] {
+    const char* s = getenv("EAS_WAIT_BUDGET_CYCLES");
+    const long long v = s ? atoll(s) : 0;
+    return v > 0 ? v : (1LL << 31);
+  }();
+  return b;
+}
+
+// The driver's encoder of tensor maps (no link to libcuda), or null.
+MapEncoder map_encoder() {
+  static const MapEncoder f = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
+    const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q);
+    return e == cudaSuccess && q == cudaDriverEntryPointSuccess ? reinterpret_cast<MapEncoder>(p) : nullptr;
+  }();
+  return f;
+}
+
+bool muon_sizes(long long L, long long rows, long long cols) {
+  if (L < 0 || L > 65535 || rows < 1 || rows > EAS_MAX_MUON_SIDE || cols < 1 || cols > EAS_MAX_MUON_SIDE) return false;
+  return L * ((rows + 127) / 128) * ((cols + 127) / 128) < (1LL << 30);
 }
 
 }  // namespace
@@ -357,6 +384,84 @@ eas_status eas_token_logprobs_bwd(const float* g_logprob, const float* g_entropy
                           static_cast<DevStatus*>(ws), 1};
   Trace tr_(kTrScoreBwd, s);
   EAS_CUDA(launch_score_bwd(a, dtype == EAS_BF16, di.sms, s), "token_logprobs_bwd");
+  return EAS_OK;
+}
+
+size_t eas_orthogonalize_workspace_size(int64_t L, int64_t rows, int64_t cols) {
+  return muon_sizes(L, rows, cols) ? muon_plan(L, rows, cols).total : 0;
+}
+
+eas_status eas_orthogonalize(const void* grad, eas_dtype grad_dtype, const void* momentum,
+                             void* new_momentum, eas_dtype momentum_dtype, int64_t L, int64_t rows,
+                             int64_t cols, double beta, int32_t nesterov, const float* coeffs,
+                             int32_t steps, float eps, float scale, void* out, void* ws,
+                             size_t ws_bytes, void* stream) {
+  if (!muon_sizes(L, rows, cols))
+    return fail(EAS_ERR_INVALID_ARG, "[%lld][%lld][%lld] out of range", (long long)L, (long long)rows, (long long)cols);
+  if (grad_dtype != EAS_BF16 && grad_dtype != EAS_FP32) return fail(EAS_ERR_INVALID_ARG, "dtype %d", (int)grad_dtype);
+  if ((momentum == nullptr) != (new_momentum == nullptr))
+    return fail(EAS_ERR_INVALID_ARG, "momentum and new_momentum come together");
+  if (momentum && momentum_dtype != EAS_BF16 && momentum_dtype != EAS_FP32)
+    return fail(EAS_ERR_INVALID_ARG, "dtype %d", (int)momentum_dtype);
+  if (momentum && !(beta >= 0.f && beta <= 1.f)) return fail(EAS_ERR_INVALID_ARG, "beta must be in [0, 1]");
+  if (nesterov != 0 && nesterov != 1) return fail(EAS_ERR_INVALID_ARG, "nesterov must be 0 or 1");
+  if (steps < 1 || steps > EAS_MAX_MUON_STEPS) return fail(EAS_ERR_INVALID_ARG, "steps=%d out of range", steps);
+  if (!coeffs || !ws || (L > 0 && (!grad || !out))) return fail(EAS_ERR_INVALID_ARG, "null pointer");
+  for (int i = 0; i < 3 * steps; ++i)
+    if (!std::isfinite(coeffs[i])) return fail(EAS_ERR_INVALID_ARG, "coefficients must be finite");
+  if (!(eps > 0.f) || !std::isfinite(eps)) return fail(EAS_ERR_INVALID_ARG, "eps must be positive");
+  if (!std::isfinite(scale)) return fail(EAS_ERR_INVALID_ARG, "scale must be finite");
+  const size_t ge = elem_size(grad_dtype), me = momentum ? elem_size(momentum_dtype) : 4;
+  if (!aligned(grad, ge) || !aligned(momentum, me) || !aligned(new_momentum, me) || !aligned(out, 2) || !aligned(ws, 256))
+    return fail(EAS_ERR_INVALID_ARG, "tensors must be aligned to their elements and ws to 256 bytes");
+  const MuonPlan p = muon_plan(L, rows, cols);
+  if (ws_bytes < p.total) return fail(EAS_ERR_WORKSPACE, "workspace %zu < %zu", ws_bytes, p.total);
+  const size_t n = static_cast<size_t>(L) * static_cast<size_t>(rows) * static_cast<size_t>(cols);
+  if (!disjoint({{new_momentum, n * me, true}, {out, 2 * n}, {ws, p.total}},
+                {{grad, n * ge}, {momentum, n * me, true}}))
+    return overlap_error();
+  DevInfo di;
+  eas_status st = device_info(&di);
+  if (st != EAS_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (L == 0) {
+    EAS_CUDA(cudaMemsetAsync(ws, 0, sizeof(DevStatus), s), "clear status");
+    return EAS_OK;
+  }
+  const MapEncoder enc = map_encoder();
+  if (!enc) return fail(EAS_ERR_CUDA, "cuTensorMapEncodeTiled unavailable");
+  MuonArgs a = {};
+  a.grad = grad;
+  a.mom = momentum;
+  a.new_mom = new_momentum;
+  a.mom_bf16 = momentum_dtype == EAS_BF16;
+  a.rows = static_cast<int>(rows);
+  a.cols = static_cast<int>(cols);
+  a.L = static_cast<int>(L);
+  a.tall = rows > cols;
+  a.n = a.tall ? a.cols : a.rows;
+  a.m = a.tall ? a.rows : a.cols;
+  a.beta = static_cast<float>(beta);
+  a.rest = static_cast<float>(1. - beta);      // of the fp64 beta: 1 - fp32(beta) is 2.4e-7 off at 0.9
+  a.nesterov = nesterov;
+  a.eps = eps;
+  a.scale = scale;
+  a.coeffs = coeffs;
+  a.steps = steps;
+  a.out = static_cast<__nv_bfloat16*>(out);
+  a.partial = at<double>(ws, p.partial);
+  a.chunk = static_cast<int>(p.chunk);
+  a.chunks = static_cast<int>(p.chunks);
+  a.u = at<float>(ws, p.x[2]);
+  for (int i = 0; i < 2; ++i) a.x[i] = {at<__half>(ws, p.x[2 * i]), at<__half>(ws, p.x[2 * i + 1])};
+  a.gram = at<__half>(ws, p.gram);
+  a.poly = at<__half>(ws, p.poly);
+  a.ldx = p.ldx;
+  a.lda = p.lda;
+  a.status = static_cast<DevStatus*>(ws);
+  a.budget = wait_budget();
+  Trace tr_(kTrMuon, s);
+  EAS_CUDA(launch_muon(a, grad_dtype == EAS_BF16, enc, di.sms, s), "orthogonalize");
   return EAS_OK;
 }
 

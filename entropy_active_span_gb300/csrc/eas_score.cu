@@ -465,7 +465,6 @@ __device__ __forceinline__ void store_cta0(const float* p, float v) {
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 2) score_fwd_kernel(const ScoreFwdArgs a) {
   __shared__ Shared sm;
-  constexpr int VEC = kVec16<T>;
   const int split = a.split, rank = split > 1 ? blockIdx.x % split : 0;
   const long long row = blockIdx.x / split;
   const int nt = blockDim.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;

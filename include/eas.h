@@ -361,7 +361,7 @@ eas_status eas_lmhead_fwd_noalloc(const void* hidden, const void* weight,
                                   void* stream);
 
 /*
- * In the calls from here to eas_token_logprobs_bwd no output and no workspace may
+ * In the calls from here to eas_orthogonalize no output and no workspace may
  * share a byte with another buffer of the call, except where an argument says
  * that it may replace another (EAS_ERR_INVALID_ARG).
  */
@@ -521,6 +521,45 @@ eas_status eas_token_logprobs_bwd(const float* g_logprob, const float* g_entropy
                                   int64_t N, int64_t V, int64_t M, eas_dtype dtype, float scale,
                                   void* dlogits, int64_t ld_dlogits, void* ws, size_t ws_bytes,
                                   void* stream);
+
+/* ------------------------------------------------- orthogonalised update */
+
+/*
+ * Update of L matrices [rows][cols] by momentum and Newton-Schulz products (the
+ * step of the Muon optimiser, behind the clipping):
+ *   m' = beta m + (1 - beta) g,  u = nesterov ? beta m' + (1 - beta) g : m'
+ *   (u = g without a momentum);  X = u / (|u| + eps), the 2-norm over the matrix;
+ *   for each (a, b, c) of coeffs:  Q = X X^T,  X = a X + (b Q + c Q Q) X;
+ *   out = bf16(scale X).
+ * Products take fp16 operands (X itself is kept in 22 bits) and fp32 sums: out is
+ * within about 2e-3 of its norm, its rounding to bf16 alone being 1.7e-3.  Singular
+ * values have to stay below 4 through all steps, and |a| + |b| s^2 + |c| s^4 below 16
+ * (with the usual coefficients they stay below 1.3).  Results repeat to the bit.  Where
+ * a matrix holds NaN or Inf, or its norm is not finite, its out is NaN.
+ *
+ *   grad     [L][rows][cols] bf16 or fp32 (grad_dtype), contiguous, like the others
+ *   momentum, new_momentum : [L][rows][cols] bf16 or fp32 (momentum_dtype) in and
+ *            out, or both NULL.  new_momentum may be momentum itself.  u is taken
+ *            from m' before it is rounded.
+ *   beta     in [0, 1]; nesterov 0 or 1
+ *   coeffs   HOST array [steps][3], copied before the call returns;
+ *            1 <= steps <= EAS_MAX_MUON_STEPS
+ *   eps      > 0 (a zero matrix gives zeros)
+ *   out      [L][rows][cols] bf16
+ *   ws       eas_orthogonalize_workspace_size(L, rows, cols) bytes, about
+ *            8 + 4 n / m bytes an element for n <= m; holds the status word
+ * rows and cols are at most EAS_MAX_MUON_SIDE, L at most 65535.
+ */
+#define EAS_MAX_MUON_SIDE 65536
+#define EAS_MAX_MUON_STEPS 32
+
+size_t eas_orthogonalize_workspace_size(int64_t L, int64_t rows, int64_t cols);
+
+eas_status eas_orthogonalize(const void* grad, eas_dtype grad_dtype, const void* momentum,
+                             void* new_momentum, eas_dtype momentum_dtype, int64_t L, int64_t rows,
+                             int64_t cols, double beta, int32_t nesterov, const float* coeffs,
+                             int32_t steps, float eps, float scale, void* out, void* ws,
+                             size_t ws_bytes, void* stream);
 
 /* ------------------------------------------------------------- utilities */
 
