@@ -40,6 +40,15 @@ __device__ __forceinline__ void arrive_at(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
+// Writes `v` to the same place of CTA 1's shared memory and arrives on its barrier.
+__device__ __forceinline__ void send_to_peer(const int* p, int v, const uint64_t* bar) {
+  uint32_t pa, ba;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, 1;" : "=r"(pa) : "r"(smem_u32(p)));
+  asm volatile("mapa.shared::cluster.u32 %0, %1, 1;" : "=r"(ba) : "r"(smem_u32(bar)));
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(pa), "r"(v) : "memory");
+  arrive_at(ba);
+}
+
 __device__ __forceinline__ bool try_wait(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
@@ -65,6 +74,11 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile in
     }
   }
   return true;
+}
+
+// The same by a whole warp, whose lanes go on or give up together.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort, long long budget) {
+  return __all_sync(0xffffffffu, wait(bar, parity, abort, budget));
 }
 
 // TMA loads into this CTA's shared memory, their bytes counted on the leader's

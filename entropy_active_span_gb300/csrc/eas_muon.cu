@@ -136,6 +136,11 @@ __global__ void __launch_bounds__(kPrepThreads) muon_update_kernel(const MuonArg
     a.partial[blockIdx.y * gridDim.x + blockIdx.x] = sum;
     if (blockIdx.x == 0 && blockIdx.y == 0) *a.status = DevStatus{0, 0, 0, 0};
   }
+  // the products' counters
+  const long long cta = static_cast<long long>(blockIdx.y) * gridDim.x + blockIdx.x;
+  for (long long i = cta * kPrepThreads + threadIdx.x; i < a.sync_words;
+       i += static_cast<long long>(gridDim.x) * gridDim.y * kPrepThreads)
+    a.sync[i] = 0;
 }
 
 // X's first pair: u (or the gradient) times 2^12 / (norm + eps), transposed where it
@@ -184,14 +189,31 @@ __global__ void __launch_bounds__(kPrepThreads) muon_scale_kernel(const MuonArgs
 }
 
 // ------------------------------------------------------------------ products
+//
+// All products of all steps run in one launch.  Their tiles form one list (step by
+// step: the tiles of A, of B, of X; each for all L matrices) that the CTAs draw from in
+// order; a tile waits, 128 or 256 k at a time, for the tiles of earlier products that
+// hold its operands.  Each tile has a counter for that: its storing warps add one when
+// their stores are visible.  So the last tiles of a product and the first of the next
+// one run side by side, and nothing is launched in between.  [4096][4096] takes 1.79 +
+// 1.79 + 3.37 rounds of 76 tiles a step instead of 2 + 2 + 4.
+//
+// No CTA waits for a tile that no running CTA has drawn, since tiles are drawn in
+// order and depend on earlier ones alone.  What a tile overwrites has no reader left
+// when its operands are there: A(i, j) of a step needs rows i and j of X, those need
+// rows i and j of the B before, and those all readers of the A(i, j) before; B and X
+// likewise.
 
 enum Kind { kGram, kPoly, kApply, kLast };
 
-constexpr int kThreads = 192;
-constexpr int kStages = 6;
+constexpr int kStoreWarps = 8;
+constexpr int kThreads = 64 + 32 * kStoreWarps;
+constexpr int kStages = 5;
+constexpr int kRing = 4;                           // tile numbers on their way to the warps
 constexpr int kOperand = 16384;                    // 128 rows (columns) x 64 k
 constexpr int kEpiWarp = 8192;                     // two boxes a warp
-constexpr int kSmem = kStages * 2 * kOperand + 4 * kEpiWarp + 1024 + 512;
+constexpr int kSmem = kStages * 2 * kOperand + kStoreWarps * kEpiWarp + 1024 + 512;
+constexpr int kBand = 4;                           // rows of tiles of X that are computed together
 
 // CG = 2: a pair of CTAs computes 256 x 256 tiles, each 128 of the rows; CG = 1: a CTA
 // 128 x 128 tiles.
@@ -199,35 +221,44 @@ template <int CG>
 struct Geo {
   static constexpr int kM = 128 * CG, kN = 128 * CG;
   static constexpr uint32_t kCols = 2 * kN;        // two accumulators
+  static constexpr int kChunk = 2 * CG;            // k-blocks of 64 in a tile's width
+  static constexpr int kDone = kStoreWarps * CG;   // arrivals that finish a tile
 };
 
 struct GemmArgs {
-  CUtensorMap ma, mb;       // operands
-  CUtensorMap s0, s1;       // stores: the tile; its transpose (Gram, Poly) or lo (Apply)
-  int n, m, L;              // extents of the result: n x n (Gram, Poly) or n x m
-  int num_kb;               // 64-deep k-blocks
-  int num_m, num_n, per;    // tiles a matrix
-  float ca, cb, cc;         // the step's coefficients
-  const __half* p0;         // Poly: A; Apply, Last: X hi
-  const __half* p1;         // Apply, Last: X lo
-  long long ld;             // their row pitch
-  __nv_bfloat16* out;       // Last
+  CUtensorMap xk[2], xn[2], xh[2], xl[2];   // X's pairs: rows as operand, columns as operand, stores
+  CUtensorMap ak, as, at, bk, bs, bt;       // A and B: operand, store, transposed store
+  const __half *hi[2], *lo[2], *gram;
+  long long ldx, lda;
+  int n, m, L, steps;
+  int num_m, num_n;                         // tiles down and across X
+  int tri, full;                            // tiles of A (or B), of X, a matrix
+  float coeffs[3 * kMuonSteps];
+  __nv_bfloat16* out;
   float scale;
   int tall;
+  int* counter;                             // next tile
+  int* done_a;                              // [L][num_m][num_m], upper triangle
+  int* done_b;
+  int* done_x;                              // [L][num_m][num_n]
   DevStatus* status;
   long long budget;
 };
 
 struct Tile {
-  int l, m, n;
+  int kind, step, l, m, n;
 };
 
-template <int kKind>
 __device__ __forceinline__ Tile tile_of(int t, const GemmArgs& a) {
   Tile w;
-  w.l = t / a.per;
-  t -= w.l * a.per;
-  if constexpr (kKind <= kPoly) {
+  const int per_step = a.L * (2 * a.tri + a.full);
+  w.step = t / per_step;
+  t -= w.step * per_step;
+  if (t < 2 * a.L * a.tri) {
+    w.kind = t < a.L * a.tri ? kGram : kPoly;
+    if (w.kind == kPoly) t -= a.L * a.tri;
+    w.l = t / a.tri;
+    t -= w.l * a.tri;
     // column by column of the upper triangle: n (n + 1) / 2 tiles before column n
     int n = static_cast<int>((sqrtf(8.f * t + 1.f) - 1.f) * 0.5f);
     while (n * (n + 1) / 2 > t) --n;
@@ -235,11 +266,41 @@ __device__ __forceinline__ Tile tile_of(int t, const GemmArgs& a) {
     w.n = n;
     w.m = t - n * (n + 1) / 2;
   } else {
-    // the tiles of one column strip of X together: they share its k-blocks
-    w.n = t / a.num_m;
-    w.m = t - w.n * a.num_m;
+    w.kind = w.step + 1 < a.steps ? kApply : kLast;
+    t -= 2 * a.L * a.tri;
+    w.l = t / a.full;
+    t -= w.l * a.full;
+    // bands of rows, column by column: the next step's first tiles need the first
+    // rows alone, and a band's tiles share X's columns
+    const int band = t / (kBand * a.num_n), height = min(kBand, a.num_m - band * kBand);
+    t -= band * kBand * a.num_n;
+    w.n = t / height;
+    w.m = band * kBand + t - w.n * height;
   }
   return w;
+}
+
+__device__ __forceinline__ int acquire(const int* p) {
+  int v;
+  asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ void release_add(int* p) {
+  asm volatile("red.release.gpu.global.add.s32 [%0], 1;" ::"l"(p) : "memory");
+}
+// Orders this thread's acquired or released values with its TMA loads or stores.
+__device__ __forceinline__ void fence_async_global() { asm volatile("fence.proxy.async.global;" ::: "memory"); }
+
+// Counter of the operand that a tile reads at chunk c of k: its first operand's
+// (which = 0) or its second one's.  null: none to wait for.
+template <int CG>
+__device__ __forceinline__ const int* operand_counter(const Tile& w, int c, int which, const GemmArgs& a) {
+  const int row = which ? w.n : w.m;
+  if (which && (w.kind >= kApply || w.m == w.n)) return nullptr;   // Apply: B's row waits for all of X
+  if (w.kind == kGram)
+    return w.step ? a.done_x + static_cast<long long>(w.l) * a.full + row * a.num_n + c : nullptr;
+  return (w.kind == kPoly ? a.done_a : a.done_b) + static_cast<long long>(w.l) * a.num_m * a.num_m +
+         min(row, c) * a.num_m + max(row, c);
 }
 
 // 64 columns of this thread's accumulator row.
@@ -248,17 +309,17 @@ __device__ __forceinline__ void load64(uint32_t taddr, float (&v)[64]) {
   tmem_ld32(taddr + 32, *reinterpret_cast<float(*)[32]>(&v[32]));
 }
 
-// 64 fp16 values of a row in global memory.
-__device__ __forceinline__ void row64(const __half* p, uint4 (&r)[8]) {
-#pragma unroll
-  for (int j = 0; j < 8; ++j) r[j] = reinterpret_cast<const uint4*>(p)[j];
-}
 __device__ __forceinline__ float2 pair_of(const uint4 (&r)[8], int i) {
   const uint32_t w[4] = {r[i / 4].x, r[i / 4].y, r[i / 4].z, r[i / 4].w};
   return __half22float2(*reinterpret_cast<const __half2*>(&w[i % 4]));
 }
 
-// The row of a [32][64] fp16 box in the 128-byte swizzled layout: value pair i.
+// The row of a [32][64] fp16 box in the 128-byte swizzled layout.
+__device__ __forceinline__ void get_box(const uint8_t* box, int lane, uint4 (&r)[8]) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    r[j] = *reinterpret_cast<const uint4*>(box + lane * 128 + ((j ^ (lane & 7)) << 4));
+}
 __device__ __forceinline__ void put_box(uint8_t* box, int lane, const uint32_t (&w)[32]) {
 #pragma unroll
   for (int j = 0; j < 8; ++j)
@@ -271,29 +332,64 @@ __device__ __forceinline__ uint32_t half2_bits(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// One warp's 32 rows (from row0 on; this thread's is row0 + lane) of a tile whose
-// first column is n0.
-template <int kKind, int kTileN>
-__device__ __forceinline__ void epilogue(const GemmArgs& a, const Tile& w, uint32_t tbase, int row0, int n0,
-                                         int lane, uint8_t* box) {
+// What a storing warp keeps: its two boxes, their load barrier and its phase.
+struct Boxes {
+  uint8_t* box;
+  uint64_t* bar;
+  uint32_t phase;
+};
+
+// Lane 0: the values of X (hi and lo) or A that the tile's columns from `col` on add to
+// their products, to the warp's boxes.
+template <int kKind>
+__device__ __forceinline__ void fetch(const GemmArgs& a, const Tile& w, const Boxes& b, int row0, int col) {
+  if constexpr (kKind == kGram) return;
+  mbar_arrive_expect_tx(b.bar, kKind == kPoly ? 4096 : 8192);
+  const int from = w.step & 1;
+  mma::load_3d<1>(b.box, kKind == kPoly ? &a.as : &a.xh[from], smem_u32(b.bar), col, row0, w.l);
+  if constexpr (kKind >= kApply) mma::load_3d<1>(b.box + 4096, &a.xl[from], smem_u32(b.bar), col, row0, w.l);
+}
+
+// A warp's 32 rows (from row0 on; this thread's is row0 + lane) and kCols columns
+// (from n0 on) of a tile.  The first columns' values have been fetched.
+template <int kKind, int kCols>
+__device__ __forceinline__ bool epilogue(const GemmArgs& a, const Tile& w, uint32_t tbase, int row0, int n0,
+                                         int lane, Boxes& b, volatile int* abort_flag) {
   const int width = kKind <= kPoly ? a.n : a.m;
   const int row = row0 + lane;
   const bool mirror = kKind <= kPoly && w.m != w.n;
+  const int to = (w.step & 1) ^ 1;
+  const float* abc = a.coeffs + 3 * w.step;
+  // Poly: b A + c A A; Apply, Last: a X + B X
+  const float f = kKind == kPoly ? abc[1] : abc[0], g = kKind == kPoly ? abc[2] * kDown : kDown;
+  const CUtensorMap* s0 = kKind == kGram ? &a.as : kKind == kPoly ? &a.bs : &a.xh[to];
+  const CUtensorMap* s1 = kKind == kGram ? &a.at : kKind == kPoly ? &a.bt : &a.xl[to];
+  uint8_t* box = b.box;
 #pragma unroll 1
-  for (int c = 0; c < kTileN / 64; ++c) {
+  for (int c = 0; c < kCols / 64; ++c) {
     const int col = n0 + c * 64;
     if (col >= width || row0 >= a.n) break;        // the same for the warp
+    if (c) {
+      // the boxes have been read (and, Last, written by the lanes) before they are
+      // filled again
+      if constexpr (kKind == kLast) fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        if constexpr (kKind != kLast) mma::stores_read();
+        fetch<kKind>(a, w, b, row0, col);
+      }
+    }
     float v[64];
     load64(tbase + c * 64, v);
     if constexpr (kKind == kGram) {
 #pragma unroll
       for (int j = 0; j < 64; ++j) v[j] *= kDown;
+      __syncwarp();                                // lane 0 has waited for the boxes
     } else {
-      // rows past the end read the last one; they are not stored
-      const long long o = (static_cast<long long>(w.l) * a.n + min(row, a.n - 1)) * a.ld + col;
+      if (!mma::warp_wait(b.bar, b.phase, abort_flag, a.budget)) return false;
+      b.phase ^= 1u;
       uint4 r[8];
-      row64(a.p0 + o, r);
-      const float f = kKind == kPoly ? a.cb : a.ca, g = kKind == kPoly ? a.cc * kDown : kDown;
+      get_box(box, lane, r);
 #pragma unroll
       for (int j = 0; j < 32; ++j) {
         const float2 x = pair_of(r, j);
@@ -301,7 +397,7 @@ __device__ __forceinline__ void epilogue(const GemmArgs& a, const Tile& w, uint3
         v[2 * j + 1] = fmaf(v[2 * j + 1], g, f * x.y);
       }
       if constexpr (kKind >= kApply) {
-        row64(a.p1 + o, r);
+        get_box(box + 4096, lane, r);
 #pragma unroll
         for (int j = 0; j < 32; ++j) {
           const float2 x = pair_of(r, j);
@@ -309,22 +405,22 @@ __device__ __forceinline__ void epilogue(const GemmArgs& a, const Tile& w, uint3
           v[2 * j + 1] = fmaf(f, x.y, v[2 * j + 1]);
         }
       }
+      __syncwarp();                                // Poly's transposed box and Last's pairs lie across rows
     }
     if constexpr (kKind == kLast) {
-      const float f = a.scale * kDown;
+      const float up = a.scale * kDown;
       if (a.tall) {
         // X's rows are the output's columns: 32 lanes store 64 bytes in a row
         if (row < a.n) {
 #pragma unroll
           for (int j = 0; j < 64; ++j)
             if (col + j < a.m)
-              a.out[(static_cast<long long>(w.l) * a.m + col + j) * a.n + row] = __float2bfloat16_rn(v[j] * f);
+              a.out[(static_cast<long long>(w.l) * a.m + col + j) * a.n + row] = __float2bfloat16_rn(v[j] * up);
         }
       } else {
         uint32_t* s = reinterpret_cast<uint32_t*>(box);      // [32][33] pairs
-        __syncwarp();
 #pragma unroll
-        for (int j = 0; j < 32; ++j) s[lane * 33 + j] = pack_bf16x2(v[2 * j] * f, v[2 * j + 1] * f);
+        for (int j = 0; j < 32; ++j) s[lane * 33 + j] = pack_bf16x2(v[2 * j] * up, v[2 * j + 1] * up);
         __syncwarp();
         const bool even = (a.m & 1) == 0 && (reinterpret_cast<uintptr_t>(a.out) & 3u) == 0;
         const int cc = col + 2 * lane;
@@ -346,8 +442,6 @@ __device__ __forceinline__ void epilogue(const GemmArgs& a, const Tile& w, uint3
       uint32_t hi[32];
 #pragma unroll
       for (int j = 0; j < 32; ++j) hi[j] = half2_bits(v[2 * j], v[2 * j + 1]);
-      if (lane == 0) mma::stores_read();             // the boxes' last stores have read them
-      __syncwarp();
       put_box(box, lane, hi);
       if constexpr (kKind == kApply) {
         uint32_t lo[32];
@@ -370,19 +464,20 @@ __device__ __forceinline__ void epilogue(const GemmArgs& a, const Tile& w, uint3
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
-        mma::store_3d(&a.s0, box, col, row0, w.l);
-        if constexpr (kKind == kApply) mma::store_3d(&a.s1, box + 4096, col, row0, w.l);
-        else if (mirror) mma::store_3d(&a.s1, box + 4096, row0, col, w.l);
+        mma::store_3d(s0, box, col, row0, w.l);
+        if constexpr (kKind == kApply) mma::store_3d(s1, box + 4096, col, row0, w.l);
+        else if (mirror) mma::store_3d(s1, box + 4096, row0, col, w.l);
         mma::store_commit();
       }
     }
   }
+  return true;
 }
 
-// Persistent: CTA (pair) p computes tiles p, p + grid, ...  Warp 0 loads, warp 1
-// issues the MMAs, warps 2 to 5 store; two accumulators, so that a tile's store runs
-// under the next one's products.
-template <int CG, int kKind>
+// Warp 0 draws tiles, waits for their operands and loads them, warp 1 issues the MMAs,
+// warps 2 to 9 store (two for each 32 rows, half of the columns each); two accumulators, so that a tile's stores run under the next
+// one's products.
+template <int CG>
 __global__ void __launch_bounds__(kThreads, 1) muon_gemm_kernel(const __grid_constant__ GemmArgs a) {
   using G = Geo<CG>;
   extern __shared__ uint8_t smem_raw[];
@@ -391,13 +486,18 @@ __global__ void __launch_bounds__(kThreads, 1) muon_gemm_kernel(const __grid_con
   uint8_t* s_a = smem;
   uint8_t* s_b = smem + kStages * kOperand;
   uint8_t* s_epi = s_b + kStages * kOperand;
-  uint64_t* full = reinterpret_cast<uint64_t*>(s_epi + 4 * kEpiWarp);
+  uint64_t* full = reinterpret_cast<uint64_t*>(s_epi + kStoreWarps * kEpiWarp);
   uint64_t* empty = full + kStages;
   uint64_t* tfull = empty + kStages;
   uint64_t* tempty = tfull + 2;
-  uint64_t* drain = tempty + 2;
-  uint32_t* slot = reinterpret_cast<uint32_t*>(drain + 1);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(slot + 1);
+  uint64_t* rfull = tempty + 2;
+  uint64_t* rempty = rfull + kRing;
+  uint64_t* there = rempty + kRing;        // of the tile in a ring slot: its operands
+  uint64_t* fetched = there + kRing;       // of a storing warp: what it adds
+  uint64_t* drain = fetched + kStoreWarps;
+  int* ring = reinterpret_cast<int*>(drain + 1);
+  uint32_t* slot_addr = reinterpret_cast<uint32_t*>(ring + kRing);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(slot_addr + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = mma::rank_in_pair<CG>();
@@ -409,83 +509,156 @@ __global__ void __launch_bounds__(kThreads, 1) muon_gemm_kernel(const __grid_con
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&tfull[i], 1);
-      mbar_init(&tempty[i], 4 * CG);
+      mbar_init(&tempty[i], kStoreWarps * CG);
     }
+    for (int i = 0; i < kRing; ++i) {
+      mbar_init(&rfull[i], 1);
+      mbar_init(&rempty[i], (1 + kStoreWarps) * CG);   // MMA warp (CTA 1: loader), storing warps
+      mbar_init(&there[i], 1);
+    }
+    for (int i = 0; i < kStoreWarps; ++i) mbar_init(&fetched[i], 1);
     mbar_init(drain, 1);
     *abort_flag = 0;
     fence_barrier_init();
     fence_proxy_async_smem();
-    tma_prefetch_desc(&a.ma);
-    tma_prefetch_desc(&a.mb);
   }
-  if (warp == 1) mma::tmem_alloc<CG, G::kCols>(slot);
+  if (warp == 1) mma::tmem_alloc<CG, G::kCols>(slot_addr);
   tc_fence_before();
   mma::sync_pair<CG>();
   tc_fence_after();
-  const uint32_t tmem = *slot;
-  // the set-up above overlaps the launch before; nothing of its output is read
-  // earlier
-  wait_for_launch_before();
-  launch_dependents();
+  const uint32_t tmem = *slot_addr;
+  const int total = a.steps * a.L * (2 * a.tri + a.full);
+  const uint32_t rempty0 = mma::leader_addr<CG>(&rempty[0]);
 
-  const int total = a.per * a.L, step = gridDim.x / CG, first = blockIdx.x / CG;
   if (warp == 0) {
-    if (lane == 0) {
-      int stage = 0;
-      uint32_t phase = 0;
-      bool ok = true;
-      const uint32_t full0 = mma::leader_addr<CG>(&full[0]);
-      for (int t = first; ok && t < total; t += step) {
-        const Tile w = tile_of<kKind>(t, a);
-        const int mrow = w.m * G::kM + static_cast<int>(rank) * 128;
-        const int ncol = w.n * G::kN + static_cast<int>(rank) * 128;
-        for (int kb = 0; kb < a.num_kb; ++kb) {
-          if (!mma::wait(&empty[stage], phase ^ 1u, abort_flag, a.budget)) {
-            report(a.status, kStTimeout, kWhereMuon, t);
-            ok = false;
-            break;
+    int stage = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    const uint32_t full0 = mma::leader_addr<CG>(&full[0]);
+    for (int it = 0; ok; ++it) {
+      const int slot = it % kRing;
+      const uint32_t rph = (it / kRing) & 1;
+      int t = -1;
+      if (lane == 0) {
+        if (leader) {
+          ok = mma::wait(&rempty[slot], rph ^ 1u, abort_flag, a.budget);
+          if (ok) {
+            const int got = atomicAdd(a.counter, 1);
+            t = got < total ? got : -1;
+            ring[slot] = t;
+            mbar_arrive(&rfull[slot]);
+            if constexpr (CG == 2) mma::send_to_peer(&ring[slot], t, &rfull[slot]);
           }
-          const uint32_t bar = full0 + 8 * stage;
-          if (leader) mbar_arrive_expect_tx(&full[stage], CG * 2 * kOperand);
-          mma::load_3d<CG>(s_a + stage * kOperand, &a.ma, bar, kb * 64, mrow, w.l);
-          if constexpr (kKind <= kPoly)
-            mma::load_3d<CG>(s_b + stage * kOperand, &a.mb, bar, kb * 64, ncol, w.l);
-          else
-            mma::load_4d<CG>(s_b + stage * kOperand, &a.mb, bar, 0, kb * 64, ncol >> 6, w.l);
-          if (++stage == kStages) {
-            stage = 0;
-            phase ^= 1u;
+        } else {
+          ok = mma::wait(&rfull[slot], rph, abort_flag, a.budget);
+          if (ok) {
+            t = ring[slot];
+            mma::arrive_at(rempty0 + 8 * slot);
           }
         }
+        if (!ok) report(a.status, kStTimeout, kWhereMuon, it);
       }
-      if (!ok && leader) {
-        // loads on their way still land
-        for (int i = 0; i < kStages; ++i) {
-          const uint32_t par = i < stage ? phase : phase ^ 1u;
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      t = __shfl_sync(0xffffffffu, t, 0);
+      if (!ok || t < 0) break;
+      const Tile w = tile_of(t, a);
+      const int from = w.step & 1;
+      const CUtensorMap* ma = w.kind == kGram ? &a.xk[from] : w.kind == kPoly ? &a.ak : &a.bk;
+      const CUtensorMap* mb = w.kind == kGram ? &a.xk[from] : w.kind == kPoly ? &a.ak : &a.xn[from];
+      const int mrow = w.m * G::kM + static_cast<int>(rank) * 128;
+      const int ncol = w.n * G::kN + static_cast<int>(rank) * 128;
+      const int num_kb = ((w.kind == kGram ? a.m : a.n) + 63) / 64;
+      const int chunks = (num_kb + G::kChunk - 1) / G::kChunk;
+      const int want = G::kDone * (w.kind == kGram ? w.step : w.step + 1);
+      for (int c0 = 0; ok && c0 < chunks; c0 += 16) {
+        // lanes 0 to 15 watch the first operand's counters, 16 to 31 the second one's
+        const int mine = c0 + (lane & 15);
+        const int* at = mine < chunks ? operand_counter<CG>(w, mine, lane >> 4, a) : nullptr;
+        bool ready = !at || acquire(at) >= want;
+        unsigned have = __ballot_sync(0xffffffffu, ready);
+        for (int c = c0; ok && c < min(c0 + 16, chunks); ++c) {
+          const unsigned need = 0x10001u << (c - c0);
           const long long t0 = clock64();
-          while (!mma::try_wait(&full[i], par) && clock64() - t0 < a.budget) {
+          while ((have & need) != need) {
+            if (!ready) ready = acquire(at) >= want;
+            have = __ballot_sync(0xffffffffu, ready);
+            const bool stop = *abort_flag || clock64() - t0 > a.budget;
+            if (__any_sync(0xffffffffu, stop)) {
+              ok = (have & need) == need;
+              break;
+            }
           }
+          if (!ok) {
+            if (lane == 0) {
+              *abort_flag = 1;
+              report(a.status, kStTimeout, kWhereMuon + 1, t);
+            }
+            break;
+          }
+          __syncwarp();                    // the counters' acquires, for lane 0
+          if (lane == 0) {
+            fence_async_global();
+            if (c == chunks - 1) mbar_arrive(&there[slot]);
+            for (int kb = c * G::kChunk; kb < min((c + 1) * G::kChunk, num_kb); ++kb) {
+              if (!mma::wait(&empty[stage], phase ^ 1u, abort_flag, a.budget)) {
+                report(a.status, kStTimeout, kWhereMuon + 2, t);
+                ok = false;
+                break;
+              }
+              const uint32_t bar = full0 + 8 * stage;
+              if (leader) mbar_arrive_expect_tx(&full[stage], CG * 2 * kOperand);
+              mma::load_3d<CG>(s_a + stage * kOperand, ma, bar, kb * 64, mrow, w.l);
+              if (w.kind <= kPoly) mma::load_3d<CG>(s_b + stage * kOperand, mb, bar, kb * 64, ncol, w.l);
+              else mma::load_4d<CG>(s_b + stage * kOperand, mb, bar, 0, kb * 64, ncol >> 6, w.l);
+              if (++stage == kStages) {
+                stage = 0;
+                phase ^= 1u;
+              }
+            }
+          }
+          ok = __shfl_sync(0xffffffffu, ok, 0);
+        }
+      }
+    }
+    if (!ok && leader && lane == 0) {
+      // loads on their way still land
+      for (int i = 0; i < kStages; ++i) {
+        const uint32_t par = i < stage ? phase : phase ^ 1u;
+        const long long t0 = clock64();
+        while (!mma::try_wait(&full[i], par) && clock64() - t0 < a.budget) {
         }
       }
     }
   } else if (warp == 1) {
     if (leader && lane == 0) {
-      constexpr uint32_t idesc = mma::idesc_f16_f32(G::kM, G::kN, false, kKind > kPoly);
-      constexpr uint32_t b_lbo = kKind > kPoly ? 8192 : 16, b_step = kKind > kPoly ? 2048 : 32;
-      int stage = 0, it = 0;
+      int stage = 0;
       uint32_t phase = 0;
       bool ok = true;
-      for (int t = first; ok && t < total; t += step, ++it) {
+      for (int it = 0; ok; ++it) {
+        const int slot = it % kRing;
+        if (!mma::wait(&rfull[slot], (it / kRing) & 1, abort_flag, a.budget)) {
+          report(a.status, kStTimeout, kWhereMuon + 3, it);
+          break;
+        }
+        const int t = ring[slot];
+        mbar_arrive(&rempty[slot]);
+        if (t < 0) break;
+        const Tile w = tile_of(t, a);
+        const bool k_rows = w.kind > kPoly;        // X's rows are k
+        const int num_kb = ((w.kind == kGram ? a.m : a.n) + 63) / 64;
+        const uint32_t idesc = k_rows ? mma::idesc_f16_f32(G::kM, G::kN, false, true)
+                                      : mma::idesc_f16_f32(G::kM, G::kN, false, false);
+        const uint32_t b_lbo = k_rows ? 8192 : 16, b_step = k_rows ? 2048 : 32;
         const int buf = it & 1;
         if (!mma::wait(&tempty[buf], ((it >> 1) & 1) ^ 1u, abort_flag, a.budget)) {
-          report(a.status, kStTimeout, kWhereMuon + 1, t);
+          report(a.status, kStTimeout, kWhereMuon + 4, t);
           break;
         }
         tc_fence_after();
         const uint32_t d = tmem + buf * G::kN;
-        for (int kb = 0; kb < a.num_kb; ++kb) {
+        for (int kb = 0; kb < num_kb; ++kb) {
           if (!mma::wait(&full[stage], phase, abort_flag, a.budget)) {
-            report(a.status, kStTimeout, kWhereMuon + 2, t);
+            report(a.status, kStTimeout, kWhereMuon + 5, t);
             ok = false;
             break;
           }
@@ -509,23 +682,64 @@ __global__ void __launch_bounds__(kThreads, 1) muon_gemm_kernel(const __grid_con
       }
     }
   } else {
-    const int q = warp & 3;
-    uint8_t* box = s_epi + q * kEpiWarp;
+    const int q = warp & 3, half = (warp - 2) >> 2;
+    constexpr int kCols = G::kN / 2;
+    Boxes b = {s_epi + (warp - 2) * kEpiWarp, &fetched[warp - 2], 0};
     const uint32_t tempty0 = mma::leader_addr<CG>(&tempty[0]);
-    int it = 0;
-    for (int t = first; t < total; t += step, ++it) {
-      const Tile w = tile_of<kKind>(t, a);
+    for (int it = 0;; ++it) {
+      const int slot = it % kRing;
+      const uint32_t rph = (it / kRing) & 1;
+      if (!mma::warp_wait(&rfull[slot], rph, abort_flag, a.budget)) {
+        report(a.status, kStTimeout, kWhereMuon + 6, it);
+        break;
+      }
+      const int t = ring[slot];
+      if (t >= 0 && !mma::warp_wait(&there[slot], rph, abort_flag, a.budget)) {
+        report(a.status, kStTimeout, kWhereMuon + 7, t);
+        break;
+      }
+      __syncwarp();
+      if (lane == 0) mma::arrive_at(rempty0 + 8 * slot);
+      if (t < 0) break;
+      const Tile w = tile_of(t, a);
       const int buf = it & 1;
-      if (!mma::wait(&tfull[buf], (it >> 1) & 1, abort_flag, a.budget)) {
-        report(a.status, kStTimeout, kWhereMuon + 3, t);
+      const uint32_t tbase = tmem + (static_cast<uint32_t>(q * 32) << 16) + buf * G::kN + half * kCols;
+      const int row0 = w.m * G::kM + static_cast<int>(rank) * 128 + q * 32, n0 = w.n * G::kN + half * kCols;
+      if (lane == 0 && row0 < a.n && n0 < (w.kind <= kPoly ? a.n : a.m)) {
+        // the boxes are free: the tile before waited for its stores (and, Last, all
+        // lanes are through with theirs)
+        fence_async_global();
+        if (w.kind == kPoly) fetch<kPoly>(a, w, b, row0, n0);
+        else if (w.kind >= kApply) fetch<kApply>(a, w, b, row0, n0);
+      }
+      if (!mma::warp_wait(&tfull[buf], (it >> 1) & 1, abort_flag, a.budget)) {
+        report(a.status, kStTimeout, kWhereMuon + 8, t);
         break;
       }
       tc_fence_after();
-      epilogue<kKind, G::kN>(a, w, tmem + (static_cast<uint32_t>(q * 32) << 16) + buf * G::kN,
-                             w.m * G::kM + static_cast<int>(rank) * 128 + q * 32, w.n * G::kN, lane, box);
+      bool ok;
+      if (w.kind == kGram) ok = epilogue<kGram, kCols>(a, w, tbase, row0, n0, lane, b, abort_flag);
+      else if (w.kind == kPoly) ok = epilogue<kPoly, kCols>(a, w, tbase, row0, n0, lane, b, abort_flag);
+      else if (w.kind == kApply) ok = epilogue<kApply, kCols>(a, w, tbase, row0, n0, lane, b, abort_flag);
+      else ok = epilogue<kLast, kCols>(a, w, tbase, row0, n0, lane, b, abort_flag);
+      if (!ok) {
+        report(a.status, kStTimeout, kWhereMuon + 9, t);
+        break;
+      }
       tc_fence_before();
+      if (w.kind == kLast) fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mma::arrive_at(tempty0 + 8 * buf);
+      if (lane == 0) {
+        mma::arrive_at(tempty0 + 8 * buf);
+        if (w.kind != kLast) {
+          mma::stores_done();
+          fence_async_global();
+          const long long l = w.l;
+          release_add(w.kind == kApply ? a.done_x + l * a.full + w.m * a.num_n + w.n
+                                       : (w.kind == kGram ? a.done_a : a.done_b) + l * a.num_m * a.num_m +
+                                             w.m * a.num_m + w.n);
+        }
+      }
     }
     if (lane == 0) mma::stores_done();
   }
@@ -535,26 +749,6 @@ __global__ void __launch_bounds__(kThreads, 1) muon_gemm_kernel(const __grid_con
     tc_fence_after();
     mma::tmem_free<CG, G::kCols>(tmem);
   }
-}
-
-template <int CG, int kKind>
-cudaError_t launch_gemm(const GemmArgs& a, int num_sms, cudaStream_t s) {
-  cudaError_t e = allow_smem<muon_gemm_kernel<CG, kKind>>(kSmem);
-  if (e != cudaSuccess) return e;
-  const long long tiles = static_cast<long long>(a.per) * a.L, most = num_sms / CG;
-  cudaLaunchAttribute attr[2] = {};
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim = {CG, 1, 1};
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(CG * (tiles < most ? tiles : most)));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = kSmem;
-  cfg.stream = s;
-  cfg.attrs = attr;
-  cfg.numAttrs = CG == 1 ? 1 : 2;
-  return cudaLaunchKernelEx(&cfg, muon_gemm_kernel<CG, kKind>, a);
 }
 
 // ------------------------------------------------------------------ the steps
@@ -591,71 +785,65 @@ bool map_k_rows(MapEncoder enc, CUtensorMap* m, const __half* base, long long co
 
 template <int CG>
 cudaError_t run_steps(const MuonArgs& a, MapEncoder enc, int num_sms, cudaStream_t s) {
-  constexpr int T = 128 * CG;
-  CUtensorMap xk[2], xn[2], xh[2], xl[2], ak, as, at, bk, bs, bt;
-  bool ok = true;
-  for (int i = 0; i < 2; ++i) {
-    ok = ok && map_3d(enc, &xk[i], a.x[i].hi, a.m, a.n, a.L, a.ldx, 64, 128);
-    ok = ok && map_k_rows(enc, &xn[i], a.x[i].hi, a.m, a.n, a.L, a.ldx);
-    ok = ok && map_3d(enc, &xh[i], a.x[i].hi, a.m, a.n, a.L, a.ldx, 64, 32);
-    ok = ok && map_3d(enc, &xl[i], a.x[i].lo, a.m, a.n, a.L, a.ldx, 64, 32);
-  }
-  ok = ok && map_3d(enc, &ak, a.gram, a.n, a.n, a.L, a.lda, 64, 128) &&
-       map_3d(enc, &as, a.gram, a.n, a.n, a.L, a.lda, 64, 32) &&
-       map_3d(enc, &at, a.gram, a.n, a.n, a.L, a.lda, 32, 64, false) &&
-       map_3d(enc, &bk, a.poly, a.n, a.n, a.L, a.lda, 64, 128) &&
-       map_3d(enc, &bs, a.poly, a.n, a.n, a.L, a.lda, 64, 32) &&
-       map_3d(enc, &bt, a.poly, a.n, a.n, a.L, a.lda, 32, 64, false);
-  if (!ok) return cudaErrorInvalidValue;
   GemmArgs g;
   memset(&g, 0, sizeof(g));
+  bool ok = true;
+  for (int i = 0; i < 2; ++i) {
+    g.hi[i] = a.x[i].hi;
+    g.lo[i] = a.x[i].lo;
+    ok = ok && map_3d(enc, &g.xk[i], a.x[i].hi, a.m, a.n, a.L, a.ldx, 64, 128) &&
+         map_k_rows(enc, &g.xn[i], a.x[i].hi, a.m, a.n, a.L, a.ldx) &&
+         map_3d(enc, &g.xh[i], a.x[i].hi, a.m, a.n, a.L, a.ldx, 64, 32) &&
+         map_3d(enc, &g.xl[i], a.x[i].lo, a.m, a.n, a.L, a.ldx, 64, 32);
+  }
+  ok = ok && map_3d(enc, &g.ak, a.gram, a.n, a.n, a.L, a.lda, 64, 128) &&
+       map_3d(enc, &g.as, a.gram, a.n, a.n, a.L, a.lda, 64, 32) &&
+       map_3d(enc, &g.at, a.gram, a.n, a.n, a.L, a.lda, 32, 64, false) &&
+       map_3d(enc, &g.bk, a.poly, a.n, a.n, a.L, a.lda, 64, 128) &&
+       map_3d(enc, &g.bs, a.poly, a.n, a.n, a.L, a.lda, 64, 32) &&
+       map_3d(enc, &g.bt, a.poly, a.n, a.n, a.L, a.lda, 32, 64, false);
+  if (!ok) return cudaErrorInvalidValue;
+  constexpr int T = Geo<CG>::kM;
+  g.gram = a.gram;
+  g.ldx = a.ldx;
+  g.lda = a.lda;
   g.n = a.n;
   g.m = a.m;
   g.L = a.L;
+  g.steps = a.steps;
   g.num_m = (a.n + T - 1) / T;
+  g.num_n = (a.m + T - 1) / T;
+  g.tri = g.num_m * (g.num_m + 1) / 2;
+  g.full = g.num_m * g.num_n;
+  memcpy(g.coeffs, a.coeffs, sizeof(float) * 3 * static_cast<size_t>(a.steps));
   g.out = a.out;
   g.scale = a.scale;
   g.tall = a.tall;
+  g.counter = a.sync;
+  g.done_a = a.sync + 32;
+  g.done_b = g.done_a + static_cast<long long>(a.L) * g.num_m * g.num_m;
+  g.done_x = g.done_b + static_cast<long long>(a.L) * g.num_m * g.num_m;
   g.status = a.status;
   g.budget = a.budget;
-  for (int i = 0; i < a.steps; ++i) {
-    const MuonPair &x = a.x[i & 1];
-    const int to = (i + 1) & 1;
-    g.ca = a.coeffs[3 * i];
-    g.cb = a.coeffs[3 * i + 1];
-    g.cc = a.coeffs[3 * i + 2];
-    // A = X X^T
-    g.ma = g.mb = xk[i & 1];
-    g.s0 = as;
-    g.s1 = at;
-    g.num_kb = (a.m + 63) / 64;
-    g.num_n = g.num_m;
-    g.per = g.num_m * (g.num_m + 1) / 2;
-    cudaError_t e = launch_gemm<CG, kGram>(g, num_sms, s);
-    if (e != cudaSuccess) return e;
-    // B = b A + c A A
-    g.ma = g.mb = ak;
-    g.s0 = bs;
-    g.s1 = bt;
-    g.num_kb = (a.n + 63) / 64;
-    g.p0 = a.gram;
-    g.ld = a.lda;
-    e = launch_gemm<CG, kPoly>(g, num_sms, s);
-    if (e != cudaSuccess) return e;
-    // X = a X + B X
-    g.ma = bk;
-    g.mb = xn[i & 1];
-    g.s0 = xh[to];
-    g.s1 = xl[to];
-    g.num_n = (a.m + T - 1) / T;
-    g.per = g.num_m * g.num_n;
-    g.p0 = x.hi;
-    g.p1 = x.lo;
-    g.ld = a.ldx;
-    e = i + 1 < a.steps ? launch_gemm<CG, kApply>(g, num_sms, s) : launch_gemm<CG, kLast>(g, num_sms, s);
-    if (e != cudaSuccess) return e;
-  }
-  return cudaSuccess;
+  const auto kernel = muon_gemm_kernel<CG>;
+  cudaError_t e = allow_smem<muon_gemm_kernel<CG>>(kSmem);
+  if (e != cudaSuccess) return e;
+  // a CTA an SM at most; CTAs wait for one another, so they are launched to run
+  // together
+  const long long tiles = static_cast<long long>(g.tri + g.tri + g.full) * a.L * a.steps, most = num_sms / CG;
+  cudaLaunchAttribute attr[2] = {};
+  attr[0].id = cudaLaunchAttributeCooperative;
+  attr[0].val.cooperative = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim = {CG, 1, 1};
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(CG * (tiles < most ? tiles : most)));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmem;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = CG == 1 ? 1 : 2;
+  return cudaLaunchKernelEx(&cfg, kernel, g);
 }
 
 template <typename G>
@@ -684,7 +872,11 @@ MuonPlan muon_plan(long long L, long long rows, long long cols) {
   p.chunks = (size + p.chunk - 1) / p.chunk;
   auto up = [](size_t x) { return (x + 1023) / 1024 * 1024; };
   const size_t x = up(static_cast<size_t>(2 * L * n * p.ldx)), q = up(static_cast<size_t>(2 * L * n * p.lda));
-  p.partial = up(sizeof(DevStatus));
+  // a drawing counter (a line of its own) and one a tile, of the smaller tiles
+  const size_t tn = static_cast<size_t>((n + 127) / 128), tm = static_cast<size_t>((m + 127) / 128);
+  p.sync_words = 32 + static_cast<size_t>(L) * tn * (2 * tn + tm);
+  p.sync = up(sizeof(DevStatus));
+  p.partial = p.sync + up(4 * p.sync_words);
   p.x[0] = p.partial + up(static_cast<size_t>(8 * L * p.chunks));
   for (int i = 1; i < 4; ++i) p.x[i] = p.x[i - 1] + x;
   p.gram = p.x[3] + x;
@@ -696,10 +888,11 @@ MuonPlan muon_plan(long long L, long long rows, long long cols) {
 cudaError_t launch_muon(const MuonArgs& a, int grad_bf16, MapEncoder enc, int num_sms, cudaStream_t s) {
   cudaError_t e = grad_bf16 ? prepare<__nv_bfloat16>(a, s) : prepare<float>(a, s);
   if (e != cudaSuccess) return e;
-  // 256 x 256 tiles by pairs of CTAs where they fill the machine about twice, else
-  // 128 x 128 tiles
-  const long long wide = static_cast<long long>(a.L) * ((a.n + 255) / 256) * ((a.m + 255) / 256);
-  return wide >= num_sms ? run_steps<2>(a, enc, num_sms, s) : run_steps<1>(a, enc, num_sms, s);
+  // 128 x 128 tiles where each SM gets one of X's at most, so that a product takes as
+  // little as its depth allows; else 256 x 256 tiles by pairs, which take in half the
+  // bytes an operation
+  const long long small = static_cast<long long>(a.L) * ((a.n + 127) / 128) * ((a.m + 127) / 128);
+  return small > num_sms ? run_steps<2>(a, enc, num_sms, s) : run_steps<1>(a, enc, num_sms, s);
 }
 
 }  // namespace eas

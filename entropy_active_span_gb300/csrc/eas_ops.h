@@ -141,7 +141,9 @@ struct ScoreBwdArgs {
 cudaError_t launch_score_bwd(const ScoreBwdArgs& a, int is_bf16, int num_sms, cudaStream_t s);
 
 // ---- orthogonalised update (eas_muon.cu) ----
+constexpr int kMuonSteps = 32;    // EAS_MAX_MUON_STEPS
 struct MuonPlan {         // sizes of the workspace, in bytes from its start
+  size_t sync, sync_words;
   size_t partial;         // double [L][chunks]
   size_t x[4];            // X's two pairs: hi, lo, hi, lo; u [L][rows][cols] fp32 from x[2] on
   size_t gram, poly;
@@ -174,6 +176,8 @@ struct MuonArgs {
   __half* gram;           // A
   __half* poly;           // B
   long long ldx, lda;
+  int* sync;              // counters of the products, zero at their start
+  long long sync_words;
   DevStatus* status;
   long long budget;       // clocks a wait may take
 };

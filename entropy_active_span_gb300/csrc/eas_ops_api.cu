@@ -101,12 +101,13 @@ MapEncoder map_encoder() {
 
 bool muon_sizes(long long L, long long rows, long long cols) {
   if (L < 0 || L > 65535 || rows < 1 || rows > EAS_MAX_MUON_SIDE || cols < 1 || cols > EAS_MAX_MUON_SIDE) return false;
-  return L * ((rows + 127) / 128) * ((cols + 127) / 128) < (1LL << 30);
+  // tile numbers of 32 steps fit an int
+  return L * ((rows + 127) / 128) * ((cols + 127) / 128) < (1LL << 24);
 }
 
 }  // namespace
 
-static_assert(EAS_MAX_TOP == kMaxTop && EAS_MAX_TOKENS == kMaxTokens, "eas.h and eas_ops.h");
+static_assert(EAS_MAX_MUON_STEPS == kMuonSteps && EAS_MAX_TOP == kMaxTop && EAS_MAX_TOKENS == kMaxTokens, "eas.h and eas_ops.h");
 
 extern "C" {
 
@@ -458,6 +459,8 @@ eas_status eas_orthogonalize(const void* grad, eas_dtype grad_dtype, const void*
   a.poly = at<__half>(ws, p.poly);
   a.ldx = p.ldx;
   a.lda = p.lda;
+  a.sync = at<int>(ws, p.sync);
+  a.sync_words = static_cast<long long>(p.sync_words);
   a.status = static_cast<DevStatus*>(ws);
   a.budget = wait_budget();
   Trace tr_(kTrMuon, s);
