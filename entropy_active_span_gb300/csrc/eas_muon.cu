@@ -35,13 +35,8 @@ constexpr int kWhereMuon = 50;
 // ------------------------------------------------- momentum, norm, conversion
 
 constexpr int kPrepThreads = 256;
-constexpr int kChunk = 16384;     // elements a CTA at least
+constexpr int kChunk = 4096;      // elements a CTA at least
 constexpr int kMostChunks = 1024; // partial sums a matrix
-
-template <typename T>
-__device__ __forceinline__ float load1(const void* p, long long i) {
-  return to_f32(static_cast<const T*>(p)[i]);
-}
 
 // Sum of squares in fp64, added up in fp32 over a vector where that is safe.
 template <int VEC>
@@ -82,29 +77,43 @@ __device__ __forceinline__ void write_values(T* p, const float (&f)[VEC]) {
 
 // Each CTA a chunk of a matrix: the new momentum, u (fp32) where there is a momentum,
 // and the chunk's sum of squares.
+// A thread has kItems vectors (kVec) or single values on their way at a time.
 template <typename G, typename M, bool kMom, bool kVec>
 __device__ double update_chunk(const MuonArgs& a, long long base, long long lo, long long hi) {
-  constexpr int VEC = kVec ? 8 : 1;
+  constexpr int VEC = kVec ? 8 : 1, kItems = kVec ? 2 : 8;
   const float beta = a.beta, rest = a.rest;
+  const G* grad = static_cast<const G*>(a.grad) + base;
+  const M* mom = static_cast<const M*>(a.mom) + base;
+  M* new_mom = static_cast<M*>(a.new_mom) + base;
+  float* out = a.u + base;
   double sum = 0.;
-  for (long long i = lo + static_cast<long long>(threadIdx.x) * VEC; i < hi; i += kPrepThreads * VEC) {
-    float g[VEC], u[VEC];
-    read_values(static_cast<const G*>(a.grad) + base + i, g);
-    if constexpr (kMom) {
-      float m[VEC];
-      read_values(static_cast<const M*>(a.mom) + base + i, m);
+  for (long long i0 = lo + static_cast<long long>(threadIdx.x) * VEC; i0 < hi; i0 += kItems * kPrepThreads * VEC) {
+    float g[kItems][VEC], m[kItems][VEC];
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        m[j] = fmaf(beta, m[j], rest * g[j]);
-        u[j] = a.nesterov ? fmaf(beta, m[j], rest * g[j]) : m[j];
-      }
-      write_values(static_cast<M*>(a.new_mom) + base + i, m);
-      write_values(a.u + base + i, u);
-    } else {
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) u[j] = g[j];
+    for (int k = 0; k < kItems; ++k) {
+      const long long i = i0 + k * kPrepThreads * VEC;
+      if (i >= hi) break;
+      read_values(grad + i, g[k]);
+      if constexpr (kMom) read_values(mom + i, m[k]);
     }
-    sum += squares<VEC>(u);
+#pragma unroll
+    for (int k = 0; k < kItems; ++k) {
+      const long long i = i0 + k * kPrepThreads * VEC;
+      if (i >= hi) break;
+      if constexpr (kMom) {
+        float u[VEC];
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) {
+          m[k][j] = fmaf(beta, m[k][j], rest * g[k][j]);
+          u[j] = a.nesterov ? fmaf(beta, m[k][j], rest * g[k][j]) : m[k][j];
+        }
+        write_values(new_mom + i, m[k]);
+        write_values(out + i, u);
+        sum += squares<VEC>(u);
+      } else {
+        sum += squares<VEC>(g[k]);
+      }
+    }
   }
   return sum;
 }
@@ -143,48 +152,86 @@ __global__ void __launch_bounds__(kPrepThreads) muon_update_kernel(const MuonArg
     a.sync[i] = 0;
 }
 
-// X's first pair: u (or the gradient) times 2^12 / (norm + eps), transposed where it
-// is taller than wide.  A CTA a 64 x 64 tile; grid (tiles of X's columns, of its
-// rows, L).
-template <typename G>
-__global__ void __launch_bounds__(kPrepThreads) muon_scale_kernel(const MuonArgs a) {
-  __shared__ float tile[64][65];
+// Eight values from p on as a pair of fp16 each, times f.
+__device__ __forceinline__ void write_pair(const MuonPair& x, long long o, const float (&v)[8], float f) {
+  uint4 hi, lo;
+  uint32_t* h = reinterpret_cast<uint32_t*>(&hi);
+  uint32_t* l = reinterpret_cast<uint32_t*>(&lo);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float p = v[2 * j] * f, q = v[2 * j + 1] * f;
+    const __half2 a = __floats2half2_rn(p, q);
+    const __half2 b = __floats2half2_rn(p - __low2float(a), q - __high2float(a));
+    h[j] = *reinterpret_cast<const uint32_t*>(&a);
+    l[j] = *reinterpret_cast<const uint32_t*>(&b);
+  }
+  *reinterpret_cast<uint4*>(x.hi + o) = hi;
+  *reinterpret_cast<uint4*>(x.lo + o) = lo;
+}
+
+// X's first pair: src (u, or the gradient where there is no momentum) times 2^12 /
+// (norm + eps), transposed where it is taller than wide.  grid (CTAs, L); a CTA takes
+// 64 x 64 tiles of X in turn.
+template <typename S, bool kTall>
+__global__ void __launch_bounds__(kPrepThreads) muon_scale_kernel(const MuonArgs a, const S* src) {
+  __shared__ float tile[kTall ? 64 : 1][65];
   __shared__ float factor;
-  const int tid = threadIdx.x, l = blockIdx.z;
+  const int tid = threadIdx.x;
+  const long long l = blockIdx.y;
   wait_for_launch_before();
   double s = 0.;
-  for (int i = tid; i < a.chunks; i += kPrepThreads) s += a.partial[static_cast<long long>(l) * a.chunks + i];
+  for (int i = tid; i < a.chunks; i += kPrepThreads) s += a.partial[l * a.chunks + i];
   s = block_sum(s);
   if (tid == 0) factor = static_cast<float>(kUp / (sqrt(s) + a.eps));
-  const long long base = static_cast<long long>(l) * a.rows * a.cols;
-  const int r0 = blockIdx.y * 64, c0 = blockIdx.x * 64;        // of X
-  auto value = [&](int r, int c) {
-    const long long i = base + static_cast<long long>(r) * a.cols + c;
-    return a.mom ? a.u[i] : load1<G>(a.grad, i);
-  };
-  if (a.tall) {
-    for (int i = tid; i < 64 * 64; i += kPrepThreads) {
-      const int c = i / 64, r = i % 64;                        // consecutive r: consecutive in memory
-      tile[r][c] = r0 + r < a.n && c0 + c < a.m ? value(c0 + c, r0 + r) : 0.f;
-    }
-  }
   __syncthreads();
   const float f = factor;
-  for (int i = tid; i < 64 * 32; i += kPrepThreads) {
-    const int r = i / 32, c = i % 32 * 2;
-    if (r0 + r >= a.n) break;
-    float v[2];
+  src += l * a.rows * a.cols;
+  const int across = (a.m + 63) / 64, tiles = across * ((a.n + 63) / 64);
+  // rows of the source in vectors of eight
+  const bool vec = (a.cols & 7) == 0 && aligned16(src);
+  for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
+    const int r0 = t / across * 64, c0 = t % across * 64;      // of X
+    // a tile is 64 rows of eight vectors of the source: two a thread
+    float v[2][8];
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      if (a.tall) v[j] = tile[r][c + j];
-      else v[j] = c0 + c + j < a.m ? value(r0 + r, c0 + c + j) : 0.f;
-      v[j] *= f;
+    for (int k = 0; k < 2; ++k) {
+      const int i = k * kPrepThreads + tid;
+      const int sr = (kTall ? c0 : r0) + i / 8, sc = (kTall ? r0 : c0) + i % 8 * 8;
+      const S* p = src + static_cast<long long>(sr) * a.cols + sc;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[k][j] = 0.f;
+      if (sr < a.rows) {
+        if (vec) {
+          if (sc < a.cols) read_values(p, v[k]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (sc + j < a.cols) v[k][j] = to_f32(p[j]);
+        }
+      }
     }
-    const __half2 hi = __floats2half2_rn(v[0], v[1]);
-    const __half2 lo = __floats2half2_rn(v[0] - __low2float(hi), v[1] - __high2float(hi));
-    const long long o = (static_cast<long long>(l) * a.n + r0 + r) * a.ldx + c0 + c;
-    *reinterpret_cast<__half2*>(a.x[0].hi + o) = hi;
-    *reinterpret_cast<__half2*>(a.x[0].lo + o) = lo;
+    if constexpr (kTall) {
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int i = k * kPrepThreads + tid;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) tile[i / 8][i % 8 * 8 + j] = v[k][j];
+      }
+      __syncthreads();
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        // eight lanes a row of X, four rows a warp: a bank each
+        const int i = k * kPrepThreads + tid;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[k][j] = tile[i % 8 * 8 + j][i / 8];
+      }
+      __syncthreads();
+    }
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int i = k * kPrepThreads + tid, r = r0 + i / 8;
+      if (r < a.n) write_pair(a.x[0], (l * a.n + r) * a.ldx + c0 + i % 8 * 8, v[k], f);
+    }
   }
 }
 
@@ -846,17 +893,23 @@ cudaError_t run_steps(const MuonArgs& a, MapEncoder enc, int num_sms, cudaStream
   return cudaLaunchKernelEx(&cfg, kernel, g);
 }
 
+template <typename S>
+cudaError_t scale(const MuonArgs& a, const S* src, int num_sms, cudaStream_t s) {
+  const long long tiles = static_cast<long long>((a.m + 63) / 64) * ((a.n + 63) / 64), most = 8LL * num_sms;
+  const dim3 grid(static_cast<unsigned>(tiles < most ? tiles : most), static_cast<unsigned>(a.L));
+  return a.tall ? launch_overlapped(muon_scale_kernel<S, true>, grid, dim3(kPrepThreads), 0, s, a, src)
+                : launch_overlapped(muon_scale_kernel<S, false>, grid, dim3(kPrepThreads), 0, s, a, src);
+}
+
 template <typename G>
-cudaError_t prepare(const MuonArgs& a, cudaStream_t s) {
+cudaError_t prepare(const MuonArgs& a, int num_sms, cudaStream_t s) {
   const dim3 grid(static_cast<unsigned>(a.chunks), static_cast<unsigned>(a.L));
   if (!a.mom) muon_update_kernel<G, float, false><<<grid, kPrepThreads, 0, s>>>(a);
   else if (a.mom_bf16) muon_update_kernel<G, __nv_bfloat16, true><<<grid, kPrepThreads, 0, s>>>(a);
   else muon_update_kernel<G, float, true><<<grid, kPrepThreads, 0, s>>>(a);
-  cudaError_t e = cudaGetLastError();
+  const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  const dim3 tiles(static_cast<unsigned>((a.m + 63) / 64), static_cast<unsigned>((a.n + 63) / 64),
-                   static_cast<unsigned>(a.L));
-  return launch_overlapped(muon_scale_kernel<G>, tiles, dim3(kPrepThreads), 0, s, a);
+  return a.mom ? scale<float>(a, a.u, num_sms, s) : scale<G>(a, static_cast<const G*>(a.grad), num_sms, s);
 }
 
 }  // namespace
@@ -886,7 +939,7 @@ MuonPlan muon_plan(long long L, long long rows, long long cols) {
 }
 
 cudaError_t launch_muon(const MuonArgs& a, int grad_bf16, MapEncoder enc, int num_sms, cudaStream_t s) {
-  cudaError_t e = grad_bf16 ? prepare<__nv_bfloat16>(a, s) : prepare<float>(a, s);
+  const cudaError_t e = grad_bf16 ? prepare<__nv_bfloat16>(a, num_sms, s) : prepare<float>(a, num_sms, s);
   if (e != cudaSuccess) return e;
   // 128 x 128 tiles where each SM gets one of X's at most, so that a product takes as
   // little as its depth allows; else 256 x 256 tiles by pairs, which take in half the

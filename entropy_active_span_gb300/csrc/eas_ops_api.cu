@@ -74,7 +74,7 @@ eas_status check_scores(long long N, long long V, long long M, long long ld, eas
   if (M < 0 || M > EAS_MAX_TOKENS) return fail(EAS_ERR_INVALID_ARG, "M=%lld out of range", M);
   if (ld < V || ld > (1LL << 40)) return fail(EAS_ERR_INVALID_ARG, "row pitch %lld below V or out of range", ld);
   if (dt != EAS_BF16 && dt != EAS_FP32) return fail(EAS_ERR_INVALID_ARG, "dtype %d", (int)dt);
-  if (!(scale > 0.f) || !std::isfinite(scale)) return fail(EAS_ERR_INVALID_ARG, "scale must be positive");
+  if (!(scale > 0.f) || scale > 0x1p40f) return fail(EAS_ERR_INVALID_ARG, "scale must be in (0, 2^40]");
   return EAS_OK;
 }
 

@@ -489,7 +489,8 @@ eas_status eas_clip_grad_norm(const void* const* grads, void* const* outs, const
  *            [0, V) also gives 0, and EAS_ERR_INVALID_ARG in the status word of ws.
  *   mask     [N] uint8 or NULL (every row active).  Inactive rows are not read; they
  *            get zeros, and -1 in top_ids.
- *   scale    > 0, finite (the inverse of a temperature)
+ *   scale    > 0, at most 2^40 (the inverse of a temperature); scale times the
+ *            logits, -inf apart, has to stay within fp32
  *   k        0 <= k <= min(EAS_MAX_TOP, V); 0: top_logprob and top_ids may be NULL
  *   logprob [N, M], entropy [N], lse [N], top_logprob [N, k] fp32, top_ids [N, k]
  *            int32 : out
