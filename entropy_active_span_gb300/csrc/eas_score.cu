@@ -30,10 +30,9 @@ namespace {
 
 constexpr int kThreads = 512;     // at most
 constexpr int kGroup = 4;         // vectors a thread loads at a time
-constexpr int kCand = 512;        // values above t that are kept
-constexpr int kTies = 128;        // and values equal to it
+constexpr int kCand = 512;        // values that wait to be ordered
 constexpr int kPieces = 8;        // of a thread's part
-constexpr int kTiePieces = 512;   // pieces whose maximum is t that are read again
+constexpr int kTiePieces = 256;   // pieces whose maximum is t that are read again, at most
 constexpr int kMaxSplit = 8;      // CTAs a row
 constexpr int kWhereScore = 40;   // `where` of the status word
 
@@ -192,9 +191,9 @@ struct Walk {
   float m = -INFINITY, cm = 0.f;     // reference of the sums
   Sums sum = {0.f, 0.f, 0.f, 0.f};
 
-  // Returns the group's largest value.
-  template <typename T, int N>
-  __device__ __forceinline__ float add(const uint4 (&r)[N], float c) {
+  // Returns the group's largest value.  again(i): the group's i-th vector once more.
+  template <typename T, int N, typename F>
+  __device__ __forceinline__ float add(const uint4 (&r)[N], float c, F again) {
     const float most = group_max<T>(r);
     best = max_nan(best, most);
     if (!(fmaf(most, c, -cm) <= 4.f) || m == -INFINITY) {
@@ -215,7 +214,11 @@ struct Walk {
     sum.add_group<T, false>(r, m, cm, c);
     if (!(fabsf(sum.u0 + sum.u1) < INFINITY)) {        // 0 * -inf: again, with care
       sum = before;
-      sum.add_group<T, true>(r, m, cm, c);
+#pragma unroll 1
+      for (int i = 0; i < N; ++i) {
+        const uint4 v[1] = {again(i)};
+        sum.add_group<T, true>(v, m, cm, c);
+      }
     }
     return most;
   }
@@ -225,17 +228,17 @@ struct Walk {
 
 // ------------------------------------------------------------ the k largest
 
-// NT: threads of the CTA, at most.
+// What a walk leaves of a row, NT threads at most: order bits of each thread's maximum
+// (0: it had no vector) and the maxima of its pieces.
 template <int NT>
-struct Shared {
-  uint32_t best[NT];                              // order bits of the threads' maxima
+struct Maxima {
+  uint32_t best[NT];
+  float piece[kPieces][NT];
+};
+// What the selecting warp works in.
+struct Scratch {
   unsigned long long cand[kCand];
-  unsigned long long tie[kTies];
-  float piece[kPieces][NT];                       // maxima of the threads' pieces
-  uint16_t read[kMaxTop * kPieces + kTiePieces];  // pieces to be read again: above t, then t
-  int scan[NT / 32];
-  uint32_t t;
-  int n_above, n_tie, n_pieces, n_tie_pieces;
+  uint16_t read[kMaxTop * kPieces + kTiePieces];   // pieces to be read again: above t, then t
 };
 
 // Order bits of the 16-byte block's values.
@@ -249,215 +252,185 @@ __device__ __forceinline__ void block_bits(const uint4& r, uint32_t (&b)[kVec16<
   for (int j = 0; j < kVec16<T>; ++j) b[j] = order_bits(f[j]);
 }
 
-// The largest t such that k of the threads' maxima reach it (0: fewer have one).
-// The bits below kLow are the same in every value of the type and its sign.
-template <typename T, int kWarps>
-__device__ __forceinline__ uint32_t kth_of_maxima(const uint32_t* best, int nt, int k, int lane) {
+// A t that k of the threads' maxima reach: the k-th largest of them, or one that exactly
+// k reach.  0: fewer than k threads have one.  The bits below kLow are the same in every
+// value of the type and its sign.
+template <typename T, int NT>
+__device__ __forceinline__ uint32_t kth_of_maxima(const uint32_t* best, int nt, int k) {
   constexpr int kLow = sizeof(T) == 2 ? 16 : 0;
-  uint32_t key[kWarps];
+  const int lane = threadIdx.x & 31;
+  uint32_t key[NT / 32], most = 0, least = 0xffffffffu;
+  int n = 0;
 #pragma unroll
-  for (int i = 0; i < kWarps; ++i) key[i] = i * 32 < nt ? best[i * 32 + lane] : 0u;
-  uint32_t t = 0;
+  for (int i = 0; i < NT / 32; ++i) {
+    key[i] = i * 32 < nt ? best[i * 32 + lane] : 0u;
+    most = max(most, key[i]);
+    if (key[i]) {
+      least = min(least, key[i]);
+      ++n;
+    }
+  }
+  if (__reduce_add_sync(0xffffffffu, n) < k) return 0;
+  most = __reduce_max_sync(0xffffffffu, most);
+  least = __reduce_min_sync(0xffffffffu, least);
+  if (most == least) return most;
+  // the bits that all share, then one after the other
+  int bit = 31 - __clz(most ^ least);
+  uint32_t t = most & (0xfffffffeu << bit);
 #pragma unroll 1
-  for (int bit = 31; bit >= kLow; --bit) {
+  for (; bit >= kLow; --bit) {
     const uint32_t c = t | (1u << bit);
-    int n = 0;
+    n = 0;
 #pragma unroll
-    for (int i = 0; i < kWarps; ++i) n += key[i] >= c;
-    if (__reduce_add_sync(0xffffffffu, n) >= k) t = c;
+    for (int i = 0; i < NT / 32; ++i) n += key[i] >= c;
+    n = __reduce_add_sync(0xffffffffu, n);
+    if (n >= k) t = c;
+    if (n == k) return t;
   }
   // a negative value's low bits are ones
-  if (kLow && t && !(t & 0x80000000u)) t |= (1u << kLow) - 1;
+  if (kLow && !(t & 0x80000000u)) t |= (1u << kLow) - 1;
   return t;
 }
 
-// Sum over the CTA of a count, and what the threads before this one have of it.
-__device__ __forceinline__ int scan_counts(int n, int* scan, int nt, int& total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int inc = n;
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const int o = __shfl_up_sync(0xffffffffu, inc, d);
-    if (lane >= d) inc += o;
-  }
-  __syncthreads();
-  if (lane == 31) scan[warp] = inc;
-  __syncthreads();
-  int before = 0;
-  total = 0;
-  for (int w = 0; w < nt / 32; ++w) {
-    if (w < warp) before += scan[w];
-    total += scan[w];
-  }
-  return before + inc - n;
-}
-
-// The first `need` values equal to t of the slice, by column, to sm.cand[from ..].
+// The k largest of the slice in order, to `out` (0 where it has fewer), by one warp.
+// The walk was that of nt threads in `groups` groups, `span` groups to a piece.
 template <typename T, int NT>
-__device__ void first_ties(const Slice<T>& sl, Shared<NT>& sm, uint32_t t, int from, int need) {
-  constexpr int VEC = kVec16<T>;
-  const int nt = blockDim.x, tid = threadIdx.x;
-  int have = 0;
-  // head, blocks of nt vectors, tail
-  const int steps = (sl.v1 - sl.v0 + nt - 1) / nt;
-#pragma unroll 1
-  for (int i = -1; i <= steps && have < need; ++i) {
-    uint32_t b[VEC] = {};
-    int col = 0, count = 0;
-    if (i < 0 || i == steps) {
-      const int n = i < 0 ? (sl.first ? sl.head : 0) : (sl.last ? sl.tail : 0);
-      if (tid < n) {
-        col = i < 0 ? tid : sl.head + sl.nvec * VEC + tid;
-        b[0] = order_bits(to_f32(sl.row[col]));
-      }
-    } else {
-      const int v = sl.v0 + i * nt + tid;
-      if (v < sl.v1) {
-        col = sl.column(v);
-        block_bits<T>(load_block(sl.row, col), b);
-      }
-    }
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) count += b[j] == t;
-    int total;
-    int at = have + scan_counts(count, sm.scan, nt, total);
-#pragma unroll
-    for (int j = 0; j < VEC; ++j)
-      if (b[j] == t) {
-        if (at < need) sm.cand[from + at] = order_key(t, col + j);
-        ++at;
-      }
-    have += total;
-  }
-  __syncthreads();
-}
-
-// Calls f(order bits, column) for every value of the slice.
-template <typename T, typename F>
-__device__ __forceinline__ void for_all(const Slice<T>& sl, F f) {
-  constexpr int VEC = kVec16<T>;
-  for (int v = sl.v0 + threadIdx.x; v < sl.v1; v += blockDim.x) {
-    uint32_t b[VEC];
-    const int col = sl.column(v);
-    block_bits<T>(load_block(sl.row, col), b);
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) f(b[j], col + j);
-  }
-  if (static_cast<int>(threadIdx.x) < sl.loose()) {
-    const int col = sl.loose_column(threadIdx.x);
-    f(order_bits(to_f32(sl.row[col])), col);
-  }
-}
-
-__device__ __forceinline__ void push(unsigned long long* list, int* n, int most, uint32_t b, int col) {
-  const int at = atomicAdd(n, 1);
-  if (at < most) list[at] = order_key(b, col);
-}
-
-// The k largest of the slice in order, to `out` (0 where it has fewer).  `best`: the
-// thread's maximum over its vectors (if it has any), in `groups` groups, `span` to a
-// piece.
-template <typename T, int NT>
-__device__ void k_largest(const Slice<T>& sl, Shared<NT>& sm, float best, int groups, int span, int k,
+__device__ void k_largest(const Slice<T>& sl, const Maxima<NT>& mx, int nt, int groups, int span, int k, Scratch& sc,
                           unsigned long long* out) {
   constexpr int VEC = kVec16<T>;
-  const int nt = blockDim.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const uint32_t mine = sl.v0 + tid < sl.v1 ? order_bits(best) : 0u;
-  sm.best[tid] = mine;
-  if (tid == 0) sm.n_above = sm.n_tie = sm.n_pieces = sm.n_tie_pieces = 0;
-  __syncthreads();
-  if (warp == 0) {
-    const uint32_t t = kth_of_maxima<T, NT / 32>(sm.best, nt, k, lane);
-    if (lane == 0) sm.t = t;
-  }
-  __syncthreads();
-  uint32_t t = sm.t;
-  // fewer than k threads have pieces above t
-  if (mine >= t && mine) {
-    const int pieces = (groups + span - 1) / span;
+  constexpr unsigned kAll = 0xffffffffu;
+  const int lane = threadIdx.x & 31;
+  const unsigned below = (1u << lane) - 1;
+  const uint32_t t = kth_of_maxima<T, NT>(mx.best, nt, k);
+  const int pieces = (groups + span - 1) / span;
+
+  // the pieces that reach t; at most k threads have some above it
+  int above = 0, equal = 0;
+  for (int b = 0; b < nt && t; b += 32) {
+    const bool hit = mx.best[b + lane] >= t;
+    if (!__any_sync(kAll, hit)) continue;
     for (int p = 0; p < pieces; ++p) {
-      if (sl.v0 + p * span * kGroup * nt + tid >= sl.v1) break;
-      const uint32_t b = order_bits(sm.piece[p][tid]);
-      const uint16_t id = static_cast<uint16_t>(p * nt + tid);
-      if (b > t && t) {
-        sm.read[atomicAdd(&sm.n_pieces, 1)] = id;
-      } else if (b == t) {
-        const int at = atomicAdd(&sm.n_tie_pieces, 1);
-        if (at < kTiePieces) sm.read[kMaxTop * kPieces + at] = id;
-      }
+      const bool in = hit && sl.v0 + p * span * kGroup * nt + b + lane < sl.v1;
+      const uint32_t bits = in ? order_bits(mx.piece[p][b + lane]) : 0u;
+      const unsigned up = __ballot_sync(kAll, bits > t), eq = __ballot_sync(kAll, bits == t);
+      const uint16_t id = static_cast<uint16_t>(p * nt + b + lane);
+      if (bits > t) sc.read[above + __popc(up & below)] = id;
+      above += __popc(up);
+      const int at = equal + __popc(eq & below);
+      if (bits == t && at < kTiePieces) sc.read[kMaxTop * kPieces + at] = id;
+      equal += __popc(eq);
     }
   }
-  __syncthreads();
+  __syncwarp();
   // many pieces with the same maximum (a row of equal values, or of -inf): the ties are
-  // looked for in the order of the columns instead.  t = 0: every value is above it.
-  const int above = t ? sm.n_pieces : 0, equal = sm.n_tie_pieces;
+  // looked for in the order of the columns instead
   const bool take_ties = t && equal <= kTiePieces;
-  const int pieces = above + (take_ties ? equal : 0);
-  auto see = [&](uint32_t b, int col) {
-    if (b > t) push(sm.cand, &sm.n_above, kCand, b, col);
-    else if (take_ties && b == t) push(sm.tie, &sm.n_tie, kTies, b, col);
+  const int todo = above + (take_ties ? equal : 0);
+
+  // values above `floor` wait in sc.cand; where it fills up, the k largest of them stay
+  int n = 0;
+  unsigned long long floor = static_cast<unsigned long long>(t) << 32 | (t && !take_ties ? 0xffffffffu : 0u);
+  auto order = [&] {
+    __syncwarp();
+    for (int i = lane; i < n; i += 32) {
+      const unsigned long long key = sc.cand[i];
+      int place = 0;
+#pragma unroll 8
+      for (int j = 0; j < n; ++j) place += sc.cand[j] > key;
+      if (place < k) out[place] = key;
+    }
+    __syncwarp();
   };
-  // kGroup lanes a piece
-  for (int i = tid / kGroup; i < pieces; i += nt / kGroup) {
-    const int id = sm.read[i < above ? i : kMaxTop * kPieces + i - above], p = id / nt;
-    for (int g = 0; g < span; ++g) {
-      const int v = sl.v0 + ((p * span + g) * kGroup + tid % kGroup) * nt + id - p * nt;
-      if (v >= sl.v1) break;
-      uint32_t b[VEC];
-      const int col = sl.column(v);
-      block_bits<T>(load_block(sl.row, col), b);
+  auto see = [&](bool in, uint32_t b, int col) {
+    const unsigned long long key = order_key(b, col);
+    const unsigned who = __ballot_sync(kAll, in && key > floor);
+    if (who >> lane & 1u) sc.cand[n + __popc(who & below)] = key;
+    n += __popc(who);
+  };
+  auto see_vector = [&](bool in, const uint4& r, int v) {
+    uint32_t b[VEC];
+    const int col = sl.column(v);
+    block_bits<T>(r, b);
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) see(b[j], col + j);
+    for (int j = 0; j < VEC; ++j) see(in, b[j], col + j);
+    if (n > kCand - 32 * VEC) {
+      order();
+      n = n < k ? n : k;
+      for (int i = lane; i < n; i += 32) sc.cand[i] = out[i];
+      if (n == k) floor = out[k - 1];
+      __syncwarp();
+    }
+  };
+  // vectors of the pieces, or, t = 0, all of them: four a lane on their way
+  const int units = t ? todo * span * kGroup : sl.v1 - sl.v0;
+  for (int u0 = 0; u0 < units; u0 += 4 * 32) {
+    uint4 r[4];
+    int v[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int u = u0 + q * 32 + lane;
+      v[q] = sl.v1;
+      if (u < units) {
+        if (t) {
+          const int i = u / (span * kGroup), in = u - i * (span * kGroup);
+          const int id = sc.read[i < above ? i : kMaxTop * kPieces + i - above], p = id / nt;
+          v[q] = sl.v0 + (p * span * kGroup + in) * nt + id - p * nt;
+        } else {
+          v[q] = sl.v0 + u;
+        }
+      }
+      r[q] = v[q] < sl.v1 ? load_block(sl.row, sl.column(v[q])) : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      if (u0 + q * 32 >= units) break;
+      see_vector(v[q] < sl.v1, r[q], v[q]);
     }
   }
-  if (t == 0) {
-    for_all(sl, see);
-  } else if (tid < sl.loose()) {
-    const int col = sl.loose_column(tid);
-    see(order_bits(to_f32(sl.row[col])), col);
+  {
+    const bool in = lane < sl.loose();
+    const int col = in ? sl.loose_column(lane) : 0;
+    see(in, in ? order_bits(to_f32(sl.row[col])) : 0u, col);
   }
-  __syncthreads();
-  int n = sm.n_above;
-  const int ties = sm.n_tie;
-  bool look = t != 0 && n < k && !(take_ties && ties <= kTies);
-  if (n > kCand) {
-    // the few pieces that reach t hold too many values above it (a row whose large values
-    // lie in few pieces): the k-th largest value itself, bit by bit
-    t = 0;
-#pragma unroll 1
-    for (int bit = 31; bit >= 0; --bit) {
-      const uint32_t c = t | (1u << bit);
-      int count = 0, total;
-      for_all(sl, [&](uint32_t b, int) { count += b >= c; });
-      scan_counts(count, sm.scan, nt, total);
-      if (total >= k) t = c;
+  if (t && !take_ties && n < k) {
+    // values equal to t by column: head, vectors, tail
+    const int need = k - n, steps = (sl.v1 - sl.v0 + 31) / 32;
+    int have = 0;
+    for (int i = -1; i <= steps && have < need; ++i) {
+      uint32_t b[VEC] = {};
+      int col = 0, count = 0;
+      if (i < 0 || i == steps) {
+        const int in = i < 0 ? (sl.first ? sl.head : 0) : (sl.last ? sl.tail : 0);
+        if (lane < in) {
+          col = i < 0 ? lane : sl.head + sl.nvec * VEC + lane;
+          b[0] = order_bits(to_f32(sl.row[col]));
+        }
+      } else if (sl.v0 + i * 32 + lane < sl.v1) {
+        col = sl.column(sl.v0 + i * 32 + lane);
+        block_bits<T>(load_block(sl.row, col), b);
+      }
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) count += b[j] == t;
+      int upto = count;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(kAll, upto, d);
+        if (lane >= d) upto += o;
+      }
+      int at = have + upto - count;
+#pragma unroll
+      for (int j = 0; j < VEC; ++j)
+        if (b[j] == t) {
+          if (at < need) sc.cand[n + at] = order_key(t, col + j);
+          ++at;
+        }
+      have += __shfl_sync(kAll, upto, 31);
     }
-    __syncthreads();
-    if (tid == 0) sm.n_above = 0;
-    __syncthreads();
-    for_all(sl, [&](uint32_t b, int col) {
-      if (b > t) push(sm.cand, &sm.n_above, kCand, b, col);
-    });
-    __syncthreads();
-    n = sm.n_above;               // below k
-    look = true;
+    n = have < need ? n + have : k;
   }
-  if (look) {
-    first_ties(sl, sm, t, n, k - n);
-    n = k;
-  } else if (n < k && t != 0) {
-    for (int i = tid; i < ties; i += nt) sm.cand[n + i] = sm.tie[i];
-    n += ties;
-    __syncthreads();
-  }
-  // their places by counting
-  for (int i = tid; i < n; i += nt) {
-    const unsigned long long key = sm.cand[i];
-    int place = 0;
-    for (int j = 0; j < n; ++j) place += sm.cand[j] > key;
-    if (place < k) out[place] = key;
-  }
-  for (int i = n + tid; i < k; i += nt) out[i] = 0;
+  order();
+  for (int i = n + lane; i < k; i += 32) out[i] = 0;
+  __syncwarp();
 }
 
 // ------------------------------------------------------------------ cluster
@@ -489,13 +462,26 @@ __device__ __forceinline__ void write_zeros(const ScoreFwdArgs& a, long long row
   if (tid == 0) a.entropy[row] = a.lse[row] = 0.f;
 }
 
-// Groups to a piece, and the maximum of the thread's piece that group g belongs to.
+// Groups to a piece.
 __device__ __forceinline__ int span_of(int groups) { return (groups + kPieces - 1) / kPieces; }
-template <int NT>
-__device__ __forceinline__ void keep_piece(Shared<NT>& sm, int g, int span, float most) {
-  float& p = sm.piece[g / span][threadIdx.x];
-  p = g % span ? max_nan(p, most) : most;
-}
+// A thread's maxima of its pieces while it walks.
+struct Pieces {
+  float* at;            // of the current piece
+  int span, left;       // groups to a piece, and of the current one
+  float most = -INFINITY;
+  template <int NT>
+  __device__ __forceinline__ Pieces(Maxima<NT>& mx, int span_) : at(&mx.piece[0][threadIdx.x]), span(span_), left(span_) {}
+  template <int NT>
+  __device__ __forceinline__ void add(float x) {
+    most = max_nan(most, x);
+    *at = most;
+    if (--left == 0) {
+      left = span;
+      at += NT;
+      most = -INFINITY;
+    }
+  }
+};
 
 // The log probability of a value; ls = log2 s.
 __device__ __forceinline__ float log_prob(float x, const Stats& st, float ls, const ScoreFwdArgs& a) {
@@ -556,7 +542,8 @@ __device__ __forceinline__ Stats row_stats(const Stats* warps, int n, float c) {
 // A row a cluster of a.split CTAs (1: no cluster).
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 2) score_fwd_kernel(const ScoreFwdArgs a) {
-  __shared__ Shared<kThreads> sm;
+  __shared__ Maxima<kThreads> mx;
+  __shared__ Scratch sc;
   __shared__ Stats warps[kThreads / 32];
   __shared__ Stats part[kMaxSplit];                         // of the row's CTAs, in CTA 0
   __shared__ unsigned long long list[kMaxSplit * kMaxTop];  // their k largest, in CTA 0
@@ -573,34 +560,38 @@ __global__ void __launch_bounds__(kThreads, 2) score_fwd_kernel(const ScoreFwdAr
 
   Walk w;
   const int groups = (sl.v1 - sl.v0 + kGroup * nt - 1) / (kGroup * nt), span = span_of(groups);
-  int g = 0;
-  for (int v = sl.v0 + tid; v < sl.v1; v += kGroup * nt, ++g) {
+  Pieces pieces(mx, span);
+  for (int v = sl.v0 + tid; v < sl.v1; v += kGroup * nt) {
     uint4 r[kGroup];
+    if (v + (kGroup - 1) * nt < sl.v1) {
 #pragma unroll
-    for (int i = 0; i < kGroup; ++i)
-      if (v + i * nt < sl.v1) r[i] = load_block(x, sl.column(v + i * nt));
+      for (int i = 0; i < kGroup; ++i) r[i] = load_block(x, sl.column(v + i * nt));
+    }
+    auto again = [&](int i) { return load_block(x, sl.column(v + i * nt)); };
     float most;
     if (v + (kGroup - 1) * nt < sl.v1) {
-      most = w.add<T>(r, a.c);
+      most = w.add<T>(r, a.c, again);
     } else {
-      const uint4 one[1] = {r[0]};
-      most = w.add<T>(one, a.c);
-#pragma unroll
-      for (int i = 1; i < kGroup - 1; ++i)
-        if (v + i * nt < sl.v1) {
-          const uint4 next[1] = {r[i]};
-          most = max_nan(most, w.add<T>(next, a.c));
-        }
+      most = -INFINITY;
+#pragma unroll 1
+      for (int i = 0; v + i * nt < sl.v1; ++i) {
+        const uint4 one[1] = {again(i)};
+        most = max_nan(most, w.add<T>(one, a.c, [&](int) { return again(i); }));
+      }
     }
-    if (a.k) keep_piece(sm, g, span, most);
+    pieces.add<kThreads>(most);
   }
   Stats st = w.stats();
   if (tid < sl.loose()) add_value(st, to_f32(x[sl.loose_column(tid)]), a.c);
   st = warp_stats(st, a.c);
   if ((tid & 31) == 0) warps[tid >> 5] = st;
-  if (a.k) k_largest(sl, sm, w.best, groups, span, a.k, list);
+  mx.best[tid] = sl.v0 + tid < sl.v1 ? order_bits(w.best) : 0u;
   __syncthreads();
-  if (tid < 32) st = row_stats(warps, nt / 32, a.c);
+  if (tid < 32) {
+    st = row_stats(warps, nt / 32, a.c);
+    if (a.k) k_largest(sl, mx, nt, groups, span, a.k, sc, list);
+  }
+  __syncthreads();
   if (split > 1) {
     cluster_wait();
     if (rank) {
@@ -633,24 +624,36 @@ __global__ void __launch_bounds__(kThreads, 2) score_fwd_kernel(const ScoreFwdAr
         }
         place += lo;
       }
-      if (key && place < a.k) sm.cand[place] = key;
+      if (key && place < a.k) sc.cand[place] = key;
     }
     __syncthreads();
   }
-  if (tid < 32) write_row(a, row, x, st, split > 1 ? sm.cand : list);
+  if (tid < 32) write_row(a, row, x, st, split > 1 ? sc.cand : list);
 }
 
 // ------------------------------------------------------------ many long rows
 //
-// Four CTAs an SM take rows in turn.  A thread's next vectors come by cp.async into its
-// own places of a ring in shared memory, on into the CTA's next row while the k
-// largest of this one are found: the loads never pause.  [16384][128256] bf16 behind
-// a 62 % mask: 674 us with a CTA a row.
+// Two CTAs an SM take rows in turn.  Eight warps walk: a thread's next vectors come by
+// cp.async into its own places of a ring in shared memory, on into the CTA's next row.
+// Three other warps, each for every third row, find the k largest and write a row's
+// outputs while the walk goes on.  [16384][128256] bf16 behind a 62 % mask: 674 us with a
+// CTA a row that does one after the other.
 
-constexpr int kRowThreads = 256;
-constexpr int kRowCtas = 4;       // an SM
-constexpr int kRingGroups = 2;    // groups of vectors on their way
+constexpr int kRowThreads = 256;                  // that walk
+constexpr int kSelect = 3;                        // warps that find the k largest
+constexpr int kRowAll = kRowThreads + 32 * kSelect;
+constexpr int kRowCtas = 2;       // an SM
+constexpr int kRingGroups = 3;    // groups of vectors on their way
 constexpr int kRingBytes = kRingGroups * kGroup * kRowThreads * 16;
+
+// Barriers of the walking warps and a selecting one: `arrive` does not wait.
+__device__ __forceinline__ void barrier_sync(int id) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "n"(kRowThreads + 32) : "memory");
+}
+__device__ __forceinline__ void barrier_arrive(int id) {
+  __threadfence_block();
+  asm volatile("bar.arrive %0, %1;" ::"r"(id), "n"(kRowThreads + 32) : "memory");
+}
 
 __device__ __forceinline__ void copy_async(uint4* to, const void* from) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to)), "l"(from) : "memory");
@@ -674,97 +677,128 @@ __device__ __forceinline__ long long active_row(const ScoreFwdArgs& a, long long
   return r;
 }
 
+struct RowShared {
+  Maxima<kRowThreads> mx[kSelect];                 // of kSelect rows in turn
+  Stats warps[kSelect][kRowThreads / 32];
+  Scratch scratch[kSelect];
+  unsigned long long list[kSelect][kMaxTop];
+};
+constexpr int kRowBytes = kRingBytes + static_cast<int>(sizeof(RowShared));
+
 template <typename T>
-__global__ void __launch_bounds__(kRowThreads, kRowCtas) score_rows_kernel(const ScoreFwdArgs a) {
-  extern __shared__ uint4 ring[];     // [kRingGroups][kGroup][kRowThreads]
-  __shared__ Shared<kRowThreads> sm;
-  // of two rows in turn: warp 0 writes a row's outputs while the others are in the next
-  __shared__ unsigned long long list[2][kMaxTop];
-  __shared__ Stats warps[2][kRowThreads / 32];
+__global__ void __launch_bounds__(kRowAll, kRowCtas) score_rows_kernel(const ScoreFwdArgs a) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  uint4* ring = reinterpret_cast<uint4*>(smem);    // [kRingGroups][kGroup][kRowThreads]
+  RowShared& sh = *reinterpret_cast<RowShared*>(smem + kRingBytes);
   constexpr int VEC = kVec16<T>, kStep = kGroup * kRowThreads;
+  constexpr int kFull = 1, kEmpty = 1 + kSelect;   // barriers: + turn
   const int tid = threadIdx.x;
   const long long step = gridDim.x;
   const T* base = static_cast<const T*>(a.x);
   if (a.mask)
-    for (long long r = blockIdx.x + tid * step; r < a.N; r += kRowThreads * step)
+    for (long long r = blockIdx.x + tid * step; r < a.N; r += kRowAll * step)
       if (!a.mask[r]) write_zeros(a, r, 0, 1);
 
-  // the next group to be copied: of row `coming`, `ahead` of its `whole` vectors done
-  const long long first = active_row(a, blockIdx.x, step);
-  long long coming = first;
-  const T* body = nullptr;            // this thread's next vector
-  int ahead = 0, whole = 0, slot_in = 0;
-  auto open = [&] {
-    if (coming >= a.N) return;
-    const Slice<T> sl(base + coming * a.ld, a.V, 0, 1);
-    body = sl.row + sl.head + tid * VEC;
-    whole = sl.nvec;
-    ahead = 0;
-  };
-  auto issue = [&] {
-    if (coming < a.N) {
-      uint4* to = ring + slot_in * kStep + tid;
-      if (ahead + kStep <= whole) {
-#pragma unroll
-        for (int k = 0; k < kGroup; ++k) copy_async(to + k * kRowThreads, body + k * kRowThreads * VEC);
-      } else {
-#pragma unroll
-        for (int k = 0; k < kGroup; ++k)
-          if (ahead + k * kRowThreads + tid < whole) copy_async(to + k * kRowThreads, body + k * kRowThreads * VEC);
-      }
-      body += kStep * VEC;
-      ahead += kStep;
-      if (ahead >= whole) {
-        coming = active_row(a, coming + step, step);
-        open();
-      }
+  long long row = active_row(a, blockIdx.x, step);
+  int turn = 0;
+  if (tid >= kRowThreads) {
+    // every kSelect-th row of the CTA's
+    turn = (tid - kRowThreads) >> 5;
+    auto on = [&](long long r, int n) {
+      for (int i = 0; i < n && r < a.N; ++i) r = active_row(a, r + step, step);
+      return r;
+    };
+    row = on(row, turn);
+    Scratch& sc = sh.scratch[turn];
+    unsigned long long* list = sh.list[turn];
+    while (row < a.N) {
+      const long long next = on(row, kSelect);
+      const Slice<T> sl(base + row * a.ld, a.V, 0, 1);
+      const int groups = (sl.nvec + kStep - 1) / kStep;
+      barrier_sync(kFull + turn);
+      if (a.k) k_largest(sl, sh.mx[turn], kRowThreads, groups, span_of(groups), a.k, sc, list);
+      const Stats st = row_stats(sh.warps[turn], kRowThreads / 32, a.c);
+      __syncwarp();
+      if (next < a.N) barrier_arrive(kEmpty + turn);
+      write_row(a, row, sl.row, st, list);
+      __syncwarp();
+      row = next;
     }
-    slot_in = slot_in + 1 == kRingGroups ? 0 : slot_in + 1;
+    return;
+  }
+  if (row >= a.N) return;
+  // copies to a slot the group of vectors from `from` on, `left` of them this thread's
+  auto issue = [&](int to, const T* from, int left) {
+    uint4* p = ring + to * kStep + tid;
+    if (left > (kGroup - 1) * kRowThreads) {
+#pragma unroll
+      for (int k = 0; k < kGroup; ++k) copy_async(p + k * kRowThreads, from + k * kRowThreads * VEC);
+    } else {
+#pragma unroll 1
+      for (int k = 0; k * kRowThreads < left; ++k) copy_async(p + k * kRowThreads, from + k * kRowThreads * VEC);
+    }
     copies_commit();
   };
-  open();
+  Slice<T> sl(base + row * a.ld, a.V, 0, 1);
 #pragma unroll 1
-  for (int i = 0; i < kRingGroups; ++i) issue();
+  for (int g = 0; g < kRingGroups; ++g)
+    issue(g, sl.row + sl.head + (tid + g * kStep) * VEC, sl.nvec - tid - g * kStep);
 
-  long long row = first;
-  int slot = 0, turn = 0;
+  int slot = 0, done = 0;
 #pragma unroll 1
-  while (row < a.N) {
-    const T* x = base + row * a.ld;
-    const Slice<T> sl(x, a.V, 0, 1);
-    Walk w;
+  while (true) {
+    const long long next = active_row(a, row + step, step);
+    const Slice<T> after(base + (next < a.N ? next : row) * a.ld, a.V, 0, 1);
     const int groups = (sl.nvec + kStep - 1) / kStep, span = span_of(groups);
+    // kRingGroups groups from here: of this row, then of the next one (rows have as many
+    // groups or one more or less; more than kRingGroups)
+    const T* from = sl.row + sl.head + (tid + kRingGroups * kStep) * VEC;
+    int here = sl.nvec - tid;          // this thread's vectors: every kRowThreads-th of them
+    int ahead = here - kRingGroups * kStep;
+    if (done >= kSelect) barrier_sync(kEmpty + turn);
+    Walk w;
+    Pieces pieces(sh.mx[turn], span);
 #pragma unroll 1
-    for (int g = 0; g < groups; ++g) {
+    for (int g = groups; g > 0; --g) {
       copies_wait<kRingGroups - 1>();
-      const uint4* from = ring + slot * kStep + tid;
-      const int left = sl.nvec - g * kStep - tid;      // vectors of this thread: every kRowThreads-th of them
+      const uint4* in = ring + slot * kStep + tid;
+      auto again = [&](int i) { return in[i * kRowThreads]; };
       float most = -INFINITY;
-      if (left > (kGroup - 1) * kRowThreads) {
+      if (here > (kGroup - 1) * kRowThreads) {
         uint4 r[kGroup];
 #pragma unroll
-        for (int k = 0; k < kGroup; ++k) r[k] = from[k * kRowThreads];
-        most = w.add<T>(r, a.c);
+        for (int k = 0; k < kGroup; ++k) r[k] = again(k);
+        most = w.add<T>(r, a.c, again);
       } else {
 #pragma unroll 1
-        for (int k = 0; k * kRowThreads < left; ++k) {
-          const uint4 r[1] = {from[k * kRowThreads]};
-          most = max_nan(most, w.add<T>(r, a.c));
+        for (int k = 0; k * kRowThreads < here; ++k) {
+          const uint4 r[1] = {again(k)};
+          most = max_nan(most, w.add<T>(r, a.c, [&](int) { return again(k); }));
         }
       }
-      if (a.k) keep_piece(sm, g, span, most);
-      issue();
+      pieces.add<kRowThreads>(most);
+      if (g == kRingGroups) {
+        from = after.row + after.head + tid * VEC;
+        ahead = (next < a.N ? after.nvec : 0) - tid;
+      }
+      issue(slot, from, ahead);
+      from += kStep * VEC;
+      ahead -= kStep;
+      here -= kStep;
       slot = slot + 1 == kRingGroups ? 0 : slot + 1;
     }
     Stats st = w.stats();
-    if (tid < sl.loose()) add_value(st, to_f32(x[sl.loose_column(tid)]), a.c);
+    if (tid < sl.loose()) add_value(st, to_f32(sl.row[sl.loose_column(tid)]), a.c);
     st = warp_stats(st, a.c);
-    if ((tid & 31) == 0) warps[turn][tid >> 5] = st;
-    if (a.k) k_largest(sl, sm, w.best, groups, span, a.k, list[turn]);
-    __syncthreads();
-    if (tid < 32) write_row(a, row, x, row_stats(warps[turn], kRowThreads / 32, a.c), list[turn]);
-    turn ^= 1;
-    row = active_row(a, row + step, step);
+    if ((tid & 31) == 0) sh.warps[turn][tid >> 5] = st;
+    sh.mx[turn].best[tid] = tid < sl.nvec ? order_bits(w.best) : 0u;
+    __syncwarp();
+    barrier_arrive(kFull + turn);
+    turn = turn + 1 == kSelect ? 0 : turn + 1;
+    ++done;
+    if (next >= a.N) break;
+    row = next;
+    sl = after;
   }
   copies_wait<0>();
 }
@@ -885,12 +919,12 @@ cudaError_t launch_score_fwd(const ScoreFwdArgs& args, int is_bf16, int num_sms,
   if (args.N == 0) return cudaSuccess;
   ScoreFwdArgs a = args;
   const long long nvec = a.V / (is_bf16 ? 8 : 4);
-  if (a.N > kRowCtas * static_cast<long long>(num_sms) && nvec >= 2 * kGroup * kRowThreads) {
+  if (a.N > kRowCtas * static_cast<long long>(num_sms) && nvec >= (kRingGroups + 1) * kGroup * kRowThreads) {
     const auto kernel = is_bf16 ? score_rows_kernel<__nv_bfloat16> : score_rows_kernel<float>;
-    const cudaError_t e = is_bf16 ? allow_smem<score_rows_kernel<__nv_bfloat16>>(kRingBytes)
-                                  : allow_smem<score_rows_kernel<float>>(kRingBytes);
+    const cudaError_t e = is_bf16 ? allow_smem<score_rows_kernel<__nv_bfloat16>>(kRowBytes)
+                                  : allow_smem<score_rows_kernel<float>>(kRowBytes);
     if (e != cudaSuccess) return e;
-    kernel<<<kRowCtas * num_sms, kRowThreads, kRingBytes, s>>>(a);
+    kernel<<<kRowCtas * num_sms, kRowAll, kRowBytes, s>>>(a);
     return cudaGetLastError();
   }
   const int nt = threads_of(nvec);
