@@ -29,7 +29,6 @@ namespace eas {
 namespace {
 
 constexpr int kThreads = 512;     // at most
-constexpr int kGroup = 4;         // vectors a thread loads at a time
 constexpr int kCand = 512;        // values that wait to be ordered
 constexpr int kPieces = 8;        // of a thread's part
 constexpr int kTiePieces = 256;   // pieces whose maximum is t that are read again, at most
@@ -68,6 +67,15 @@ struct Slice {
 template <typename T>
 __device__ __forceinline__ uint4 load_block(const T* row, int col) {
   return __ldg(reinterpret_cast<const uint4*>(row + col));
+}
+
+// A vector that adds nothing to sums whose largest value is above kFillerMost, if c is
+// below kFillerScale (-1e30 everywhere): what a thread takes where it has none left.
+constexpr float kFillerMost = -1e25f, kFillerScale = 1e7f;
+template <typename T>
+__device__ __forceinline__ uint4 filler() {
+  const uint32_t w = sizeof(T) == 2 ? 0xf14af14au : 0xf149f2cau;
+  return make_uint4(w, w, w, w);
 }
 
 // Monotonic bits of a value: -0 as 0, NaN above everything; 0 stands for none.
@@ -159,11 +167,14 @@ __device__ __forceinline__ float group_max(const uint4 (&r)[N]) {
 struct Sums {
   float s0, s1, u0, u1;
 
-  // kCareful: some of the values are -inf or so low that y is not finite.
+  // kCareful: some of the values are -inf or so low that y is not finite; wild: c m is not.
   template <bool kCareful>
-  __device__ __forceinline__ void add(float x0, float x1, float m, float cm, float c) {
-    const float y0 = kCareful ? fmaxf(exponent(x0, m, c), kLeast) : fmaf(x0, c, -cm);
-    const float y1 = kCareful ? fmaxf(exponent(x1, m, c), kLeast) : fmaf(x1, c, -cm);
+  __device__ __forceinline__ void add(float x0, float x1, float m, float cm, float c, bool wild) {
+    float y0 = fmaf(x0, c, -cm), y1 = fmaf(x1, c, -cm);
+    if constexpr (kCareful) {
+      y0 = fmaxf(wild ? (x0 - m) * c : y0, kLeast);
+      y1 = fmaxf(wild ? (x1 - m) * c : y1, kLeast);
+    }
     const float e0 = ex2_approx(y0), e1 = ex2_approx(y1);
     s0 += e0;
     s1 += e1;
@@ -172,21 +183,26 @@ struct Sums {
   }
   template <typename T, bool kCareful, int N>
   __device__ __forceinline__ void add_group(const uint4 (&r)[N], float m, float cm, float c) {
+    const bool wild = kCareful && isinf(cm);
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const uint32_t w[4] = {r[i].x, r[i].y, r[i].z, r[i].w};
       if constexpr (sizeof(T) == 2) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) add<kCareful>(bf16_lo(w[j]), bf16_hi(w[j]), m, cm, c);
+        for (int j = 0; j < 4; ++j) add<kCareful>(bf16_lo(w[j]), bf16_hi(w[j]), m, cm, c, wild);
       } else {
-        add<kCareful>(__uint_as_float(w[0]), __uint_as_float(w[1]), m, cm, c);
-        add<kCareful>(__uint_as_float(w[2]), __uint_as_float(w[3]), m, cm, c);
+        add<kCareful>(__uint_as_float(w[0]), __uint_as_float(w[1]), m, cm, c, wild);
+        add<kCareful>(__uint_as_float(w[2]), __uint_as_float(w[3]), m, cm, c, wild);
       }
     }
   }
 };
 
+// kAgain: the careful path reads a group's vectors once more, one at a time, which keeps
+// the code short (it fits the instruction cache); else it takes them from registers.
+template <bool kAgain>
 struct Walk {
+  bool low = false;                  // a group with values for the careful path has come
   float best = -INFINITY;            // the largest value
   float m = -INFINITY, cm = 0.f;     // reference of the sums
   Sums sum = {0.f, 0.f, 0.f, 0.f};
@@ -210,15 +226,34 @@ struct Walk {
       cm = __fmul_rn(m, c);
       if (!(to < INFINITY)) sum.s0 = NAN;
     }
-    const Sums before = sum;
-    sum.add_group<T, false>(r, m, cm, c);
-    if (!(fabsf(sum.u0 + sum.u1) < INFINITY)) {        // 0 * -inf: again, with care
+    if (!low) {
+      const Sums before = sum;
+      sum.add_group<T, false>(r, m, cm, c);
+      if (fabsf(sum.u0 + sum.u1) < INFINITY) return most;
+      low = true;                    // 0 * -inf: again, with care
       sum = before;
+    }
+    if constexpr (kAgain) {
 #pragma unroll 1
       for (int i = 0; i < N; ++i) {
         const uint4 v[1] = {again(i)};
         sum.add_group<T, true>(v, m, cm, c);
       }
+    } else {
+      sum.add_group<T, true>(r, m, cm, c);
+    }
+    return most;
+  }
+
+  // The same of a group of which only the first n vectors may be there (all: they are).
+  template <typename T, int N, typename F>
+  __device__ __forceinline__ float add_some(const uint4 (&r)[N], bool all, float c, F again, int n) {
+    if (all || (c < kFillerScale && group_max<T>(r) > kFillerMost)) return add<T>(r, c, again);
+    float most = -INFINITY;
+#pragma unroll 1
+    for (int i = 0; i < N && i < n; ++i) {
+      const uint4 one[1] = {again(i)};
+      most = max_nan(most, add<T>(one, c, [&](int) { return again(i); }));
     }
     return most;
   }
@@ -238,6 +273,7 @@ struct Maxima {
 // What the selecting warp works in.
 struct Scratch {
   unsigned long long cand[kCand];
+  uint16_t hit[kThreads];                          // threads that reach t
   uint16_t read[kMaxTop * kPieces + kTiePieces];   // pieces to be read again: above t, then t
 };
 
@@ -293,8 +329,9 @@ __device__ __forceinline__ uint32_t kth_of_maxima(const uint32_t* best, int nt, 
 }
 
 // The k largest of the slice in order, to `out` (0 where it has fewer), by one warp.
-// The walk was that of nt threads in `groups` groups, `span` groups to a piece.
-template <typename T, int NT>
+// The walk was that of nt threads (a power of two) in `groups` groups of kGroup vectors,
+// `span` groups to a piece.
+template <typename T, int NT, int kGroup>
 __device__ void k_largest(const Slice<T>& sl, const Maxima<NT>& mx, int nt, int groups, int span, int k, Scratch& sc,
                           unsigned long long* out) {
   constexpr int VEC = kVec16<T>;
@@ -304,22 +341,28 @@ __device__ void k_largest(const Slice<T>& sl, const Maxima<NT>& mx, int nt, int 
   const uint32_t t = kth_of_maxima<T, NT>(mx.best, nt, k);
   const int pieces = (groups + span - 1) / span;
 
-  // the pieces that reach t; at most k threads have some above it
-  int above = 0, equal = 0;
+  // the threads that reach t, then their pieces that do; at most k threads have some above
+  int above = 0, equal = 0, hits = 0;
   for (int b = 0; b < nt && t; b += 32) {
     const bool hit = mx.best[b + lane] >= t;
-    if (!__any_sync(kAll, hit)) continue;
-    for (int p = 0; p < pieces; ++p) {
-      const bool in = hit && sl.v0 + p * span * kGroup * nt + b + lane < sl.v1;
-      const uint32_t bits = in ? order_bits(mx.piece[p][b + lane]) : 0u;
-      const unsigned up = __ballot_sync(kAll, bits > t), eq = __ballot_sync(kAll, bits == t);
-      const uint16_t id = static_cast<uint16_t>(p * nt + b + lane);
-      if (bits > t) sc.read[above + __popc(up & below)] = id;
-      above += __popc(up);
-      const int at = equal + __popc(eq & below);
-      if (bits == t && at < kTiePieces) sc.read[kMaxTop * kPieces + at] = id;
-      equal += __popc(eq);
-    }
+    const unsigned who = __ballot_sync(kAll, hit);
+    if (hit) sc.hit[hits + __popc(who & below)] = static_cast<uint16_t>(b + lane);
+    hits += __popc(who);
+  }
+  __syncwarp();
+  const float per = 1.f / pieces;            // below 2^13 pieces: exact after the floor
+  for (int u0 = 0; u0 < hits * pieces; u0 += 32) {
+    const int u = u0 + lane, i = static_cast<int>((u + 0.5f) * per), p = u - i * pieces;
+    const int who = u < hits * pieces ? sc.hit[i] : 0;
+    const bool in = u < hits * pieces && sl.v0 + p * span * kGroup * nt + who < sl.v1;
+    const uint32_t bits = in ? order_bits(mx.piece[p][who]) : 0u;
+    const unsigned up = __ballot_sync(kAll, bits > t), eq = __ballot_sync(kAll, bits == t);
+    const uint16_t id = static_cast<uint16_t>(p * nt + who);
+    if (bits > t) sc.read[above + __popc(up & below)] = id;
+    above += __popc(up);
+    const int at = equal + __popc(eq & below);
+    if (bits == t && at < kTiePieces) sc.read[kMaxTop * kPieces + at] = id;
+    equal += __popc(eq);
   }
   __syncwarp();
   // many pieces with the same maximum (a row of equal values, or of -inf): the ties are
@@ -347,12 +390,27 @@ __device__ void k_largest(const Slice<T>& sl, const Maxima<NT>& mx, int nt, int 
     if (who >> lane & 1u) sc.cand[n + __popc(who & below)] = key;
     n += __popc(who);
   };
+  // a vector a lane: first which of its values reach t at all (NaN does), then those,
+  // one a lane at a time
+  const float least = t ? from_order_bits(t) : -INFINITY;
   auto see_vector = [&](bool in, const uint4& r, int v) {
-    uint32_t b[VEC];
-    const int col = sl.column(v);
-    block_bits<T>(r, b);
+    float f[VEC];
+    Raw<T, VEC> raw;
+    raw.v = r;
+    widen<T, VEC>(raw, f);
+    unsigned hits = 0;
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) see(in, b[j], col + j);
+    for (int j = 0; j < VEC; ++j) hits |= !(f[j] < least) ? 1u << j : 0u;
+    if (!in) hits = 0;
+    const int col = sl.column(v);
+    while (__any_sync(kAll, hits)) {
+      const int j = __ffs(hits) - 1;
+      float x = f[0];
+#pragma unroll
+      for (int i = 1; i < VEC; ++i) x = i == j ? f[i] : x;
+      see(hits, order_bits(x), col + j);
+      hits &= hits - 1;
+    }
     if (n > kCand - 32 * VEC) {
       order();
       n = n < k ? n : k;
@@ -362,7 +420,8 @@ __device__ void k_largest(const Slice<T>& sl, const Maxima<NT>& mx, int nt, int 
     }
   };
   // vectors of the pieces, or, t = 0, all of them: four a lane on their way
-  const int units = t ? todo * span * kGroup : sl.v1 - sl.v0;
+  const int each = span * kGroup, units = t ? todo * each : sl.v1 - sl.v0, log_nt = 31 - __clz(nt);
+  const float part = 1.f / each;             // u below 2^15: exact after the floor
   for (int u0 = 0; u0 < units; u0 += 4 * 32) {
     uint4 r[4];
     int v[4];
@@ -372,9 +431,9 @@ __device__ void k_largest(const Slice<T>& sl, const Maxima<NT>& mx, int nt, int 
       v[q] = sl.v1;
       if (u < units) {
         if (t) {
-          const int i = u / (span * kGroup), in = u - i * (span * kGroup);
-          const int id = sc.read[i < above ? i : kMaxTop * kPieces + i - above], p = id / nt;
-          v[q] = sl.v0 + (p * span * kGroup + in) * nt + id - p * nt;
+          const int i = static_cast<int>((u + 0.5f) * part);
+          const int id = sc.read[i < above ? i : kMaxTop * kPieces + i - above], p = id >> log_nt;
+          v[q] = sl.v0 + ((p * each + u - i * each) << log_nt) + (id & (nt - 1));
         } else {
           v[q] = sl.v0 + u;
         }
@@ -547,6 +606,7 @@ __global__ void __launch_bounds__(kThreads, 2) score_fwd_kernel(const ScoreFwdAr
   __shared__ Stats warps[kThreads / 32];
   __shared__ Stats part[kMaxSplit];                         // of the row's CTAs, in CTA 0
   __shared__ unsigned long long list[kMaxSplit * kMaxTop];  // their k largest, in CTA 0
+  constexpr int kGroup = 4;           // vectors a thread loads at a time
   const int split = a.split, rank = split > 1 ? blockIdx.x % split : 0;
   const long long row = blockIdx.x / split;
   const int nt = blockDim.x, tid = threadIdx.x;
@@ -558,27 +618,15 @@ __global__ void __launch_bounds__(kThreads, 2) score_fwd_kernel(const ScoreFwdAr
   const T* x = static_cast<const T*>(a.x) + row * a.ld;
   const Slice<T> sl(x, a.V, rank, split);
 
-  Walk w;
+  Walk<false> w;
   const int groups = (sl.v1 - sl.v0 + kGroup * nt - 1) / (kGroup * nt), span = span_of(groups);
   Pieces pieces(mx, span);
   for (int v = sl.v0 + tid; v < sl.v1; v += kGroup * nt) {
+    auto again = [&](int i) { return v + i * nt < sl.v1 ? load_block(x, sl.column(v + i * nt)) : filler<T>(); };
     uint4 r[kGroup];
-    if (v + (kGroup - 1) * nt < sl.v1) {
 #pragma unroll
-      for (int i = 0; i < kGroup; ++i) r[i] = load_block(x, sl.column(v + i * nt));
-    }
-    auto again = [&](int i) { return load_block(x, sl.column(v + i * nt)); };
-    float most;
-    if (v + (kGroup - 1) * nt < sl.v1) {
-      most = w.add<T>(r, a.c, again);
-    } else {
-      most = -INFINITY;
-#pragma unroll 1
-      for (int i = 0; v + i * nt < sl.v1; ++i) {
-        const uint4 one[1] = {again(i)};
-        most = max_nan(most, w.add<T>(one, a.c, [&](int) { return again(i); }));
-      }
-    }
+    for (int i = 0; i < kGroup; ++i) r[i] = again(i);
+    const float most = w.add_some<T>(r, v + (kGroup - 1) * nt < sl.v1, a.c, again, (sl.v1 - v + nt - 1) / nt);
     pieces.add<kThreads>(most);
   }
   Stats st = w.stats();
@@ -589,7 +637,7 @@ __global__ void __launch_bounds__(kThreads, 2) score_fwd_kernel(const ScoreFwdAr
   __syncthreads();
   if (tid < 32) {
     st = row_stats(warps, nt / 32, a.c);
-    if (a.k) k_largest(sl, mx, nt, groups, span, a.k, sc, list);
+    if (a.k) k_largest<T, kThreads, kGroup>(sl, mx, nt, groups, span, a.k, sc, list);
   }
   __syncthreads();
   if (split > 1) {
@@ -643,8 +691,13 @@ constexpr int kRowThreads = 256;                  // that walk
 constexpr int kSelect = 3;                        // warps that find the k largest
 constexpr int kRowAll = kRowThreads + 32 * kSelect;
 constexpr int kRowCtas = 2;       // an SM
-constexpr int kRingGroups = 3;    // groups of vectors on their way
-constexpr int kRingBytes = kRingGroups * kGroup * kRowThreads * 16;
+// Groups of vectors on their way: kGroup vectors are walked at a time.  Eight at a time
+// take 10 % fewer instructions a value than four (4096 rows of 128256 bf16 with eight
+// alternatives 176 us and 184), but need rows of more than two groups of 2048 vectors.
+template <int kGroup>
+constexpr int kRingGroups = kGroup == 8 ? 2 : 3;
+template <int kGroup>
+constexpr int kRingBytes = kRingGroups<kGroup> * kGroup * kRowThreads * 16;
 
 // Barriers of the walking warps and a selecting one: `arrive` does not wait.
 __device__ __forceinline__ void barrier_sync(int id) {
@@ -683,14 +736,15 @@ struct RowShared {
   Scratch scratch[kSelect];
   unsigned long long list[kSelect][kMaxTop];
 };
-constexpr int kRowBytes = kRingBytes + static_cast<int>(sizeof(RowShared));
+template <int kGroup>
+constexpr int kRowBytes = kRingBytes<kGroup> + static_cast<int>(sizeof(RowShared));
 
-template <typename T>
+template <typename T, int kGroup>
 __global__ void __launch_bounds__(kRowAll, kRowCtas) score_rows_kernel(const ScoreFwdArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
-  uint4* ring = reinterpret_cast<uint4*>(smem);    // [kRingGroups][kGroup][kRowThreads]
-  RowShared& sh = *reinterpret_cast<RowShared*>(smem + kRingBytes);
-  constexpr int VEC = kVec16<T>, kStep = kGroup * kRowThreads;
+  uint4* ring = reinterpret_cast<uint4*>(smem);    // [kAhead][kGroup][kRowThreads]
+  RowShared& sh = *reinterpret_cast<RowShared*>(smem + kRingBytes<kGroup>);
+  constexpr int VEC = kVec16<T>, kStep = kGroup * kRowThreads, kAhead = kRingGroups<kGroup>;
   constexpr int kFull = 1, kEmpty = 1 + kSelect;   // barriers: + turn
   const int tid = threadIdx.x;
   const long long step = gridDim.x;
@@ -716,7 +770,7 @@ __global__ void __launch_bounds__(kRowAll, kRowCtas) score_rows_kernel(const Sco
       const Slice<T> sl(base + row * a.ld, a.V, 0, 1);
       const int groups = (sl.nvec + kStep - 1) / kStep;
       barrier_sync(kFull + turn);
-      if (a.k) k_largest(sl, sh.mx[turn], kRowThreads, groups, span_of(groups), a.k, sc, list);
+      if (a.k) k_largest<T, kRowThreads, kGroup>(sl, sh.mx[turn], kRowThreads, groups, span_of(groups), a.k, sc, list);
       const Stats st = row_stats(sh.warps[turn], kRowThreads / 32, a.c);
       __syncwarp();
       if (next < a.N) barrier_arrive(kEmpty + turn);
@@ -741,7 +795,7 @@ __global__ void __launch_bounds__(kRowAll, kRowCtas) score_rows_kernel(const Sco
   };
   Slice<T> sl(base + row * a.ld, a.V, 0, 1);
 #pragma unroll 1
-  for (int g = 0; g < kRingGroups; ++g)
+  for (int g = 0; g < kAhead; ++g)
     issue(g, sl.row + sl.head + (tid + g * kStep) * VEC, sl.nvec - tid - g * kStep);
 
   int slot = 0, done = 0;
@@ -750,34 +804,31 @@ __global__ void __launch_bounds__(kRowAll, kRowCtas) score_rows_kernel(const Sco
     const long long next = active_row(a, row + step, step);
     const Slice<T> after(base + (next < a.N ? next : row) * a.ld, a.V, 0, 1);
     const int groups = (sl.nvec + kStep - 1) / kStep, span = span_of(groups);
-    // kRingGroups groups from here: of this row, then of the next one (rows have as many
-    // groups or one more or less; more than kRingGroups)
-    const T* from = sl.row + sl.head + (tid + kRingGroups * kStep) * VEC;
+    // kAhead groups from here: of this row, then of the next one (rows have as many
+    // groups or one more or less; more than kAhead)
+    const T* from = sl.row + sl.head + (tid + kAhead * kStep) * VEC;
     int here = sl.nvec - tid;          // this thread's vectors: every kRowThreads-th of them
-    int ahead = here - kRingGroups * kStep;
+    int ahead = here - kAhead * kStep;
     if (done >= kSelect) barrier_sync(kEmpty + turn);
-    Walk w;
+    Walk<true> w;
     Pieces pieces(sh.mx[turn], span);
 #pragma unroll 1
     for (int g = groups; g > 0; --g) {
-      copies_wait<kRingGroups - 1>();
+      copies_wait<kAhead - 1>();
       const uint4* in = ring + slot * kStep + tid;
-      auto again = [&](int i) { return in[i * kRowThreads]; };
-      float most = -INFINITY;
-      if (here > (kGroup - 1) * kRowThreads) {
-        uint4 r[kGroup];
+      const bool all = here > (kGroup - 1) * kRowThreads;
+      auto again = [&](int i) { return i * kRowThreads < here ? in[i * kRowThreads] : filler<T>(); };
+      uint4 r[kGroup];
+      if (all) {
+#pragma unroll
+        for (int k = 0; k < kGroup; ++k) r[k] = in[k * kRowThreads];
+      } else {
 #pragma unroll
         for (int k = 0; k < kGroup; ++k) r[k] = again(k);
-        most = w.add<T>(r, a.c, again);
-      } else {
-#pragma unroll 1
-        for (int k = 0; k * kRowThreads < here; ++k) {
-          const uint4 r[1] = {again(k)};
-          most = max_nan(most, w.add<T>(r, a.c, [&](int) { return again(k); }));
-        }
       }
+      const float most = w.add_some<T>(r, all, a.c, again, (here + kRowThreads - 1) / kRowThreads);
       pieces.add<kRowThreads>(most);
-      if (g == kRingGroups) {
+      if (g == kAhead) {
         from = after.row + after.head + tid * VEC;
         ahead = (next < a.N ? after.nvec : 0) - tid;
       }
@@ -785,7 +836,7 @@ __global__ void __launch_bounds__(kRowAll, kRowCtas) score_rows_kernel(const Sco
       from += kStep * VEC;
       ahead -= kStep;
       here -= kStep;
-      slot = slot + 1 == kRingGroups ? 0 : slot + 1;
+      slot = slot + 1 == kAhead ? 0 : slot + 1;
     }
     Stats st = w.stats();
     if (tid < sl.loose()) add_value(st, to_f32(sl.row[sl.loose_column(tid)]), a.c);
@@ -913,19 +964,24 @@ int threads_of(long long nvec) {
   return nt;
 }
 
+template <typename T, int kGroup>
+cudaError_t launch_rows(const ScoreFwdArgs& a, int num_sms, cudaStream_t s) {
+  const cudaError_t e = allow_smem<score_rows_kernel<T, kGroup>>(kRowBytes<kGroup>);
+  if (e != cudaSuccess) return e;
+  score_rows_kernel<T, kGroup><<<kRowCtas * num_sms, kRowAll, kRowBytes<kGroup>, s>>>(a);
+  return cudaGetLastError();
+}
+
 }  // namespace
 
 cudaError_t launch_score_fwd(const ScoreFwdArgs& args, int is_bf16, int num_sms, cudaStream_t s) {
   if (args.N == 0) return cudaSuccess;
   ScoreFwdArgs a = args;
   const long long nvec = a.V / (is_bf16 ? 8 : 4);
-  if (a.N > kRowCtas * static_cast<long long>(num_sms) && nvec >= (kRingGroups + 1) * kGroup * kRowThreads) {
-    const auto kernel = is_bf16 ? score_rows_kernel<__nv_bfloat16> : score_rows_kernel<float>;
-    const cudaError_t e = is_bf16 ? allow_smem<score_rows_kernel<__nv_bfloat16>>(kRowBytes)
-                                  : allow_smem<score_rows_kernel<float>>(kRowBytes);
-    if (e != cudaSuccess) return e;
-    kernel<<<kRowCtas * num_sms, kRowAll, kRowBytes, s>>>(a);
-    return cudaGetLastError();
+  if (a.N > kRowCtas * static_cast<long long>(num_sms) && nvec > 3 * 4 * kRowThreads + 8) {
+    return nvec > 2 * 8 * kRowThreads + 8   // more groups than are on their way, wherever a row starts
+               ? is_bf16 ? launch_rows<__nv_bfloat16, 8>(a, num_sms, s) : launch_rows<float, 8>(a, num_sms, s)
+               : is_bf16 ? launch_rows<__nv_bfloat16, 4>(a, num_sms, s) : launch_rows<float, 4>(a, num_sms, s);
   }
   const int nt = threads_of(nvec);
   // few rows: each by several CTAs, until the machine has two CTAs an SM or a thread
