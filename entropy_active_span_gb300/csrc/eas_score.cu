@@ -31,6 +31,7 @@ namespace {
 constexpr int kThreads = 512;     // at most
 constexpr int kCand = 512;        // values that wait to be ordered
 constexpr int kPieces = 8;        // of a thread's part
+constexpr int kTieThreads = 64;   // threads whose maximum is t, and
 constexpr int kTiePieces = 256;   // pieces whose maximum is t that are read again, at most
 constexpr int kMaxSplit = 8;      // CTAs a row
 constexpr int kWhereScore = 40;   // `where` of the status word
@@ -273,7 +274,7 @@ struct Maxima {
 // What the selecting warp works in.
 struct Scratch {
   unsigned long long cand[kCand];
-  uint16_t hit[kThreads];                          // threads that reach t
+  uint16_t hit[kMaxTop + kTieThreads];             // threads that reach t
   uint16_t read[kMaxTop * kPieces + kTiePieces];   // pieces to be read again: above t, then t
 };
 
@@ -341,10 +342,14 @@ __device__ void k_largest(const Slice<T>& sl, const Maxima<NT>& mx, int nt, int 
   const uint32_t t = kth_of_maxima<T, NT>(mx.best, nt, k);
   const int pieces = (groups + span - 1) / span;
 
-  // the threads that reach t, then their pieces that do; at most k threads have some above
-  int above = 0, equal = 0, hits = 0;
+  // the threads above t (at most k) and, if they are few, those at t; then their pieces.
+  // Many at t (a row of equal values, or of -inf): ties are looked for in the order of
+  // the columns instead.
+  int above = 0, equal = 0, hits = 0, at_t = 0;
+  for (int b = 0; b < nt && t; b += 32) at_t += __popc(__ballot_sync(kAll, mx.best[b + lane] == t));
+  const uint32_t from = at_t <= kTieThreads ? t : t + 1;
   for (int b = 0; b < nt && t; b += 32) {
-    const bool hit = mx.best[b + lane] >= t;
+    const bool hit = mx.best[b + lane] >= from;
     const unsigned who = __ballot_sync(kAll, hit);
     if (hit) sc.hit[hits + __popc(who & below)] = static_cast<uint16_t>(b + lane);
     hits += __popc(who);
@@ -365,9 +370,7 @@ __device__ void k_largest(const Slice<T>& sl, const Maxima<NT>& mx, int nt, int 
     equal += __popc(eq);
   }
   __syncwarp();
-  // many pieces with the same maximum (a row of equal values, or of -inf): the ties are
-  // looked for in the order of the columns instead
-  const bool take_ties = t && equal <= kTiePieces;
+  const bool take_ties = t && from == t && equal <= kTiePieces;
   const int todo = above + (take_ties ? equal : 0);
 
   // values above `floor` wait in sc.cand; where it fills up, the k largest of them stay
