@@ -5,20 +5,22 @@
 //   each step  A = X X^T,  B = b A + c A A,  X = a X + B X;  out = scale X.
 //
 // The products run on the tensor cores with fp16 operands and fp32 accumulators.
-// X is kept as a pair of fp16, hi + lo (22 bits); only hi is multiplied, and a X takes
-// both.  What decides the precision is X's own rounding: an error in a direction of
-// small singular values grows with them by a each step, beside large ones that do
-// not grow.  On gradients of low rank with noise, X in one fp16 ends 5e-3 off, in bf16
-// 4e-2, as a pair 2e-4 (512 to 1024 rows, five steps; the output's rounding to bf16 is
-// 1.7e-3).  The roundings of A, B and of hi in the products stay where they are, each
-// step's 2^-11 of its own product.  Everything is stored times 2^12, so that fp16's range covers
-// entries from 2^-36 to 16.
+// X is kept in 14 bits: hi in fp16, and what that leaves out, lo, in e5m2 (times 2^11).
+// hi is multiplied; B holds a on its diagonal, so B hi + a lo is the next X.  What decides
+// the precision is X's own rounding: an error in a direction of small singular values
+// grows with them by a each step, beside large ones that do not grow.  On gradients of low
+// rank with noise, X in one fp16 ends 5e-3 off, in bf16 4e-2, with lo 5e-4 (512 to 1024
+// rows, five steps; Gaussian ones 1.4e-3; the output's rounding to bf16 is 1.7e-3).  The
+// roundings of A, B and of hi in the products stay where they are, each 2^-11 of its own
+// product.  Everything is stored times 2^12, so that fp16's range covers entries from
+// 2^-36 to 16.
 //
 // A and A A are symmetric: only tiles on and above the diagonal are computed, and
 // stored twice, the second time transposed.  A step takes 3 n^2 m + n^3 operations.
 #include <cstring>
 
 #include <cuda_fp16.h>
+#include <cuda_fp8.h>
 
 #include "eas_launch.cuh"
 #include "eas_mma.cuh"
@@ -30,6 +32,7 @@ namespace eas {
 namespace {
 
 constexpr float kUp = 4096.f, kDown = 1.f / 4096.f;   // the stored scale
+constexpr float kLoUp = 2048.f, kLoDown = 1.f / 2048.f;
 constexpr int kWhereMuon = 50;
 
 // ------------------------------------------------- momentum, norm, conversion
@@ -75,17 +78,24 @@ __device__ __forceinline__ void write_values(T* p, const float (&f)[VEC]) {
   }
 }
 
-// Each CTA a chunk of a matrix: the new momentum, u (fp32) where there is a momentum,
-// and the chunk's sum of squares.
-// A thread has kItems vectors (kVec) or single values on their way at a time.
+// The update u of VEC values (and the new momentum in m): in one place, so that the norm
+// and X see the same bits.
+template <int VEC>
+__device__ __forceinline__ void update_of(const MuonArgs& a, const float (&g)[VEC], float (&m)[VEC], float (&u)[VEC]) {
+#pragma unroll
+  for (int j = 0; j < VEC; ++j) {
+    m[j] = fmaf(a.beta, m[j], a.rest * g[j]);
+    u[j] = a.nesterov ? fmaf(a.beta, m[j], a.rest * g[j]) : m[j];
+  }
+}
+
+// Sum of squares of a chunk of a matrix's update.  A thread has kItems vectors (kVec) or
+// single values on their way at a time.
 template <typename G, typename M, bool kMom, bool kVec>
-__device__ double update_chunk(const MuonArgs& a, long long base, long long lo, long long hi) {
+__device__ double chunk_squares(const MuonArgs& a, long long base, long long lo, long long hi) {
   constexpr int VEC = kVec ? 8 : 1, kItems = kVec ? 2 : 8;
-  const float beta = a.beta, rest = a.rest;
   const G* grad = static_cast<const G*>(a.grad) + base;
   const M* mom = static_cast<const M*>(a.mom) + base;
-  M* new_mom = static_cast<M*>(a.new_mom) + base;
-  float* out = a.u + base;
   double sum = 0.;
   for (long long i0 = lo + static_cast<long long>(threadIdx.x) * VEC; i0 < hi; i0 += kItems * kPrepThreads * VEC) {
     float g[kItems][VEC], m[kItems][VEC];
@@ -98,17 +108,10 @@ __device__ double update_chunk(const MuonArgs& a, long long base, long long lo, 
     }
 #pragma unroll
     for (int k = 0; k < kItems; ++k) {
-      const long long i = i0 + k * kPrepThreads * VEC;
-      if (i >= hi) break;
+      if (i0 + k * kPrepThreads * VEC >= hi) break;
       if constexpr (kMom) {
         float u[VEC];
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-          m[k][j] = fmaf(beta, m[k][j], rest * g[k][j]);
-          u[j] = a.nesterov ? fmaf(beta, m[k][j], rest * g[k][j]) : m[k][j];
-        }
-        write_values(new_mom + i, m[k]);
-        write_values(out + i, u);
+        update_of<VEC>(a, g[k], m[k], u);
         sum += squares<VEC>(u);
       } else {
         sum += squares<VEC>(g[k]);
@@ -134,13 +137,13 @@ __device__ double block_sum(double v) {
 
 // grid (chunks, L)
 template <typename G, typename M, bool kMom>
-__global__ void __launch_bounds__(kPrepThreads) muon_update_kernel(const MuonArgs a) {
+__global__ void __launch_bounds__(kPrepThreads) muon_norm_kernel(const MuonArgs a) {
   const long long size = static_cast<long long>(a.rows) * a.cols, base = blockIdx.y * size;
   const long long lo = blockIdx.x * a.chunk, hi = lo + a.chunk < size ? lo + a.chunk : size;
   bool vec = (size & 7) == 0 && aligned16(a.grad);
-  if constexpr (kMom) vec = vec && aligned16(a.mom) && aligned16(a.new_mom);
-  const double sum = block_sum(vec ? update_chunk<G, M, kMom, true>(a, base, lo, hi)
-                                   : update_chunk<G, M, kMom, false>(a, base, lo, hi));
+  if constexpr (kMom) vec = vec && aligned16(a.mom);
+  const double sum = block_sum(vec ? chunk_squares<G, M, kMom, true>(a, base, lo, hi)
+                                   : chunk_squares<G, M, kMom, false>(a, base, lo, hi));
   if (threadIdx.x == 0) {
     a.partial[blockIdx.y * gridDim.x + blockIdx.x] = sum;
     if (blockIdx.x == 0 && blockIdx.y == 0) *a.status = DevStatus{0, 0, 0, 0};
@@ -152,32 +155,42 @@ __global__ void __launch_bounds__(kPrepThreads) muon_update_kernel(const MuonArg
     a.sync[i] = 0;
 }
 
-// Eight values from p on as a pair of fp16 each, times f.
+// A value's hi and lo: pairs of them.
+__device__ __forceinline__ uint32_t hi_bits(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float2 hi_values(uint32_t w) { return __half22float2(*reinterpret_cast<const __half2*>(&w)); }
+__device__ __forceinline__ uint32_t lo_bits(float a, float b, uint32_t hi) {
+  const float2 h = hi_values(hi);
+  return __nv_cvt_float2_to_fp8x2(make_float2((a - h.x) * kLoUp, (b - h.y) * kLoUp), __NV_SATFINITE, __NV_E5M2);
+}
+// Two lo (the lower 16 bits of w), times 2^11: an e5m2 is the upper half of an fp16.
+__device__ __forceinline__ float2 lo_values(uint32_t w) { return hi_values(__byte_perm(w, 0u, 0x1404)); }
+
 __device__ __forceinline__ void write_pair(const MuonPair& x, long long o, const float (&v)[8], float f) {
-  uint4 hi, lo;
-  uint32_t* h = reinterpret_cast<uint32_t*>(&hi);
-  uint32_t* l = reinterpret_cast<uint32_t*>(&lo);
+  uint32_t hi[4], lo[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const float p = v[2 * j] * f, q = v[2 * j + 1] * f;
-    const __half2 a = __floats2half2_rn(p, q);
-    const __half2 b = __floats2half2_rn(p - __low2float(a), q - __high2float(a));
-    h[j] = *reinterpret_cast<const uint32_t*>(&a);
-    l[j] = *reinterpret_cast<const uint32_t*>(&b);
+    hi[j] = hi_bits(p, q);
+    lo[j] = lo_bits(p, q, hi[j]);
   }
-  *reinterpret_cast<uint4*>(x.hi + o) = hi;
-  *reinterpret_cast<uint4*>(x.lo + o) = lo;
+  *reinterpret_cast<uint4*>(x.hi + o) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+  *reinterpret_cast<uint2*>(x.lo + o) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
 }
 
-// X's first pair: src (u, or the gradient where there is no momentum) times 2^12 /
-// (norm + eps), transposed where it is taller than wide.  grid (CTAs, L); a CTA takes
-// 64 x 64 tiles of X in turn.
-template <typename S, bool kTall>
-__global__ void __launch_bounds__(kPrepThreads) muon_scale_kernel(const MuonArgs a, const S* src) {
+// The new momentum, and X's first pair: the update times 2^12 / (norm + eps), transposed
+// where it is taller than wide.  grid (CTAs, L); a CTA takes 64 x 64 tiles of X in turn.
+template <typename G, typename M, bool kMom, bool kTall>
+__global__ void __launch_bounds__(kPrepThreads) muon_scale_kernel(const MuonArgs a) {
   __shared__ float tile[kTall ? 64 : 1][65];
   __shared__ float factor;
   const int tid = threadIdx.x;
-  const long long l = blockIdx.y;
+  const long long l = blockIdx.y, base = l * a.rows * a.cols;
+  const G* grad = static_cast<const G*>(a.grad) + base;
+  const M* mom = static_cast<const M*>(a.mom) + base;
+  M* new_mom = static_cast<M*>(a.new_mom) + base;
   wait_for_launch_before();
   double s = 0.;
   for (int i = tid; i < a.chunks; i += kPrepThreads) s += a.partial[l * a.chunks + i];
@@ -185,28 +198,53 @@ __global__ void __launch_bounds__(kPrepThreads) muon_scale_kernel(const MuonArgs
   if (tid == 0) factor = static_cast<float>(kUp / (sqrt(s) + a.eps));
   __syncthreads();
   const float f = factor;
-  src += l * a.rows * a.cols;
   const int across = (a.m + 63) / 64, tiles = across * ((a.n + 63) / 64);
   // rows of the source in vectors of eight
-  const bool vec = (a.cols & 7) == 0 && aligned16(src);
+  const bool vec = (a.cols & 7) == 0 && aligned16(grad) && (!kMom || (aligned16(mom) && aligned16(new_mom)));
   for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
     const int r0 = t / across * 64, c0 = t % across * 64;      // of X
     // a tile is 64 rows of eight vectors of the source: two a thread
-    float v[2][8];
+    float v[2][8], m[2][8];
+    long long at[2];
+    int left[2];                                               // of the row, from there on
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       const int i = k * kPrepThreads + tid;
       const int sr = (kTall ? c0 : r0) + i / 8, sc = (kTall ? r0 : c0) + i % 8 * 8;
-      const S* p = src + static_cast<long long>(sr) * a.cols + sc;
+      at[k] = static_cast<long long>(sr) * a.cols + sc;
+      left[k] = sr < a.rows ? a.cols - sc : 0;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[k][j] = 0.f;
-      if (sr < a.rows) {
+      for (int j = 0; j < 8; ++j) v[k][j] = m[k][j] = 0.f;
+      if (vec) {
+        if (left[k] > 0) {
+          read_values(grad + at[k], v[k]);
+          if constexpr (kMom) read_values(mom + at[k], m[k]);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (j < left[k]) {
+            v[k][j] = to_f32(grad[at[k] + j]);
+            if constexpr (kMom) m[k][j] = to_f32(mom[at[k] + j]);
+          }
+      }
+    }
+    if constexpr (kMom) {
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        float u[8];
+        update_of<8>(a, v[k], m[k], u);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[k][j] = u[j];
         if (vec) {
-          if (sc < a.cols) read_values(p, v[k]);
+          if (left[k] > 0) write_values(new_mom + at[k], m[k]);
         } else {
 #pragma unroll
           for (int j = 0; j < 8; ++j)
-            if (sc + j < a.cols) v[k][j] = to_f32(p[j]);
+            if (j < left[k]) {
+              const float one[1] = {m[k][j]};
+              store_vec<M, 1>(new_mom + at[k] + j, one);
+            }
         }
       }
     }
@@ -220,7 +258,6 @@ __global__ void __launch_bounds__(kPrepThreads) muon_scale_kernel(const MuonArgs
       __syncthreads();
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        // eight lanes a row of X, four rows a warp: a bank each
         const int i = k * kPrepThreads + tid;
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[k][j] = tile[i % 8 * 8 + j][i / 8];
@@ -275,8 +312,6 @@ struct Geo {
 struct GemmArgs {
   CUtensorMap xk[2], xn[2], xh[2], xl[2];   // X's pairs: rows as operand, columns as operand, stores
   CUtensorMap ak, as, at, bk, bs, bt;       // A and B: operand, store, transposed store
-  const __half *hi[2], *lo[2], *gram;
-  long long ldx, lda;
   int n, m, L, steps;
   int num_m, num_n;                         // tiles down and across X
   int tri, full;                            // tiles of A (or B), of X, a matrix
@@ -356,10 +391,7 @@ __device__ __forceinline__ void load64(uint32_t taddr, float (&v)[64]) {
   tmem_ld32(taddr + 32, *reinterpret_cast<float(*)[32]>(&v[32]));
 }
 
-__device__ __forceinline__ float2 pair_of(const uint4 (&r)[8], int i) {
-  const uint32_t w[4] = {r[i / 4].x, r[i / 4].y, r[i / 4].z, r[i / 4].w};
-  return __half22float2(*reinterpret_cast<const __half2*>(&w[i % 4]));
-}
+__device__ __forceinline__ uint32_t word_of(const uint4& r, int i) { return i == 0 ? r.x : i == 1 ? r.y : i == 2 ? r.z : r.w; }
 
 // The row of a [32][64] fp16 box in the 128-byte swizzled layout.
 __device__ __forceinline__ void get_box(const uint8_t* box, int lane, uint4 (&r)[8]) {
@@ -374,41 +406,47 @@ __device__ __forceinline__ void put_box(uint8_t* box, int lane, const uint32_t (
         make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
 }
 
-__device__ __forceinline__ uint32_t half2_bits(float a, float b) {
-  const __half2 h = __floats2half2_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&h);
+// The same of a [32][64] e5m2 box in the 64-byte swizzled layout: 16-byte block j of the
+// row.
+__device__ __forceinline__ uint4* lo_block(uint8_t* box, int lane, int j) {
+  return reinterpret_cast<uint4*>(box + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4));
 }
 
-// What a storing warp keeps: its two boxes, their load barrier and its phase.
+// What a storing warp keeps: two boxes of 4 KB (the first: A, or the values to be stored;
+// the second: their transpose, or lo of the tile's columns, 64 by 64), their load barrier
+// and its phase.
 struct Boxes {
   uint8_t* box;
   uint64_t* bar;
   uint32_t phase;
 };
 
-// Lane 0: the values of X (hi and lo) or A that the tile's columns from `col` on add to
-// their products, to the warp's boxes.
+// Lane 0: what the tile's columns from `col` on add to their products, to the warp's
+// boxes: A's (64 columns) or lo (all `cols`).
 template <int kKind>
-__device__ __forceinline__ void fetch(const GemmArgs& a, const Tile& w, const Boxes& b, int row0, int col) {
-  if constexpr (kKind == kGram) return;
-  mbar_arrive_expect_tx(b.bar, kKind == kPoly ? 4096 : 8192);
-  const int from = w.step & 1;
-  mma::load_3d<1>(b.box, kKind == kPoly ? &a.as : &a.xh[from], smem_u32(b.bar), col, row0, w.l);
-  if constexpr (kKind >= kApply) mma::load_3d<1>(b.box + 4096, &a.xl[from], smem_u32(b.bar), col, row0, w.l);
+__device__ __forceinline__ void fetch(const GemmArgs& a, const Tile& w, const Boxes& b, int row0, int col, int cols) {
+  if constexpr (kKind == kPoly) {
+    mbar_arrive_expect_tx(b.bar, 4096);
+    mma::load_3d<1>(b.box, &a.as, smem_u32(b.bar), col, row0, w.l);
+  } else if constexpr (kKind >= kApply) {
+    const int n = min((a.m - col + 63) / 64, cols / 64);
+    mbar_arrive_expect_tx(b.bar, 2048 * n);
+    for (int c = 0; c < n; ++c)
+      mma::load_3d<1>(b.box + 4096 + 2048 * c, &a.xl[w.step & 1], smem_u32(b.bar), col + 64 * c, row0, w.l);
+  }
 }
 
 // A warp's 32 rows (from row0 on; this thread's is row0 + lane) and kCols columns
-// (from n0 on) of a tile.  The first columns' values have been fetched.
+// (from n0 on) of a tile.  What the first columns (lo: all) add has been fetched.
 template <int kKind, int kCols>
 __device__ __forceinline__ bool epilogue(const GemmArgs& a, const Tile& w, uint32_t tbase, int row0, int n0,
                                          int lane, Boxes& b, volatile int* abort_flag) {
+  static_assert(kCols <= 128, "lo has room for two boxes");
   const int width = kKind <= kPoly ? a.n : a.m;
   const int row = row0 + lane;
   const bool mirror = kKind <= kPoly && w.m != w.n;
   const int to = (w.step & 1) ^ 1;
   const float* abc = a.coeffs + 3 * w.step;
-  // Poly: b A + c A A; Apply, Last: a X + B X
-  const float f = kKind == kPoly ? abc[1] : abc[0], g = kKind == kPoly ? abc[2] * kDown : kDown;
   const CUtensorMap* s0 = kKind == kGram ? &a.as : kKind == kPoly ? &a.bs : &a.xh[to];
   const CUtensorMap* s1 = kKind == kGram ? &a.at : kKind == kPoly ? &a.bt : &a.xl[to];
   uint8_t* box = b.box;
@@ -417,43 +455,55 @@ __device__ __forceinline__ bool epilogue(const GemmArgs& a, const Tile& w, uint3
     const int col = n0 + c * 64;
     if (col >= width || row0 >= a.n) break;        // the same for the warp
     if (c) {
-      // the boxes have been read (and, Last, written by the lanes) before they are
-      // filled again
-      if constexpr (kKind == kLast) fence_proxy_async_smem();
+      // the first box (Gram, Poly: both) has been read before it is filled again
       __syncwarp();
       if (lane == 0) {
         if constexpr (kKind != kLast) mma::stores_read();
-        fetch<kKind>(a, w, b, row0, col);
+        if constexpr (kKind == kPoly) fetch<kPoly>(a, w, b, row0, col, 64);
       }
     }
     float v[64];
     load64(tbase + c * 64, v);
+    if (kKind == kPoly || (kKind >= kApply && c == 0)) {
+      if (!mma::warp_wait(b.bar, b.phase, abort_flag, a.budget)) return false;
+      b.phase ^= 1u;
+    }
+    uint8_t* lo_box = box + 4096 + 2048 * c;
     if constexpr (kKind == kGram) {
 #pragma unroll
       for (int j = 0; j < 64; ++j) v[j] *= kDown;
-      __syncwarp();                                // lane 0 has waited for the boxes
-    } else {
-      if (!mma::warp_wait(b.bar, b.phase, abort_flag, a.budget)) return false;
-      b.phase ^= 1u;
+    } else if constexpr (kKind == kPoly) {
+      // a I + b A + c A A
+      const float f = abc[1], g = abc[2] * kDown;
       uint4 r[8];
       get_box(box, lane, r);
 #pragma unroll
       for (int j = 0; j < 32; ++j) {
-        const float2 x = pair_of(r, j);
+        const float2 x = hi_values(word_of(r[j / 4], j % 4));
         v[2 * j] = fmaf(v[2 * j], g, f * x.x);
         v[2 * j + 1] = fmaf(v[2 * j + 1], g, f * x.y);
       }
-      if constexpr (kKind >= kApply) {
-        get_box(box + 4096, lane, r);
+      if (!mirror) {
+        const int d = row - col;                   // the diagonal's place in the row
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
-          const float2 x = pair_of(r, j);
-          v[2 * j] = fmaf(f, x.x, v[2 * j]);
-          v[2 * j + 1] = fmaf(f, x.y, v[2 * j + 1]);
+        for (int j = 0; j < 64; ++j) v[j] += j == d ? abc[0] * kUp : 0.f;
+      }
+    } else {
+      // B hi + a lo
+      const float f = abc[0] * kLoDown;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const uint4 r = *lo_block(lo_box, lane, q);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float2 x = lo_values(word_of(r, j / 2) >> (j % 2 * 16));
+          float* o = v + 16 * q + 2 * j;
+          o[0] = fmaf(o[0], kDown, f * x.x);
+          o[1] = fmaf(o[1], kDown, f * x.y);
         }
       }
-      __syncwarp();                                // Poly's transposed box and Last's pairs lie across rows
     }
+    __syncwarp();                                  // lane 0 has waited for the box; lo and A have been read
     if constexpr (kKind == kLast) {
       const float up = a.scale * kDown;
       if (a.tall) {
@@ -488,16 +538,19 @@ __device__ __forceinline__ bool epilogue(const GemmArgs& a, const Tile& w, uint3
     } else {
       uint32_t hi[32];
 #pragma unroll
-      for (int j = 0; j < 32; ++j) hi[j] = half2_bits(v[2 * j], v[2 * j + 1]);
+      for (int j = 0; j < 32; ++j) hi[j] = hi_bits(v[2 * j], v[2 * j + 1]);
       put_box(box, lane, hi);
       if constexpr (kKind == kApply) {
-        uint32_t lo[32];
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
-          const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&hi[j]));
-          lo[j] = half2_bits(v[2 * j] - h.x, v[2 * j + 1] - h.y);
+        for (int q = 0; q < 4; ++q) {
+          uint32_t lo[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int i = 8 * q + 2 * j;
+            lo[j] = lo_bits(v[2 * i], v[2 * i + 1], hi[i]) | lo_bits(v[2 * i + 2], v[2 * i + 3], hi[i + 1]) << 16;
+          }
+          *lo_block(lo_box, lane, q) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
         }
-        put_box(box + 4096, lane, lo);
       } else if (mirror) {
         // [64][32]: the columns as rows
         __half* t = reinterpret_cast<__half*>(box + 4096);
@@ -512,7 +565,7 @@ __device__ __forceinline__ bool epilogue(const GemmArgs& a, const Tile& w, uint3
       __syncwarp();
       if (lane == 0) {
         mma::store_3d(s0, box, col, row0, w.l);
-        if constexpr (kKind == kApply) mma::store_3d(s1, box + 4096, col, row0, w.l);
+        if constexpr (kKind == kApply) mma::store_3d(s1, lo_box, col, row0, w.l);
         else if (mirror) mma::store_3d(s1, box + 4096, row0, col, w.l);
         mma::store_commit();
       }
@@ -756,8 +809,8 @@ __global__ void __launch_bounds__(kThreads, 1) muon_gemm_kernel(const __grid_con
         // the boxes are free: the tile before waited for its stores (and, Last, all
         // lanes are through with theirs)
         fence_async_global();
-        if (w.kind == kPoly) fetch<kPoly>(a, w, b, row0, n0);
-        else if (w.kind >= kApply) fetch<kApply>(a, w, b, row0, n0);
+        if (w.kind == kPoly) fetch<kPoly>(a, w, b, row0, n0, 64);
+        else if (w.kind >= kApply) fetch<kApply>(a, w, b, row0, n0, kCols);
       }
       if (!mma::warp_wait(&tfull[buf], (it >> 1) & 1, abort_flag, a.budget)) {
         report(a.status, kStTimeout, kWhereMuon + 8, t);
@@ -800,22 +853,23 @@ __global__ void __launch_bounds__(kThreads, 1) muon_gemm_kernel(const __grid_con
 
 // ------------------------------------------------------------------ the steps
 
-bool map_of(MapEncoder enc, CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims,
-            const cuuint64_t* strides, const cuuint32_t* box, bool swizzled) {
+bool map_of(MapEncoder enc, CUtensorMap* m, CUtensorMapDataType type, const void* base, int rank,
+            const cuuint64_t* dims, const cuuint64_t* strides, const cuuint32_t* box, CUtensorMapSwizzle swizzle) {
   const cuuint32_t one[4] = {1, 1, 1, 1};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, static_cast<cuuint32_t>(rank), const_cast<void*>(base), dims, strides,
-             box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             swizzled ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
-             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  return enc(m, type, static_cast<cuuint32_t>(rank), const_cast<void*>(base), dims, strides, box, one,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // [L][rows][cols] with row pitch ld, in boxes of bc columns x br rows.
-bool map_3d(MapEncoder enc, CUtensorMap* m, const __half* base, long long cols, long long rows, long long L,
-            long long ld, int bc, int br, bool swizzled = true) {
+template <typename T>
+bool map_3d(MapEncoder enc, CUtensorMap* m, const T* base, long long cols, long long rows, long long L, long long ld,
+            int bc, int br, CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(L)};
-  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld) * 2, static_cast<cuuint64_t>(ld) * 2 * rows};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld) * sizeof(T), static_cast<cuuint64_t>(ld) * sizeof(T) * rows};
   const cuuint32_t box[3] = {static_cast<cuuint32_t>(bc), static_cast<cuuint32_t>(br), 1};
-  return map_of(enc, m, base, 3, dims, strides, box, swizzled);
+  return map_of(enc, m, sizeof(T) == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, base, 3, dims,
+                strides, box, swizzle);
 }
 
 // The same as blocks of 64 columns, two blocks x 64 rows a box: an operand whose rows
@@ -827,7 +881,7 @@ bool map_k_rows(MapEncoder enc, CUtensorMap* m, const __half* base, long long co
                               static_cast<cuuint64_t>(L)};
   const cuuint64_t strides[3] = {static_cast<cuuint64_t>(ld) * 2, 128, static_cast<cuuint64_t>(ld) * 2 * rows};
   const cuuint32_t box[4] = {64, 64, 2, 1};
-  return map_of(enc, m, base, 4, dims, strides, box, true);
+  return map_of(enc, m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, base, 4, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 template <int CG>
@@ -836,24 +890,19 @@ cudaError_t run_steps(const MuonArgs& a, MapEncoder enc, int num_sms, cudaStream
   memset(&g, 0, sizeof(g));
   bool ok = true;
   for (int i = 0; i < 2; ++i) {
-    g.hi[i] = a.x[i].hi;
-    g.lo[i] = a.x[i].lo;
     ok = ok && map_3d(enc, &g.xk[i], a.x[i].hi, a.m, a.n, a.L, a.ldx, 64, 128) &&
          map_k_rows(enc, &g.xn[i], a.x[i].hi, a.m, a.n, a.L, a.ldx) &&
          map_3d(enc, &g.xh[i], a.x[i].hi, a.m, a.n, a.L, a.ldx, 64, 32) &&
-         map_3d(enc, &g.xl[i], a.x[i].lo, a.m, a.n, a.L, a.ldx, 64, 32);
+         map_3d(enc, &g.xl[i], a.x[i].lo, a.m, a.n, a.L, a.ldx, 64, 32, CU_TENSOR_MAP_SWIZZLE_64B);
   }
   ok = ok && map_3d(enc, &g.ak, a.gram, a.n, a.n, a.L, a.lda, 64, 128) &&
        map_3d(enc, &g.as, a.gram, a.n, a.n, a.L, a.lda, 64, 32) &&
-       map_3d(enc, &g.at, a.gram, a.n, a.n, a.L, a.lda, 32, 64, false) &&
+       map_3d(enc, &g.at, a.gram, a.n, a.n, a.L, a.lda, 32, 64, CU_TENSOR_MAP_SWIZZLE_NONE) &&
        map_3d(enc, &g.bk, a.poly, a.n, a.n, a.L, a.lda, 64, 128) &&
        map_3d(enc, &g.bs, a.poly, a.n, a.n, a.L, a.lda, 64, 32) &&
-       map_3d(enc, &g.bt, a.poly, a.n, a.n, a.L, a.lda, 32, 64, false);
+       map_3d(enc, &g.bt, a.poly, a.n, a.n, a.L, a.lda, 32, 64, CU_TENSOR_MAP_SWIZZLE_NONE);
   if (!ok) return cudaErrorInvalidValue;
   constexpr int T = Geo<CG>::kM;
-  g.gram = a.gram;
-  g.ldx = a.ldx;
-  g.lda = a.lda;
   g.n = a.n;
   g.m = a.m;
   g.L = a.L;
@@ -893,23 +942,21 @@ cudaError_t run_steps(const MuonArgs& a, MapEncoder enc, int num_sms, cudaStream
   return cudaLaunchKernelEx(&cfg, kernel, g);
 }
 
-template <typename S>
-cudaError_t scale(const MuonArgs& a, const S* src, int num_sms, cudaStream_t s) {
-  const long long tiles = static_cast<long long>((a.m + 63) / 64) * ((a.n + 63) / 64), most = 8LL * num_sms;
-  const dim3 grid(static_cast<unsigned>(tiles < most ? tiles : most), static_cast<unsigned>(a.L));
-  return a.tall ? launch_overlapped(muon_scale_kernel<S, true>, grid, dim3(kPrepThreads), 0, s, a, src)
-                : launch_overlapped(muon_scale_kernel<S, false>, grid, dim3(kPrepThreads), 0, s, a, src);
-}
-
-template <typename G>
+template <typename G, typename M, bool kMom>
 cudaError_t prepare(const MuonArgs& a, int num_sms, cudaStream_t s) {
-  const dim3 grid(static_cast<unsigned>(a.chunks), static_cast<unsigned>(a.L));
-  if (!a.mom) muon_update_kernel<G, float, false><<<grid, kPrepThreads, 0, s>>>(a);
-  else if (a.mom_bf16) muon_update_kernel<G, __nv_bfloat16, true><<<grid, kPrepThreads, 0, s>>>(a);
-  else muon_update_kernel<G, float, true><<<grid, kPrepThreads, 0, s>>>(a);
+  const dim3 chunks(static_cast<unsigned>(a.chunks), static_cast<unsigned>(a.L));
+  muon_norm_kernel<G, M, kMom><<<chunks, kPrepThreads, 0, s>>>(a);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  return a.mom ? scale<float>(a, a.u, num_sms, s) : scale<G>(a, static_cast<const G*>(a.grad), num_sms, s);
+  const long long tiles = static_cast<long long>((a.m + 63) / 64) * ((a.n + 63) / 64), most = 8LL * num_sms;
+  const dim3 grid(static_cast<unsigned>(tiles < most ? tiles : most), static_cast<unsigned>(a.L));
+  return a.tall ? launch_overlapped(muon_scale_kernel<G, M, kMom, true>, grid, dim3(kPrepThreads), 0, s, a)
+                : launch_overlapped(muon_scale_kernel<G, M, kMom, false>, grid, dim3(kPrepThreads), 0, s, a);
+}
+template <typename G>
+cudaError_t prepare(const MuonArgs& a, int num_sms, cudaStream_t s) {
+  return !a.mom ? prepare<G, float, false>(a, num_sms, s)
+         : a.mom_bf16 ? prepare<G, __nv_bfloat16, true>(a, num_sms, s) : prepare<G, float, true>(a, num_sms, s);
 }
 
 }  // namespace
@@ -924,14 +971,14 @@ MuonPlan muon_plan(long long L, long long rows, long long cols) {
   p.chunk = (p.chunk + 7) / 8 * 8;
   p.chunks = (size + p.chunk - 1) / p.chunk;
   auto up = [](size_t x) { return (x + 1023) / 1024 * 1024; };
-  const size_t x = up(static_cast<size_t>(2 * L * n * p.ldx)), q = up(static_cast<size_t>(2 * L * n * p.lda));
+  const size_t x = up(static_cast<size_t>(L * n * p.ldx)), q = up(static_cast<size_t>(2 * L * n * p.lda));
   // a drawing counter (a line of its own) and one a tile, of the smaller tiles
   const size_t tn = static_cast<size_t>((n + 127) / 128), tm = static_cast<size_t>((m + 127) / 128);
   p.sync_words = 32 + static_cast<size_t>(L) * tn * (2 * tn + tm);
   p.sync = up(sizeof(DevStatus));
   p.partial = p.sync + up(4 * p.sync_words);
   p.x[0] = p.partial + up(static_cast<size_t>(8 * L * p.chunks));
-  for (int i = 1; i < 4; ++i) p.x[i] = p.x[i - 1] + x;
+  for (int i = 1; i < 4; ++i) p.x[i] = p.x[i - 1] + (i % 2 ? 2 : 1) * x;     // hi, lo, hi, lo
   p.gram = p.x[3] + x;
   p.poly = p.gram + q;
   p.total = p.poly + q;

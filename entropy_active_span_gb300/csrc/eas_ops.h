@@ -145,7 +145,7 @@ constexpr int kMuonSteps = 32;    // EAS_MAX_MUON_STEPS
 struct MuonPlan {         // sizes of the workspace, in bytes from its start
   size_t sync, sync_words;
   size_t partial;         // double [L][chunks]
-  size_t x[4];            // X's two pairs: hi, lo, hi, lo; u [L][rows][cols] fp32 from x[2] on
+  size_t x[4];            // X's two pairs: hi (fp16), lo (e5m2), hi, lo
   size_t gram, poly;
   size_t total;
   long long ldx, lda;     // row pitches in elements
@@ -154,7 +154,7 @@ struct MuonPlan {         // sizes of the workspace, in bytes from its start
 MuonPlan muon_plan(long long L, long long rows, long long cols);
 struct MuonPair {
   __half* hi;
-  __half* lo;
+  uint8_t* lo;
 };
 struct MuonArgs {
   const void* grad;       // [L][rows][cols]
@@ -171,7 +171,6 @@ struct MuonArgs {
   __nv_bfloat16* out;     // [L][rows][cols]
   double* partial;
   int chunk, chunks;
-  float* u;
   MuonPair x[2];
   __half* gram;           // A
   __half* poly;           // B

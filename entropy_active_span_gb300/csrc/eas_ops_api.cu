@@ -453,8 +453,7 @@ eas_status eas_orthogonalize(const void* grad, eas_dtype grad_dtype, const void*
   a.partial = at<double>(ws, p.partial);
   a.chunk = static_cast<int>(p.chunk);
   a.chunks = static_cast<int>(p.chunks);
-  a.u = at<float>(ws, p.x[2]);
-  for (int i = 0; i < 2; ++i) a.x[i] = {at<__half>(ws, p.x[2 * i]), at<__half>(ws, p.x[2 * i + 1])};
+  for (int i = 0; i < 2; ++i) a.x[i] = {at<__half>(ws, p.x[2 * i]), at<uint8_t>(ws, p.x[2 * i + 1])};
   a.gram = at<__half>(ws, p.gram);
   a.poly = at<__half>(ws, p.poly);
   a.ldx = p.ldx;

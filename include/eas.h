@@ -532,7 +532,7 @@ eas_status eas_token_logprobs_bwd(const float* g_logprob, const float* g_entropy
  *   (u = g without a momentum);  X = u / (|u| + eps), the 2-norm over the matrix;
  *   for each (a, b, c) of coeffs:  Q = X X^T,  X = a X + (b Q + c Q Q) X;
  *   out = bf16(scale X).
- * Products take fp16 operands (X itself is kept in 22 bits) and fp32 sums: out is
+ * Products take fp16 operands (X itself is kept in 14 bits) and fp32 sums: out is
  * within about 2e-3 of its norm, its rounding to bf16 alone being 1.7e-3.  Singular
  * values have to stay below 4 through all steps, and |a| + |b| s^2 + |c| s^4 below 16
  * (with the usual coefficients they stay below 1.3).  Results repeat to the bit.  Where
@@ -548,7 +548,7 @@ eas_status eas_token_logprobs_bwd(const float* g_logprob, const float* g_entropy
  *   eps      > 0 (a zero matrix gives zeros)
  *   out      [L][rows][cols] bf16
  *   ws       eas_orthogonalize_workspace_size(L, rows, cols) bytes, about
- *            8 + 4 n / m bytes an element for n <= m; holds the status word
+ *            6 + 4 n / m bytes an element for n <= m; holds the status word
  * rows and cols are at most EAS_MAX_MUON_SIDE, L at most 65535.
  */
 #define EAS_MAX_MUON_SIDE 65536

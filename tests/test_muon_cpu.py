@@ -41,7 +41,7 @@ def test_workspace(libeas):
     size = libeas.eas_orthogonalize_workspace_size
     assert call(libeas, ws_bytes=size(L, R, C) - 1) == WORKSPACE
     assert size(-1, 4, 4) == size(1, 0, 4) == size(1, 4, 65537) == 0
-    assert size(1, 4096, 4096) >= (8 + 4) * 4096 * 4096
+    assert size(1, 4096, 4096) >= (6 + 4) * 4096 * 4096
     assert size(0, 4, 4) > 0 and size(2, 100, 300) == size(2, 300, 100)
 
 
