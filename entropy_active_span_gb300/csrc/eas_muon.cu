@@ -291,12 +291,13 @@ __global__ void __launch_bounds__(kPrepThreads) muon_scale_kernel(const MuonArgs
 enum Kind { kGram, kPoly, kApply, kLast };
 
 constexpr int kStoreWarps = 8;
-constexpr int kThreads = 64 + 32 * kStoreWarps;
+constexpr int kThreads = 96 + 32 * kStoreWarps;
 constexpr int kStages = 5;
-constexpr int kRing = 4;                           // tile numbers on their way to the warps
+constexpr int kRing = 3;                           // tile numbers on their way to the warps
 constexpr int kOperand = 16384;                    // 128 rows (columns) x 64 k
 constexpr int kEpiWarp = 8192;                     // two boxes a warp
 constexpr int kSmem = kStages * 2 * kOperand + kStoreWarps * kEpiWarp + 1024 + 512;
+constexpr int kDrawAhead = 6;                      // k-blocks before a tile's end
 constexpr int kBand = 4;                           // rows of tiles of X that are computed together
 
 // CG = 2: a pair of CTAs computes 256 x 256 tiles, each 128 of the rows; CG = 1: a CTA
@@ -372,6 +373,10 @@ __device__ __forceinline__ void release_add(int* p) {
 }
 // Orders this thread's acquired or released values with its TMA loads or stores.
 __device__ __forceinline__ void fence_async_global() { asm volatile("fence.proxy.async.global;" ::: "memory"); }
+
+// How far a CTA's it-th tile has its operands: `chunks` of them.  Grows from tile to tile
+// (and wraps around).
+__device__ __forceinline__ uint32_t operands_to(int it, int chunks) { return (static_cast<uint32_t>(it) << 12) + chunks; }
 
 // Counter of the operand that a tile reads at chunk c of k: its first operand's
 // (which = 0) or its second one's.  null: none to wait for.
@@ -574,8 +579,10 @@ __device__ __forceinline__ bool epilogue(const GemmArgs& a, const Tile& w, uint3
   return true;
 }
 
-// Warp 0 draws tiles, waits for their operands and loads them, warp 1 issues the MMAs,
-// warps 2 to 9 store (two for each 32 rows, half of the columns each); two accumulators, so that a tile's stores run under the next
+// Warp 0 loads, warp 1 issues the MMAs, warps 2 to 9 store (two for each 32 rows, half of
+// the columns each), and the last warp draws the next tile and watches its operands'
+// counters while this one's are loaded (the loads are what bounds a tile: 32 KB of
+// operands for 512 clocks of MMA); two accumulators, so that a tile's stores run under the next
 // one's products.
 template <int CG>
 __global__ void __launch_bounds__(kThreads, 1) muon_gemm_kernel(const __grid_constant__ GemmArgs a) {
@@ -594,9 +601,11 @@ __global__ void __launch_bounds__(kThreads, 1) muon_gemm_kernel(const __grid_con
   uint64_t* rempty = rfull + kRing;
   uint64_t* there = rempty + kRing;        // of the tile in a ring slot: its operands
   uint64_t* fetched = there + kRing;       // of a storing warp: what it adds
-  uint64_t* drain = fetched + kStoreWarps;
+  uint64_t* near_end = fetched + kStoreWarps;   // of the tile that is being loaded
+  uint64_t* drain = near_end + 1;
   int* ring = reinterpret_cast<int*>(drain + 1);
-  uint32_t* slot_addr = reinterpret_cast<uint32_t*>(ring + kRing);
+  volatile uint32_t* progress = reinterpret_cast<volatile uint32_t*>(ring + kRing);   // see operands_to
+  uint32_t* slot_addr = reinterpret_cast<uint32_t*>(ring + 2 * kRing);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(slot_addr + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -613,10 +622,12 @@ __global__ void __launch_bounds__(kThreads, 1) muon_gemm_kernel(const __grid_con
     }
     for (int i = 0; i < kRing; ++i) {
       mbar_init(&rfull[i], 1);
-      mbar_init(&rempty[i], (1 + kStoreWarps) * CG);   // MMA warp (CTA 1: loader), storing warps
+      mbar_init(&rempty[i], (2 + kStoreWarps) * CG);   // loader, MMA warp (CTA 1: drawer), storing warps
       mbar_init(&there[i], 1);
+      progress[i] = 0;
     }
     for (int i = 0; i < kStoreWarps; ++i) mbar_init(&fetched[i], 1);
+    mbar_init(near_end, 1);
     mbar_init(drain, 1);
     *abort_flag = 0;
     fence_barrier_init();
@@ -631,17 +642,87 @@ __global__ void __launch_bounds__(kThreads, 1) muon_gemm_kernel(const __grid_con
   const uint32_t rempty0 = mma::leader_addr<CG>(&rempty[0]);
 
   if (warp == 0) {
-    int stage = 0;
-    uint32_t phase = 0;
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      const uint32_t full0 = mma::leader_addr<CG>(&full[0]);
+      for (int it = 0; ok; ++it) {
+        const int slot = it % kRing;
+        if (!mma::wait(&rfull[slot], (it / kRing) & 1, abort_flag, a.budget)) {
+          report(a.status, kStTimeout, kWhereMuon, it);
+          break;
+        }
+        const int t = ring[slot];
+        mma::arrive_at(rempty0 + 8 * slot);
+        if (t < 0) break;
+        const Tile w = tile_of(t, a);
+        const int from = w.step & 1;
+        const CUtensorMap* ma = w.kind == kGram ? &a.xk[from] : w.kind == kPoly ? &a.ak : &a.bk;
+        const CUtensorMap* mb = w.kind == kGram ? &a.xk[from] : w.kind == kPoly ? &a.ak : &a.xn[from];
+        const int mrow = w.m * G::kM + static_cast<int>(rank) * 128;
+        const int ncol = w.n * G::kN + static_cast<int>(rank) * 128;
+        const int num_kb = ((w.kind == kGram ? a.m : a.n) + 63) / 64;
+        int known = 0;                       // k-blocks whose operands are there
+        for (int kb = 0; kb < num_kb; ++kb) {
+          if (kb == known) {
+            const uint32_t want = operands_to(it, kb / G::kChunk + 1);
+            const long long t0 = clock64();
+            uint32_t have;
+            while (static_cast<int>((have = progress[slot]) - want) < 0) {
+              if (*abort_flag || clock64() - t0 > a.budget) {
+                ok = false;
+                break;
+              }
+            }
+            if (!ok) {
+              *abort_flag = 1;
+              report(a.status, kStTimeout, kWhereMuon + 1, t);
+              break;
+            }
+            __threadfence_block();
+            fence_async_global();
+            known = (kb / G::kChunk + 1 + static_cast<int>(have - want)) * G::kChunk;
+          }
+          if (!mma::wait(&empty[stage], phase ^ 1u, abort_flag, a.budget)) {
+            report(a.status, kStTimeout, kWhereMuon + 2, t);
+            ok = false;
+            break;
+          }
+          // the next tile is drawn now: earlier, tiles would wait here that others could
+          // begin with
+          if (leader && kb == max(num_kb - kDrawAhead, 0)) mbar_arrive(near_end);
+          const uint32_t bar = full0 + 8 * stage;
+          if (leader) mbar_arrive_expect_tx(&full[stage], CG * 2 * kOperand);
+          mma::load_3d<CG>(s_a + stage * kOperand, ma, bar, kb * 64, mrow, w.l);
+          if (w.kind <= kPoly) mma::load_3d<CG>(s_b + stage * kOperand, mb, bar, kb * 64, ncol, w.l);
+          else mma::load_4d<CG>(s_b + stage * kOperand, mb, bar, 0, kb * 64, ncol >> 6, w.l);
+          if (++stage == kStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      if (!ok && leader) {
+        // loads on their way still land
+        for (int i = 0; i < kStages; ++i) {
+          const uint32_t par = i < stage ? phase : phase ^ 1u;
+          const long long t0 = clock64();
+          while (!mma::try_wait(&full[i], par) && clock64() - t0 < a.budget) {
+          }
+        }
+      }
+    }
+  } else if (warp == kThreads / 32 - 1) {
     bool ok = true;
-    const uint32_t full0 = mma::leader_addr<CG>(&full[0]);
     for (int it = 0; ok; ++it) {
       const int slot = it % kRing;
       const uint32_t rph = (it / kRing) & 1;
       int t = -1;
       if (lane == 0) {
         if (leader) {
-          ok = mma::wait(&rempty[slot], rph ^ 1u, abort_flag, a.budget);
+          ok = mma::wait(&rempty[slot], rph ^ 1u, abort_flag, a.budget) &&
+               (it == 0 || mma::wait(near_end, (it - 1) & 1, abort_flag, a.budget));
           if (ok) {
             const int got = atomicAdd(a.counter, 1);
             t = got < total ? got : -1;
@@ -656,78 +737,43 @@ __global__ void __launch_bounds__(kThreads, 1) muon_gemm_kernel(const __grid_con
             mma::arrive_at(rempty0 + 8 * slot);
           }
         }
-        if (!ok) report(a.status, kStTimeout, kWhereMuon, it);
+        if (!ok) report(a.status, kStTimeout, kWhereMuon + 10, it);
       }
       ok = __shfl_sync(0xffffffffu, ok, 0);
       t = __shfl_sync(0xffffffffu, t, 0);
       if (!ok || t < 0) break;
       const Tile w = tile_of(t, a);
-      const int from = w.step & 1;
-      const CUtensorMap* ma = w.kind == kGram ? &a.xk[from] : w.kind == kPoly ? &a.ak : &a.bk;
-      const CUtensorMap* mb = w.kind == kGram ? &a.xk[from] : w.kind == kPoly ? &a.ak : &a.xn[from];
-      const int mrow = w.m * G::kM + static_cast<int>(rank) * 128;
-      const int ncol = w.n * G::kN + static_cast<int>(rank) * 128;
       const int num_kb = ((w.kind == kGram ? a.m : a.n) + 63) / 64;
       const int chunks = (num_kb + G::kChunk - 1) / G::kChunk;
       const int want = G::kDone * (w.kind == kGram ? w.step : w.step + 1);
       for (int c0 = 0; ok && c0 < chunks; c0 += 16) {
         // lanes 0 to 15 watch the first operand's counters, 16 to 31 the second one's
-        const int mine = c0 + (lane & 15);
+        const int mine = c0 + (lane & 15), most = min(chunks - c0, 16);
         const int* at = mine < chunks ? operand_counter<CG>(w, mine, lane >> 4, a) : nullptr;
-        bool ready = !at || acquire(at) >= want;
-        unsigned have = __ballot_sync(0xffffffffu, ready);
-        for (int c = c0; ok && c < min(c0 + 16, chunks); ++c) {
-          const unsigned need = 0x10001u << (c - c0);
-          const long long t0 = clock64();
-          while ((have & need) != need) {
-            if (!ready) ready = acquire(at) >= want;
-            have = __ballot_sync(0xffffffffu, ready);
+        bool ready = !at;
+        int have = 0;                      // of these chunks, from the first on
+        long long t0 = clock64();
+        while (ok && have < most) {
+          if (!ready) ready = acquire(at) >= want;
+          const unsigned who = __ballot_sync(0xffffffffu, ready), both = who & who >> 16 & 0xffffu;
+          const int now = min(most, __ffs(~both) - 1);
+          if (now > have) {
+            have = now;
+            __threadfence_block();         // every lane's acquires before the word that tells of them
+            __syncwarp();
+            if (lane == 0) progress[slot] = operands_to(it, c0 + have);
+            t0 = clock64();
+          } else {
             const bool stop = *abort_flag || clock64() - t0 > a.budget;
-            if (__any_sync(0xffffffffu, stop)) {
-              ok = (have & need) == need;
-              break;
-            }
+            ok = !__any_sync(0xffffffffu, stop);
           }
-          if (!ok) {
-            if (lane == 0) {
-              *abort_flag = 1;
-              report(a.status, kStTimeout, kWhereMuon + 1, t);
-            }
-            break;
-          }
-          __syncwarp();                    // the counters' acquires, for lane 0
-          if (lane == 0) {
-            fence_async_global();
-            if (c == chunks - 1) mbar_arrive(&there[slot]);
-            for (int kb = c * G::kChunk; kb < min((c + 1) * G::kChunk, num_kb); ++kb) {
-              if (!mma::wait(&empty[stage], phase ^ 1u, abort_flag, a.budget)) {
-                report(a.status, kStTimeout, kWhereMuon + 2, t);
-                ok = false;
-                break;
-              }
-              const uint32_t bar = full0 + 8 * stage;
-              if (leader) mbar_arrive_expect_tx(&full[stage], CG * 2 * kOperand);
-              mma::load_3d<CG>(s_a + stage * kOperand, ma, bar, kb * 64, mrow, w.l);
-              if (w.kind <= kPoly) mma::load_3d<CG>(s_b + stage * kOperand, mb, bar, kb * 64, ncol, w.l);
-              else mma::load_4d<CG>(s_b + stage * kOperand, mb, bar, 0, kb * 64, ncol >> 6, w.l);
-              if (++stage == kStages) {
-                stage = 0;
-                phase ^= 1u;
-              }
-            }
-          }
-          ok = __shfl_sync(0xffffffffu, ok, 0);
+        }
+        if (!ok && lane == 0) {
+          *abort_flag = 1;
+          report(a.status, kStTimeout, kWhereMuon + 11, t);
         }
       }
-    }
-    if (!ok && leader && lane == 0) {
-      // loads on their way still land
-      for (int i = 0; i < kStages; ++i) {
-        const uint32_t par = i < stage ? phase : phase ^ 1u;
-        const long long t0 = clock64();
-        while (!mma::try_wait(&full[i], par) && clock64() - t0 < a.budget) {
-        }
-      }
+      if (ok && lane == 0) mbar_arrive(&there[slot]);
     }
   } else if (warp == 1) {
     if (leader && lane == 0) {
