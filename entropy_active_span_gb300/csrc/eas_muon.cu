@@ -897,6 +897,309 @@ __global__ void __launch_bounds__(kThreads, 1) muon_gemm_kernel(const __grid_con
   }
 }
 
+// ------------------------------------------------------------- small matrices
+//
+// Up to 128 rows and 512 columns of X: a CTA does a matrix from its gradient to its
+// update.  X's hi lies in shared memory as blocks of 64 columns, [128 rows][128 bytes],
+// swizzled: the layout of an operand whose rows are the result's (X X^T) and, read the
+// other way, of one whose rows are k (B X).  A and then B take two more such blocks, and
+// lo a row-major array.  No product waits for memory: 12 x [128][128] in fp32 take 78 us
+// over the counters above.
+
+constexpr int kSmallRows = 128, kSmallCols = 512, kSmallThreads = 256;
+constexpr int small_bytes(int m) { return (m + 63) / 64 * (16384 + 8192) + 32768 + 1024 + 256; }
+
+// 16-byte block j of row r in a block of 64 columns.
+__device__ __forceinline__ uint4* swizzled(uint8_t* block, int r, int j) {
+  return reinterpret_cast<uint4*>(block + r * 128 + ((j ^ (r & 7)) << 4));
+}
+// Eight columns (8 j0 on) of a row of X to their block of 64 and to lo's, which is
+// [8][128 rows] of eight values.
+__device__ __forceinline__ void put_x(uint8_t* hi, uint8_t* lo, int r, int j0, const float (&v)[8]) {
+  uint32_t h[4], l[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    h[j] = hi_bits(v[2 * j], v[2 * j + 1]);
+    l[j] = lo_bits(v[2 * j], v[2 * j + 1], h[j]);
+  }
+  *swizzled(hi, r, j0) = make_uint4(h[0], h[1], h[2], h[3]);
+  *reinterpret_cast<uint2*>(lo + (j0 * 128 + r) * 8) = make_uint2(l[0] | l[1] << 16, l[2] | l[3] << 16);
+}
+
+template <typename G, typename M, bool kMom>
+__global__ void __launch_bounds__(kSmallThreads) muon_small_kernel(const __grid_constant__ MuonArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* s_x = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                            ~static_cast<uintptr_t>(1023));
+  const int blocks = (a.m + 63) / 64;
+  uint8_t* s_a = s_x + blocks * 16384;
+  uint8_t* s_lo = s_a + 32768;
+  uint64_t* bar = reinterpret_cast<uint64_t*>(s_lo + blocks * 8192);
+  uint32_t* slot = reinterpret_cast<uint32_t*>(bar + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(slot + 1);
+  float* factor = reinterpret_cast<float*>(slot + 2);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const long long l = blockIdx.x, base = l * a.rows * a.cols;
+  const uint32_t cols = blocks <= 2 ? 128 : blocks <= 4 ? 256 : 512;
+  if (tid == 0) {
+    mbar_init(bar, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+    if (l == 0) *a.status = DevStatus{0, 0, 0, 0};
+  }
+  if (warp == 0) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(slot)), "r"(cols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+
+  // the norm
+  const G* grad = static_cast<const G*>(a.grad) + base;
+  const M* mom = static_cast<const M*>(a.mom) + base;
+  M* new_mom = static_cast<M*>(a.new_mom) + base;
+  const int size = a.rows * a.cols;
+  double sum = 0.;
+  for (int i0 = tid; i0 < size; i0 += 8 * kSmallThreads) {
+    float g[8], m[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int i = i0 + k * kSmallThreads;
+      g[k] = i < size ? to_f32(grad[i]) : 0.f;
+      m[k] = 0.f;
+      if constexpr (kMom) m[k] = i < size ? to_f32(mom[i]) : 0.f;
+    }
+    if constexpr (kMom) {
+      float u[8];
+      update_of<8>(a, g, m, u);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) g[k] = u[k];
+    }
+    sum += squares<8>(g);
+  }
+  sum = block_sum(sum);
+  if (tid == 0) *factor = static_cast<float>(kUp / (sqrt(sum) + a.eps));
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *slot;
+  const float f = *factor;
+  // X, zeros around it: eight columns of a row at a time, four times that on their way;
+  // lanes next to one another along the rows of what came
+  constexpr int kItems = 4;
+  const bool vec = !a.tall && (a.cols & 7) == 0 && aligned16(grad) && (!kMom || (aligned16(mom) && aligned16(new_mom)));
+  auto place = [&](int i, int& r, int& j0) {
+    if (a.tall) {
+      r = i % kSmallRows;
+      j0 = i / kSmallRows;
+    } else {
+      const int eight = blocks * 8;
+      r = i / eight;
+      j0 = i - r * eight;
+    }
+  };
+  auto source = [&](int r, int c) { return a.tall ? c * a.cols + r : r * a.cols + c; };
+  const int items = kSmallRows * blocks * 8;         // a multiple of kItems * kSmallThreads
+  for (int i0 = tid; i0 < items; i0 += kItems * kSmallThreads) {
+    float v[kItems][8], m[kItems][8];
+#pragma unroll
+    for (int k = 0; k < kItems; ++k) {
+      int r, j0;
+      place(i0 + k * kSmallThreads, r, j0);
+      const int c = j0 * 8;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[k][j] = m[k][j] = 0.f;
+      if (vec) {
+        if (r < a.n && c < a.m) {
+          read_values(grad + source(r, c), v[k]);
+          if constexpr (kMom) read_values(mom + source(r, c), m[k]);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (r < a.n && c + j < a.m) {
+            v[k][j] = to_f32(grad[source(r, c + j)]);
+            if constexpr (kMom) m[k][j] = to_f32(mom[source(r, c + j)]);
+          }
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kItems; ++k) {
+      int r, j0;
+      place(i0 + k * kSmallThreads, r, j0);
+      const int c = j0 * 8;
+      if constexpr (kMom) {
+        float u[8];
+        update_of<8>(a, v[k], m[k], u);
+        if (vec) {
+          if (r < a.n && c < a.m) write_values(new_mom + source(r, c), m[k]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float one[1] = {m[k][j]};
+            if (r < a.n && c + j < a.m) store_vec<M, 1>(new_mom + source(r, c + j), one);
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[k][j] = u[j];
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[k][j] *= f;
+      put_x(s_x + (j0 >> 3) * 16384, s_lo + (j0 >> 3) * 8192, r, j0 & 7, v[k]);
+    }
+  }
+
+  const int q = warp & 3, half = warp >> 2, row = q * 32 + lane;
+  const uint32_t trow = tmem + (static_cast<uint32_t>(q * 32) << 16);
+  uint32_t phase = 0;
+  bool ok = true;
+  // What the threads wrote is there for the tensor cores; then `issue` by one thread, and
+  // everybody waits for its products.
+  auto products = [&](auto issue) {
+    fence_proxy_async_smem();
+    tc_fence_before();
+    __syncthreads();
+    if (tid == 0) {
+      tc_fence_after();
+      issue();
+      mma::commit<1>(bar);
+    }
+    const bool done = mma::wait(bar, phase, abort_flag, a.budget);
+    phase ^= 1u;
+    ok = !__syncthreads_or(!done);
+    tc_fence_after();
+  };
+  for (int step = 0; ok && step < a.steps; ++step) {
+    const float ca = a.small_coeffs[3 * step], cb = a.small_coeffs[3 * step + 1], cc = a.small_coeffs[3 * step + 2];
+    // A = X X^T
+    products([&] {
+      const uint32_t x = smem_u32(s_x);
+      for (int k = 0; k < 4 * blocks; ++k) {
+        const uint64_t d = sdesc_sw128(x + (k >> 2) * 16384 + (k & 3) * 32, 16, 1024);
+        mma::mma_f16<1>(tmem, d, d, mma::idesc_f16_f32(128, 128, false, false), k > 0);
+      }
+    });
+    if (!ok) break;
+    uint8_t* mine = s_a + half * 16384;              // this thread's 64 columns of A's row
+    float v[64];
+    load64(trow + half * 64, v);
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      *swizzled(mine, row, j) = make_uint4(
+          hi_bits(v[8 * j] * kDown, v[8 * j + 1] * kDown), hi_bits(v[8 * j + 2] * kDown, v[8 * j + 3] * kDown),
+          hi_bits(v[8 * j + 4] * kDown, v[8 * j + 5] * kDown), hi_bits(v[8 * j + 6] * kDown, v[8 * j + 7] * kDown));
+    // B = a I + b A + c A A, in A's place
+    products([&] {
+      const uint32_t x = smem_u32(s_a);
+      for (int k = 0; k < 8; ++k) {
+        const uint64_t d = sdesc_sw128(x + (k >> 2) * 16384 + (k & 3) * 32, 16, 1024);
+        mma::mma_f16<1>(tmem, d, d, mma::idesc_f16_f32(128, 128, false, false), k > 0);
+      }
+    });
+    if (!ok) break;
+    load64(trow + half * 64, v);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const uint4 r = *swizzled(mine, row, j);
+      uint32_t h[4];
+#pragma unroll
+      for (int p = 0; p < 4; ++p) {
+        const float2 x = hi_values(word_of(r, p));
+        const int c = 8 * j + 2 * p;
+        float b0 = fmaf(v[c], cc * kDown, cb * x.x), b1 = fmaf(v[c + 1], cc * kDown, cb * x.y);
+        if (row == half * 64 + c) b0 += ca * kUp;
+        if (row == half * 64 + c + 1) b1 += ca * kUp;
+        h[p] = hi_bits(b0, b1);
+      }
+      *swizzled(mine, row, j) = make_uint4(h[0], h[1], h[2], h[3]);
+    }
+    // X = B hi + a lo, up to 256 columns a product
+    products([&] {
+      const uint32_t x = smem_u32(s_x), b = smem_u32(s_a);
+      for (int c = 0; c < blocks; c += 4) {
+        const int w = min(blocks - c, 4);
+        for (int k = 0; k < 8; ++k)
+          mma::mma_f16<1>(tmem + 64 * c, sdesc_sw128(b + (k >> 2) * 16384 + (k & 3) * 32, 16, 1024),
+                          sdesc_sw128(x + c * 16384 + k * 2048, 16384, 1024),
+                          mma::idesc_f16_f32(128, 64 * w, false, true), k > 0);
+      }
+    });
+    if (!ok) break;
+    const bool last = step + 1 == a.steps;
+    const float fl = ca * kLoDown, up = a.scale * kDown;
+    for (int c = half; c < blocks; c += 2) {
+      load64(trow + 64 * c, v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const uint2 r = *reinterpret_cast<const uint2*>(s_lo + c * 8192 + (j * 128 + row) * 8);
+        const uint32_t w[4] = {r.x, r.x >> 16, r.y, r.y >> 16};
+        float x[8];
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+          const float2 lo = lo_values(w[p]);
+          x[2 * p] = fmaf(v[8 * j + 2 * p], kDown, fl * lo.x);
+          x[2 * p + 1] = fmaf(v[8 * j + 2 * p + 1], kDown, fl * lo.y);
+        }
+        if (!last) {
+          put_x(s_x + c * 16384, s_lo + c * 8192, row, j, x);
+        } else if (a.tall) {
+#pragma unroll
+          for (int p = 0; p < 8; ++p)
+            if (row < a.n && c * 64 + 8 * j + p < a.m)
+              a.out[base + source(row, c * 64 + 8 * j + p)] = __float2bfloat16_rn(x[p] * up);
+        } else {
+          *swizzled(s_x + c * 16384, row, j) =
+              make_uint4(pack_bf16x2(x[0] * up, x[1] * up), pack_bf16x2(x[2] * up, x[3] * up),
+                         pack_bf16x2(x[4] * up, x[5] * up), pack_bf16x2(x[6] * up, x[7] * up));
+        }
+      }
+    }
+  }
+  if (ok && !a.tall) {
+    // the update along its rows
+    __syncthreads();
+    const bool wide = (a.cols & 7) == 0 && aligned16(a.out + base);
+    for (int i = tid; i < items; i += kSmallThreads) {
+      int r, j0;
+      place(i, r, j0);
+      const int c = j0 * 8;
+      if (r >= a.n || c >= a.m) continue;
+      const uint4 w = *swizzled(s_x + (j0 >> 3) * 16384, r, j0 & 7);
+      __nv_bfloat16* o = a.out + base + source(r, c);
+      if (wide) {
+        *reinterpret_cast<uint4*>(o) = w;
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const uint32_t p = word_of(w, j / 2) >> (j % 2 * 16);
+          if (c + j < a.m) reinterpret_cast<uint16_t*>(o)[j] = static_cast<uint16_t>(p);
+        }
+      }
+    }
+  }
+  if (!ok && tid == 0) report(a.status, kStTimeout, kWhereMuon + 12, static_cast<int>(l));
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(cols) : "memory");
+  }
+}
+
+template <typename G, typename M, bool kMom>
+cudaError_t run_small(const MuonArgs& args, cudaStream_t s) {
+  const cudaError_t e = allow_smem<muon_small_kernel<G, M, kMom>>(small_bytes(kSmallCols));
+  if (e != cudaSuccess) return e;
+  MuonArgs a = args;
+  memcpy(a.small_coeffs, args.coeffs, sizeof(float) * 3 * static_cast<size_t>(a.steps));
+  muon_small_kernel<G, M, kMom><<<static_cast<unsigned>(a.L), kSmallThreads, small_bytes(a.m), s>>>(a);
+  return cudaGetLastError();
+}
+template <typename G>
+cudaError_t run_small(const MuonArgs& a, cudaStream_t s) {
+  return !a.mom ? run_small<G, float, false>(a, s)
+         : a.mom_bf16 ? run_small<G, __nv_bfloat16, true>(a, s) : run_small<G, float, true>(a, s);
+}
+
 // ------------------------------------------------------------------ the steps
 
 bool map_of(MapEncoder enc, CUtensorMap* m, CUtensorMapDataType type, const void* base, int rank,
@@ -1032,6 +1335,7 @@ MuonPlan muon_plan(long long L, long long rows, long long cols) {
 }
 
 cudaError_t launch_muon(const MuonArgs& a, int grad_bf16, MapEncoder enc, int num_sms, cudaStream_t s) {
+  if (a.n <= kSmallRows && a.m <= kSmallCols) return grad_bf16 ? run_small<__nv_bfloat16>(a, s) : run_small<float>(a, s);
   const cudaError_t e = grad_bf16 ? prepare<__nv_bfloat16>(a, num_sms, s) : prepare<float>(a, num_sms, s);
   if (e != cudaSuccess) return e;
   // 128 x 128 tiles where each SM gets one of X's at most, so that a product takes as

@@ -167,6 +167,7 @@ struct MuonArgs {
   int nesterov;
   float eps, scale;
   const float* coeffs;    // host, [steps][3]
+  float small_coeffs[3 * kMuonSteps];   // the same, for the kernel of small matrices
   int steps;
   __nv_bfloat16* out;     // [L][rows][cols]
   double* partial;

@@ -47,7 +47,8 @@ def check_all(got, grads, coeffs=(ABC,) * 5, eps=1e-7, scale=1.0, fro=FRO):
 
 # a single value, rows, columns, tiles of 128 with odd ends, both ways round
 SHAPES = [(1, 1), (1, 7), (9, 1), (5, 3), (3, 5), (64, 64), (33, 200), (200, 33), (128, 128), (129, 257),
-          (257, 129), (128, 1000), (700, 300), (777, 1003), (1003, 777)]
+          (257, 129), (128, 1000), (700, 300), (777, 1003), (1003, 777), (100, 512), (513, 128), (128, 449),
+          (384, 127)]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
@@ -157,7 +158,7 @@ def test_tensors_off_their_vectors(n, m):
 
 def test_writes_stay_inside_their_buffers():
     from test_gpu_9_guard import Guarded
-    for L, n, m in ((1, 777, 203), (3, 70, 130), (16, 520, 1100), (20, 700, 513)):
+    for L, n, m in ((1, 777, 203), (3, 70, 130), (2, 500, 99), (16, 520, 1100), (20, 700, 513)):
         gd = Guarded(torch.device("cuda", 0))
         g, buf = gd.view((L, n, m), torch.float32), gd.view((L, n, m), torch.bfloat16)
         g.copy_(gradient(L, n, m, "fp32", 1))
