@@ -131,7 +131,12 @@ __device__ __forceinline__ Stats join(const Stats& a, const Stats& b, float c) {
 }
 
 __device__ __forceinline__ void add_value(Stats& st, float x, float c) {
-  const Stats one = {x, x == -INFINITY ? 0.f : x == INFINITY ? NAN : 1.f, 0.f};
+  Stats one = {x, 0.f, 0.f};
+  if (x != -INFINITY) {
+    const float y = exponent(x, x, c);       // what fp32(c x) leaves out; NaN for +inf
+    one.s = ex2_approx(y);
+    one.u = one.s * y;
+  }
   st = join(st, one, c);
 }
 
@@ -347,15 +352,16 @@ __device__ void k_largest(const Slice<T>& sl, const Maxima<NT>& mx, int nt, int 
   // the columns instead.
   int above = 0, equal = 0, hits = 0, at_t = 0;
   for (int b = 0; b < nt && t; b += 32) at_t += __popc(__ballot_sync(kAll, mx.best[b + lane] == t));
-  const uint32_t from = at_t <= kTieThreads ? t : t + 1;
+  const bool few = at_t <= kTieThreads;
   for (int b = 0; b < nt && t; b += 32) {
-    const bool hit = mx.best[b + lane] >= from;
+    const uint32_t best = mx.best[b + lane];
+    const bool hit = best > t || (few && best == t);
     const unsigned who = __ballot_sync(kAll, hit);
     if (hit) sc.hit[hits + __popc(who & below)] = static_cast<uint16_t>(b + lane);
     hits += __popc(who);
   }
   __syncwarp();
-  const float per = 1.f / pieces;            // below 2^13 pieces: exact after the floor
+  const float per = 1.f / pieces;            // at most 2^10 of them: exact after the floor
   for (int u0 = 0; u0 < hits * pieces; u0 += 32) {
     const int u = u0 + lane, i = static_cast<int>((u + 0.5f) * per), p = u - i * pieces;
     const int who = u < hits * pieces ? sc.hit[i] : 0;
@@ -370,7 +376,7 @@ __device__ void k_largest(const Slice<T>& sl, const Maxima<NT>& mx, int nt, int 
     equal += __popc(eq);
   }
   __syncwarp();
-  const bool take_ties = t && from == t && equal <= kTiePieces;
+  const bool take_ties = t && few && equal <= kTiePieces;
   const int todo = above + (take_ties ? equal : 0);
 
   // values above `floor` wait in sc.cand; where it fills up, the k largest of them stay
@@ -424,7 +430,6 @@ __device__ void k_largest(const Slice<T>& sl, const Maxima<NT>& mx, int nt, int 
   };
   // vectors of the pieces, or, t = 0, all of them: four a lane on their way
   const int each = span * kGroup, units = t ? todo * each : sl.v1 - sl.v0, log_nt = 31 - __clz(nt);
-  const float part = 1.f / each;             // u below 2^15: exact after the floor
   for (int u0 = 0; u0 < units; u0 += 4 * 32) {
     uint4 r[4];
     int v[4];
@@ -434,7 +439,7 @@ __device__ void k_largest(const Slice<T>& sl, const Maxima<NT>& mx, int nt, int 
       v[q] = sl.v1;
       if (u < units) {
         if (t) {
-          const int i = static_cast<int>((u + 0.5f) * part);
+          const int i = static_cast<int>(static_cast<unsigned>(u) / static_cast<unsigned>(each));
           const int id = sc.read[i < above ? i : kMaxTop * kPieces + i - above], p = id >> log_nt;
           v[q] = sl.v0 + ((p * each + u - i * each) << log_nt) + (id & (nt - 1));
         } else {
@@ -545,10 +550,13 @@ struct Pieces {
   }
 };
 
-// The log probability of a value; ls = log2 s.
+// The log probability of a value; ls = log2 s.  Where p is 1 to the last digits, ls may be
+// a rounding below y.
 __device__ __forceinline__ float log_prob(float x, const Stats& st, float ls, const ScoreFwdArgs& a) {
   const float y = exponent(x, st.m, a.c);
-  return isinf(y) ? fmaf(x - st.m, a.scale, -kLn2 * ls) : kLn2 * (y - ls);   // c x may leave fp32 where scale x does not
+  const float lp = isinf(y) ? fmaf(x - st.m, a.scale, -kLn2 * ls)   // c x may leave fp32 where scale x does not
+                            : kLn2 * (y - ls);
+  return lp > 0.f ? 0.f : lp;
 }
 
 // A row's outputs from its statistics and its k largest, by one warp.
@@ -572,7 +580,8 @@ __device__ __forceinline__ void write_row(const ScoreFwdArgs& a, long long row, 
   if (tid == 0) {
     const float cm = __fmul_rn(st.m, a.c);
     a.lse[row] = fabsf(cm) < INFINITY ? kLn2 * (cm + ls) : fmaf(kLn2, ls, st.m * a.scale);
-    a.entropy[row] = kLn2 * (ls - st.u / st.s);
+    const float h = kLn2 * (ls - st.u / st.s);
+    a.entropy[row] = h < 0.f ? 0.f : h;
   }
 }
 

@@ -166,11 +166,42 @@ def test_not_finite(N, dtype):
         base[4, 1], base[4, 2] = nan, inf
         base[5, ::2] = nan
         base[6, 1:] = -inf
+        base[7] = nan                            # more NaN than a list of ties takes
         for i in range(8):
             x = base[i:i + 1].repeat(N, 1).contiguous()
             tokens = torch.tensor([[0, 3, V - 1]], dtype=torch.int32, device="cuda").repeat(N, 1)
             got = eas.token_logprobs_fwd(x, tokens, 6)
             check_fwd(x[:1], tokens[:1], 6, 1.0, None, [t[:1] for t in got])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_many_rows_of_many_kinds(dtype):
+    """Rows that take the careful paths among ordinary ones, in the kernel that takes rows
+    in turn: each finds the shared memory as the one before left it."""
+    V = 30001
+    odd = rows_with_ties(V, dtype)
+    odd = torch.cat([odd, torch.full((1, V), math.nan, dtype=odd.dtype), torch.full((1, V), -math.inf, dtype=odd.dtype)])
+    odd[0, 5] = math.inf
+    x = make(700, V, dtype, 8)
+    at = torch.arange(0, 700, 9)[:3 * odd.shape[0]]
+    x[at] = odd.repeat(3, 1)[:at.numel()].cuda()
+    mask = torch.ones(700, dtype=torch.uint8, device="cuda")
+    mask[1::3] = 0
+    tokens = make_tokens(700, V, 2)
+    for k in (3, 64):
+        got = eas.token_logprobs_fwd(x, tokens, k, mask=mask)
+        pick = torch.cat([at[:2 * odd.shape[0]], torch.arange(1, 700, 40)])
+        check_fwd(x[pick], tokens[pick], k, 1.0, mask[pick], [t[pick] for t in got])
+
+
+@pytest.mark.parametrize("scale", [2.0 ** -30, 1e-3, 1e3, 2.0 ** 20])
+def test_scales(scale):
+    for N in (2, 330):
+        x = make(N, 30000, "fp32", 3)
+        x[0, 7] = -math.inf
+        tokens = make_tokens(N, 30000, 2)
+        got = eas.token_logprobs_fwd(x, tokens, 9, scale)
+        check_fwd(x[:9], tokens[:9], 9, scale, None, [t[:9] for t in got])
 
 
 def test_inactive_rows_are_not_read():
