@@ -9,9 +9,11 @@ operator around its one dense layer from this package:
 
 and back: lmhead_bwd -> rmsnorm_bwd -> the layer -> embed_bwd, which adds its
 sums to the LM head's gradient of E, then clip_grad_norm over all gradients and
-a plain SGD update.  Run it on a GPU:
+a plain SGD update, or with --muon the orthogonalised one of the dense layer.  At the
+end the model's own alternatives at the first active tokens, from logits that exist
+(token_logprobs_fwd).  Run it on a GPU:
 
-    python examples/tied_step.py [--fp8] [--steps N]
+    python examples/tied_step.py [--fp8] [--muon] [--steps N]
 """
 from __future__ import annotations
 
@@ -92,25 +94,46 @@ def gradients(m: Model, batch: dict, beta: float = 0.01, fp8: bool = False):
     return loss, {"table": dtable, "layer": dlayer.contiguous(), "gain": dgain}
 
 
-def step(m: Model, batch: dict, lr: float = 0.05, max_norm: float = 1.0, fp8: bool = False):
-    """One update; returns (loss, gradient norm before clipping) on the device."""
+def step(m: Model, batch: dict, lr: float = 0.05, max_norm: float = 1.0, fp8: bool = False,
+         momentum: torch.Tensor | None = None):
+    """One update; returns (loss, gradient norm before clipping) on the device.
+    momentum: [H, H] fp32, kept by the caller; with it the dense layer's update is
+    Muon's, of the size that a layer of its shape takes."""
     loss, grads = gradients(m, batch, fp8=fp8)
     clipped = {k: torch.empty_like(getattr(m, k)) for k in grads}     # in the weights' type
     norm = eas.clip_grad_norm(list(grads.values()), max_norm, out=list(clipped.values()))
+    if momentum is not None:
+        clipped["layer"] = eas.muon_update(clipped["layer"], momentum,
+                                           scale=0.2 * math.sqrt(max(m.layer.shape)))
     for k, g in clipped.items():
         getattr(m, k).sub_(g, alpha=lr)
     return loss, norm
 
 
+def alternatives(m: Model, batch: dict, k: int):
+    """(log probabilities [T, k], token ids [T, k]) of the k likeliest next tokens at the
+    active positions, as a sampler reports them: from the logits themselves."""
+    x = eas.embed_fwd(batch["ids"], m.table, m.scale)
+    y, _, _, _ = eas.rmsnorm_fwd(torch.tanh(x @ m.layer), m.gain, EPS, residual=x, mask=batch["mask"],
+                                 want_sum=False)
+    _, _, _, top, ids = eas.token_logprobs_fwd(y @ m.table.t(), None, k, mask=batch["mask"])
+    return top, ids
+
+
 def main() -> None:
     ap = argparse.ArgumentParser(description=__doc__.split("\n")[0])
     ap.add_argument("--fp8", action="store_true", help="e4m3 logits")
+    ap.add_argument("--muon", action="store_true", help="orthogonalised update of the dense layer")
     ap.add_argument("--steps", type=int, default=10)
     a = ap.parse_args()
     m, batch = make_model(4096, 512), make_batch(2048, 4096)
+    momentum = torch.zeros(m.layer.shape, device="cuda") if a.muon else None
     for i in range(a.steps):
-        loss, norm = step(m, batch, fp8=a.fp8)
+        loss, norm = step(m, batch, fp8=a.fp8, momentum=momentum)
         print(f"step {i}: loss {float(loss):.3f}  gradient norm {float(norm):.3f}")
+    top, ids = alternatives(m, batch, 3)
+    for t in batch["mask"].nonzero()[:3, 0].tolist():
+        print(f"token {t}: " + "  ".join(f"{i} ({p:.2f})" for i, p in zip(ids[t].tolist(), top[t].tolist())))
 
 
 if __name__ == "__main__":
