@@ -18,6 +18,7 @@
 // A and A A are symmetric: only tiles on and above the diagonal are computed, and
 // stored twice, the second time transposed.  A step takes 3 n^2 m + n^3 operations.
 #include <cstring>
+#include <type_traits>
 
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -121,16 +122,17 @@ __device__ double chunk_squares(const MuonArgs& a, long long base, long long lo,
   return sum;
 }
 
-// Sum over the CTA, in thread 0.
+// Sum over the CTA of kN threads, in thread 0.
+template <int kN>
 __device__ double block_sum(double v) {
-  __shared__ double part[kPrepThreads / 32];
+  __shared__ double part[kN / 32];
 #pragma unroll
   for (int d = 16; d; d >>= 1) v += __shfl_down_sync(0xffffffffu, v, d);
   if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
   __syncthreads();
   if (threadIdx.x == 0) {
     v = 0.;
-    for (int w = 0; w < kPrepThreads / 32; ++w) v += part[w];
+    for (int w = 0; w < kN / 32; ++w) v += part[w];
   }
   return v;
 }
@@ -142,7 +144,7 @@ __global__ void __launch_bounds__(kPrepThreads) muon_norm_kernel(const MuonArgs 
   const long long lo = blockIdx.x * a.chunk, hi = lo + a.chunk < size ? lo + a.chunk : size;
   bool vec = (size & 7) == 0 && aligned16(a.grad);
   if constexpr (kMom) vec = vec && aligned16(a.mom);
-  const double sum = block_sum(vec ? chunk_squares<G, M, kMom, true>(a, base, lo, hi)
+  const double sum = block_sum<kPrepThreads>(vec ? chunk_squares<G, M, kMom, true>(a, base, lo, hi)
                                    : chunk_squares<G, M, kMom, false>(a, base, lo, hi));
   if (threadIdx.x == 0) {
     a.partial[blockIdx.y * gridDim.x + blockIdx.x] = sum;
@@ -194,7 +196,7 @@ __global__ void __launch_bounds__(kPrepThreads) muon_scale_kernel(const MuonArgs
   wait_for_launch_before();
   double s = 0.;
   for (int i = tid; i < a.chunks; i += kPrepThreads) s += a.partial[l * a.chunks + i];
-  s = block_sum(s);
+  s = block_sum<kPrepThreads>(s);
   if (tid == 0) factor = static_cast<float>(kUp / (sqrt(s) + a.eps));
   __syncthreads();
   const float f = factor;
@@ -906,7 +908,7 @@ __global__ void __launch_bounds__(kThreads, 1) muon_gemm_kernel(const __grid_con
 // lo a row-major array.  No product waits for memory: 12 x [128][128] in fp32 take 78 us
 // over the counters above.
 
-constexpr int kSmallRows = 128, kSmallCols = 512, kSmallThreads = 256;
+constexpr int kSmallRows = 128, kSmallCols = 512, kSmallThreads = 512;
 constexpr int small_bytes(int m) { return (m + 63) / 64 * (16384 + 8192) + 32768 + 1024 + 256; }
 
 // 16-byte block j of row r in a block of 64 columns.
@@ -958,35 +960,46 @@ __global__ void __launch_bounds__(kSmallThreads) muon_small_kernel(const __grid_
   const M* mom = static_cast<const M*>(a.mom) + base;
   M* new_mom = static_cast<M*>(a.new_mom) + base;
   const int size = a.rows * a.cols;
+  const bool flat = (size & 7) == 0 && aligned16(grad) && (!kMom || (aligned16(mom) && aligned16(new_mom)));
+  const int count = flat ? size / 8 : size;
   double sum = 0.;
-  for (int i0 = tid; i0 < size; i0 += 8 * kSmallThreads) {
-    float g[8], m[8];
+  auto add = [&](auto vec) {
+    constexpr int VEC = decltype(vec)::value, kItems = VEC == 8 ? 2 : 8;
+    for (int i0 = tid; i0 < count; i0 += kItems * kSmallThreads) {
+      float g[kItems][VEC] = {};
+      [[maybe_unused]] float m[kItems][VEC] = {};
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const int i = i0 + k * kSmallThreads;
-      g[k] = i < size ? to_f32(grad[i]) : 0.f;
-      m[k] = 0.f;
-      if constexpr (kMom) m[k] = i < size ? to_f32(mom[i]) : 0.f;
-    }
-    if constexpr (kMom) {
-      float u[8];
-      update_of<8>(a, g, m, u);
+      for (int k = 0; k < kItems; ++k) {
+        const int i = i0 + k * kSmallThreads;
+        if (i >= count) break;
+        read_values(grad + VEC * i, g[k]);
+        if constexpr (kMom) read_values(mom + VEC * i, m[k]);
+      }
 #pragma unroll
-      for (int k = 0; k < 8; ++k) g[k] = u[k];
+      for (int k = 0; k < kItems; ++k) {
+        if constexpr (kMom) {
+          float u[VEC];
+          update_of<VEC>(a, g[k], m[k], u);
+          sum += squares<VEC>(u);
+        } else {
+          sum += squares<VEC>(g[k]);
+        }
+      }
     }
-    sum += squares<8>(g);
-  }
-  sum = block_sum(sum);
+  };
+  if (flat) add(std::integral_constant<int, 8>());
+  else add(std::integral_constant<int, 1>());
+  sum = block_sum<kSmallThreads>(sum);
   if (tid == 0) *factor = static_cast<float>(kUp / (sqrt(sum) + a.eps));
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *slot;
   const float f = *factor;
-  // X, zeros around it: eight columns of a row at a time, four times that on their way;
+  // X, zeros around it: eight columns of a row at a time, two times that on their way;
   // lanes next to one another along the rows of what came
-  constexpr int kItems = 4;
-  const bool vec = !a.tall && (a.cols & 7) == 0 && aligned16(grad) && (!kMom || (aligned16(mom) && aligned16(new_mom)));
+  constexpr int kItems = 2;
+  const bool vec = !a.tall && flat && (a.cols & 7) == 0;
   auto place = [&](int i, int& r, int& j0) {
     if (a.tall) {
       r = i % kSmallRows;
@@ -1048,7 +1061,7 @@ __global__ void __launch_bounds__(kSmallThreads) muon_small_kernel(const __grid_
     }
   }
 
-  const int q = warp & 3, half = warp >> 2, row = q * 32 + lane;
+  const int q = warp & 3, quarter = warp >> 2, row = q * 32 + lane;
   const uint32_t trow = tmem + (static_cast<uint32_t>(q * 32) << 16);
   uint32_t phase = 0;
   bool ok = true;
@@ -1079,12 +1092,14 @@ __global__ void __launch_bounds__(kSmallThreads) muon_small_kernel(const __grid_
       }
     });
     if (!ok) break;
-    uint8_t* mine = s_a + half * 16384;              // this thread's 64 columns of A's row
-    float v[64];
-    load64(trow + half * 64, v);
+    // this thread's 32 columns of A's row: half of a row of a block
+    uint8_t* mine = s_a + (quarter >> 1) * 16384;
+    const int j_a = (quarter & 1) * 4;
+    float v[32];
+    tmem_ld32(trow + quarter * 32, v);
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      *swizzled(mine, row, j) = make_uint4(
+    for (int j = 0; j < 4; ++j)
+      *swizzled(mine, row, j_a + j) = make_uint4(
           hi_bits(v[8 * j] * kDown, v[8 * j + 1] * kDown), hi_bits(v[8 * j + 2] * kDown, v[8 * j + 3] * kDown),
           hi_bits(v[8 * j + 4] * kDown, v[8 * j + 5] * kDown), hi_bits(v[8 * j + 6] * kDown, v[8 * j + 7] * kDown));
     // B = a I + b A + c A A, in A's place
@@ -1096,21 +1111,21 @@ __global__ void __launch_bounds__(kSmallThreads) muon_small_kernel(const __grid_
       }
     });
     if (!ok) break;
-    load64(trow + half * 64, v);
+    tmem_ld32(trow + quarter * 32, v);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const uint4 r = *swizzled(mine, row, j);
+    for (int j = 0; j < 4; ++j) {
+      const uint4 r = *swizzled(mine, row, j_a + j);
       uint32_t h[4];
 #pragma unroll
       for (int p = 0; p < 4; ++p) {
         const float2 x = hi_values(word_of(r, p));
         const int c = 8 * j + 2 * p;
         float b0 = fmaf(v[c], cc * kDown, cb * x.x), b1 = fmaf(v[c + 1], cc * kDown, cb * x.y);
-        if (row == half * 64 + c) b0 += ca * kUp;
-        if (row == half * 64 + c + 1) b1 += ca * kUp;
+        if (row == quarter * 32 + c) b0 += ca * kUp;
+        if (row == quarter * 32 + c + 1) b1 += ca * kUp;
         h[p] = hi_bits(b0, b1);
       }
-      *swizzled(mine, row, j) = make_uint4(h[0], h[1], h[2], h[3]);
+      *swizzled(mine, row, j_a + j) = make_uint4(h[0], h[1], h[2], h[3]);
     }
     // X = B hi + a lo, up to 256 columns a product
     products([&] {
@@ -1126,18 +1141,20 @@ __global__ void __launch_bounds__(kSmallThreads) muon_small_kernel(const __grid_
     if (!ok) break;
     const bool last = step + 1 == a.steps;
     const float fl = ca * kLoDown, up = a.scale * kDown;
-    for (int c = half; c < blocks; c += 2) {
-      load64(trow + 64 * c, v);
+    for (int u = quarter; u < 2 * blocks; u += 4) {
+      tmem_ld32(trow + 32 * u, v);
+      const int c = u >> 1;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
+      for (int i = 0; i < 4; ++i) {
+        const int j = (u & 1) * 4 + i;
         const uint2 r = *reinterpret_cast<const uint2*>(s_lo + c * 8192 + (j * 128 + row) * 8);
         const uint32_t w[4] = {r.x, r.x >> 16, r.y, r.y >> 16};
         float x[8];
 #pragma unroll
         for (int p = 0; p < 4; ++p) {
           const float2 lo = lo_values(w[p]);
-          x[2 * p] = fmaf(v[8 * j + 2 * p], kDown, fl * lo.x);
-          x[2 * p + 1] = fmaf(v[8 * j + 2 * p + 1], kDown, fl * lo.y);
+          x[2 * p] = fmaf(v[8 * i + 2 * p], kDown, fl * lo.x);
+          x[2 * p + 1] = fmaf(v[8 * i + 2 * p + 1], kDown, fl * lo.y);
         }
         if (!last) {
           put_x(s_x + c * 16384, s_lo + c * 8192, row, j, x);
