@@ -42,16 +42,25 @@ constexpr int kPrepThreads = 256;
 constexpr int kChunk = 4096;      // elements a CTA at least
 constexpr int kMostChunks = 1024; // partial sums a matrix
 
-// Sum of squares in fp64, added up in fp32 over a vector where that is safe.
-template <int VEC>
-__device__ __forceinline__ double squares(const float (&u)[VEC]) {
+// Whether a sum of squares is as good in fp32 as its roundings: it has not come near the
+// ends of fp32's range.
+__device__ __forceinline__ bool in_range(float s) { return s > 1e-30f && s < 1e30f; }
+
+// Sum of squares in fp64, added up in fp32 over the values of a call where that is safe
+// (an fp64 operation costs 32 of fp32).
+template <int K, int VEC>
+__device__ __forceinline__ double squares(const float (&u)[K][VEC]) {
   float s = 0.f;
 #pragma unroll
-  for (int j = 0; j < VEC; ++j) s = fmaf(u[j], u[j], s);
-  if (s > 1e-30f && s < 1e30f) return s;
+  for (int k = 0; k < K; ++k)
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) s = fmaf(u[k][j], u[k][j], s);
+  if (in_range(s)) return s;
   double d = 0.;
 #pragma unroll
-  for (int j = 0; j < VEC; ++j) d += static_cast<double>(u[j]) * u[j];
+  for (int k = 0; k < K; ++k)
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) d += static_cast<double>(u[k][j]) * u[k][j];
   return d;
 }
 
@@ -90,6 +99,18 @@ __device__ __forceinline__ void update_of(const MuonArgs& a, const float (&g)[VE
   }
 }
 
+// The updates of groups of values, in place of the gradients.
+template <int K, int VEC>
+__device__ __forceinline__ void updates_of(const MuonArgs& a, float (&g)[K][VEC], float (&m)[K][VEC]) {
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    float u[VEC];
+    update_of<VEC>(a, g[k], m[k], u);
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) g[k][j] = u[j];
+  }
+}
+
 // Sum of squares of a chunk of a matrix's update.  A thread has kItems vectors (kVec) or
 // single values on their way at a time.
 template <typename G, typename M, bool kMom, bool kVec>
@@ -99,7 +120,8 @@ __device__ double chunk_squares(const MuonArgs& a, long long base, long long lo,
   const M* mom = static_cast<const M*>(a.mom) + base;
   double sum = 0.;
   for (long long i0 = lo + static_cast<long long>(threadIdx.x) * VEC; i0 < hi; i0 += kItems * kPrepThreads * VEC) {
-    float g[kItems][VEC], m[kItems][VEC];
+    float g[kItems][VEC] = {};
+    [[maybe_unused]] float m[kItems][VEC] = {};
 #pragma unroll
     for (int k = 0; k < kItems; ++k) {
       const long long i = i0 + k * kPrepThreads * VEC;
@@ -107,17 +129,8 @@ __device__ double chunk_squares(const MuonArgs& a, long long base, long long lo,
       read_values(grad + i, g[k]);
       if constexpr (kMom) read_values(mom + i, m[k]);
     }
-#pragma unroll
-    for (int k = 0; k < kItems; ++k) {
-      if (i0 + k * kPrepThreads * VEC >= hi) break;
-      if constexpr (kMom) {
-        float u[VEC];
-        update_of<VEC>(a, g[k], m[k], u);
-        sum += squares<VEC>(u);
-      } else {
-        sum += squares<VEC>(g[k]);
-      }
-    }
+    if constexpr (kMom) updates_of(a, g, m);
+    sum += squares(g);
   }
   return sum;
 }
@@ -126,8 +139,15 @@ __device__ double chunk_squares(const MuonArgs& a, long long base, long long lo,
 template <int kN>
 __device__ double block_sum(double v) {
   __shared__ double part[kN / 32];
+  float f = static_cast<float>(v);
+  if (__all_sync(0xffffffffu, v == 0. || in_range(f))) {      // squares: their sum stays below 32 * 1e30
 #pragma unroll
-  for (int d = 16; d; d >>= 1) v += __shfl_down_sync(0xffffffffu, v, d);
+    for (int d = 16; d; d >>= 1) f += __shfl_down_sync(0xffffffffu, f, d);
+    v = f;
+  } else {
+#pragma unroll
+    for (int d = 16; d; d >>= 1) v += __shfl_down_sync(0xffffffffu, v, d);
+  }
   if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
   __syncthreads();
   if (threadIdx.x == 0) {
@@ -182,6 +202,13 @@ __device__ __forceinline__ void write_pair(const MuonPair& x, long long o, const
   *reinterpret_cast<uint2*>(x.lo + o) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
 }
 
+// 2^12 / (norm + eps) from the sum of squares.
+__device__ __forceinline__ float factor_of(double sum, float eps) {
+  const float s = static_cast<float>(sum);
+  if (in_range(s)) return kUp / (sqrtf(s) + eps);
+  return static_cast<float>(kUp / (sqrt(sum) + eps));
+}
+
 // The new momentum, and X's first pair: the update times 2^12 / (norm + eps), transposed
 // where it is taller than wide.  grid (CTAs, L); a CTA takes 64 x 64 tiles of X in turn.
 template <typename G, typename M, bool kMom, bool kTall>
@@ -197,7 +224,7 @@ __global__ void __launch_bounds__(kPrepThreads) muon_scale_kernel(const MuonArgs
   double s = 0.;
   for (int i = tid; i < a.chunks; i += kPrepThreads) s += a.partial[l * a.chunks + i];
   s = block_sum<kPrepThreads>(s);
-  if (tid == 0) factor = static_cast<float>(kUp / (sqrt(s) + a.eps));
+  if (tid == 0) factor = factor_of(s, a.eps);
   __syncthreads();
   const float f = factor;
   const int across = (a.m + 63) / 64, tiles = across * ((a.n + 63) / 64);
@@ -975,22 +1002,14 @@ __global__ void __launch_bounds__(kSmallThreads) muon_small_kernel(const __grid_
         read_values(grad + VEC * i, g[k]);
         if constexpr (kMom) read_values(mom + VEC * i, m[k]);
       }
-#pragma unroll
-      for (int k = 0; k < kItems; ++k) {
-        if constexpr (kMom) {
-          float u[VEC];
-          update_of<VEC>(a, g[k], m[k], u);
-          sum += squares<VEC>(u);
-        } else {
-          sum += squares<VEC>(g[k]);
-        }
-      }
+      if constexpr (kMom) updates_of(a, g, m);
+      sum += squares(g);
     }
   };
   if (flat) add(std::integral_constant<int, 8>());
   else add(std::integral_constant<int, 1>());
   sum = block_sum<kSmallThreads>(sum);
-  if (tid == 0) *factor = static_cast<float>(kUp / (sqrt(sum) + a.eps));
+  if (tid == 0) *factor = factor_of(sum, a.eps);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();

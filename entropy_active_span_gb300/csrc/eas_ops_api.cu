@@ -116,7 +116,8 @@ eas_status eas_rmsnorm_fwd(const void* x, const void* residual, const void* weig
                            void* sum_out, void* y, uint8_t* y_e4m3, float* y_scale, void* stream) {
   eas_status st = check_rows(R, H, dtype);
   if (st != EAS_OK) return st;
-  if (!(eps > 0.f) || !std::isfinite(eps)) return fail(EAS_ERR_INVALID_ARG, "eps must be positive");
+  // below, the factor of a matrix of that norm would leave fp32
+  if (!(eps >= 1e-30f) || !std::isfinite(eps)) return fail(EAS_ERR_INVALID_ARG, "eps must be 1e-30 or more");
   if (!weight || (R > 0 && !x)) return fail(EAS_ERR_INVALID_ARG, "null pointer");
   if ((y_e4m3 == nullptr) != (y_scale == nullptr))
     return fail(EAS_ERR_INVALID_ARG, "y_e4m3 and y_scale come together");
@@ -151,7 +152,8 @@ eas_status eas_rmsnorm_bwd(const void* dy, const void* sum, const void* weight, 
                            void* dx, float* dweight, void* ws, size_t ws_bytes, void* stream) {
   eas_status st = check_rows(R, H, dtype);
   if (st != EAS_OK) return st;
-  if (!(eps > 0.f) || !std::isfinite(eps)) return fail(EAS_ERR_INVALID_ARG, "eps must be positive");
+  // below, the factor of a matrix of that norm would leave fp32
+  if (!(eps >= 1e-30f) || !std::isfinite(eps)) return fail(EAS_ERR_INVALID_ARG, "eps must be 1e-30 or more");
   if (!weight || !dweight || !ws || (R > 0 && (!dy || !sum || !dx)))
     return fail(EAS_ERR_INVALID_ARG, "null pointer");
   if (!aligned(dy, 16) || !aligned(sum, 16) || !aligned(weight, 16) || !aligned(ds, 16) ||
@@ -410,7 +412,8 @@ eas_status eas_orthogonalize(const void* grad, eas_dtype grad_dtype, const void*
   if (!coeffs || !ws || (L > 0 && (!grad || !out))) return fail(EAS_ERR_INVALID_ARG, "null pointer");
   for (int i = 0; i < 3 * steps; ++i)
     if (!std::isfinite(coeffs[i])) return fail(EAS_ERR_INVALID_ARG, "coefficients must be finite");
-  if (!(eps > 0.f) || !std::isfinite(eps)) return fail(EAS_ERR_INVALID_ARG, "eps must be positive");
+  // below, the factor of a matrix of that norm would leave fp32
+  if (!(eps >= 1e-30f) || !std::isfinite(eps)) return fail(EAS_ERR_INVALID_ARG, "eps must be 1e-30 or more");
   if (!std::isfinite(scale)) return fail(EAS_ERR_INVALID_ARG, "scale must be finite");
   const size_t ge = elem_size(grad_dtype), me = momentum ? elem_size(momentum_dtype) : 4;
   if (!aligned(grad, ge) || !aligned(momentum, me) || !aligned(new_momentum, me) || !aligned(out, 2) || !aligned(ws, 256))

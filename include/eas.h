@@ -545,7 +545,7 @@ eas_status eas_token_logprobs_bwd(const float* g_logprob, const float* g_entropy
  *   beta     in [0, 1]; nesterov 0 or 1
  *   coeffs   HOST array [steps][3], copied before the call returns;
  *            1 <= steps <= EAS_MAX_MUON_STEPS
- *   eps      > 0 (a zero matrix gives zeros)
+ *   eps      >= 1e-30 (a zero matrix gives zeros)
  *   out      [L][rows][cols] bf16
  *   ws       eas_orthogonalize_workspace_size(L, rows, cols) bytes, about
  *            6 + 4 n / m bytes an element for n <= m; holds the status word

@@ -37,6 +37,12 @@ def test_refuses(libeas, bad):
     assert call(libeas, **bad) == INVALID
 
 
+@pytest.mark.parametrize("eps", [1e-38, 9e-31])
+def test_refuses_an_eps_whose_factor_leaves_fp32(libeas, eps):
+    assert call(libeas, eps=eps) == INVALID
+    assert b"eps" in libeas.eas_last_error()
+
+
 def test_workspace(libeas):
     size = libeas.eas_orthogonalize_workspace_size
     assert call(libeas, ws_bytes=size(L, R, C) - 1) == WORKSPACE
