@@ -319,8 +319,7 @@ __global__ void __launch_bounds__(kPrepThreads) muon_scale_kernel(const MuonArgs
 
 enum Kind { kGram, kPoly, kApply, kLast };
 
-constexpr int kStoreWarps = 8;
-constexpr int kThreads = 96 + 32 * kStoreWarps;
+constexpr int kStoreWarps = 8;                     // at most
 constexpr int kStages = 5;
 constexpr int kRing = 3;                           // tile numbers on their way to the warps
 constexpr int kOperand = 16384;                    // 128 rows (columns) x 64 k
@@ -330,18 +329,22 @@ constexpr int kDrawAhead = 6;                      // k-blocks before a tile's e
 constexpr int kBand = 4;                           // rows of tiles of X that are computed together
 
 // CG = 2: a pair of CTAs computes 256 x 256 tiles, each 128 of the rows; CG = 1: a CTA
-// 128 x 128 tiles.
-template <int CG>
+// 128 x 128 tiles, or (kHalves = 2) each half of their columns on its own.
+template <int CG, int kHalves>
 struct Geo {
-  static constexpr int kM = 128 * CG, kN = 128 * CG;
+  static constexpr int kM = 128 * CG, kTile = 128 * CG;
+  static constexpr int kN = kTile / kHalves;
+  static constexpr int kRowsB = 128 / kHalves;     // of the second operand that a CTA loads
   static constexpr uint32_t kCols = 2 * kN;        // two accumulators
   static constexpr int kChunk = 2 * CG;            // k-blocks of 64 in a tile's width
-  static constexpr int kDone = kStoreWarps * CG;   // arrivals that finish a tile
+  static constexpr int kStore = kStoreWarps / kHalves;
+  static constexpr int kThreads = 96 + 32 * kStore;
+  static constexpr int kDone = kStoreWarps * CG;   // arrivals that finish a tile, its halves together
 };
 
 struct GemmArgs {
-  CUtensorMap xk[2], xn[2], xh[2], xl[2];   // X's pairs: rows as operand, columns as operand, stores
-  CUtensorMap ak, as, at, bk, bs, bt;       // A and B: operand, store, transposed store
+  CUtensorMap xk[2], xs[2], xn[2], xh[2], xl[2];   // X's pairs: rows as first and second operand, columns as operand, stores
+  CUtensorMap ak, a2, as, at, bk, bs, bt;   // A and B: first and second operand, store, transposed store
   int n, m, L, steps;
   int num_m, num_n;                         // tiles down and across X
   int tri, full;                            // tiles of A (or B), of X, a matrix
@@ -358,11 +361,14 @@ struct GemmArgs {
 };
 
 struct Tile {
-  int kind, step, l, m, n;
+  int kind, step, l, m, n, half;
 };
 
+template <int kHalves>
 __device__ __forceinline__ Tile tile_of(int t, const GemmArgs& a) {
   Tile w;
+  w.half = t % kHalves;
+  t /= kHalves;
   const int per_step = a.L * (2 * a.tri + a.full);
   w.step = t / per_step;
   t -= w.step * per_step;
@@ -409,7 +415,6 @@ __device__ __forceinline__ uint32_t operands_to(int it, int chunks) { return (st
 
 // Counter of the operand that a tile reads at chunk c of k: its first operand's
 // (which = 0) or its second one's.  null: none to wait for.
-template <int CG>
 __device__ __forceinline__ const int* operand_counter(const Tile& w, int c, int which, const GemmArgs& a) {
   const int row = which ? w.n : w.m;
   if (which && (w.kind >= kApply || w.m == w.n)) return nullptr;   // Apply: B's row waits for all of X
@@ -609,13 +614,13 @@ __device__ __forceinline__ bool epilogue(const GemmArgs& a, const Tile& w, uint3
 }
 
 // Warp 0 loads, warp 1 issues the MMAs, warps 2 to 9 store (two for each 32 rows, half of
-// the columns each), and the last warp draws the next tile and watches its operands'
+// the columns each; 2 to 5 of a half tile), and the last warp draws the next tile and watches its operands'
 // counters while this one's are loaded (the loads are what bounds a tile: 32 KB of
 // operands for 512 clocks of MMA); two accumulators, so that a tile's stores run under the next
 // one's products.
-template <int CG>
-__global__ void __launch_bounds__(kThreads, 1) muon_gemm_kernel(const __grid_constant__ GemmArgs a) {
-  using G = Geo<CG>;
+template <int CG, int kHalves>
+__global__ void __launch_bounds__(Geo<CG, kHalves>::kThreads, 1) muon_gemm_kernel(const __grid_constant__ GemmArgs a) {
+  using G = Geo<CG, kHalves>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -647,15 +652,15 @@ __global__ void __launch_bounds__(kThreads, 1) muon_gemm_kernel(const __grid_con
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&tfull[i], 1);
-      mbar_init(&tempty[i], kStoreWarps * CG);
+      mbar_init(&tempty[i], G::kStore * CG);
     }
     for (int i = 0; i < kRing; ++i) {
       mbar_init(&rfull[i], 1);
-      mbar_init(&rempty[i], (2 + kStoreWarps) * CG);   // loader, MMA warp (CTA 1: drawer), storing warps
+      mbar_init(&rempty[i], (2 + G::kStore) * CG);   // loader, MMA warp (CTA 1: drawer), storing warps
       mbar_init(&there[i], 1);
       progress[i] = 0;
     }
-    for (int i = 0; i < kStoreWarps; ++i) mbar_init(&fetched[i], 1);
+    for (int i = 0; i < G::kStore; ++i) mbar_init(&fetched[i], 1);
     mbar_init(near_end, 1);
     mbar_init(drain, 1);
     *abort_flag = 0;
@@ -667,7 +672,7 @@ __global__ void __launch_bounds__(kThreads, 1) muon_gemm_kernel(const __grid_con
   mma::sync_pair<CG>();
   tc_fence_after();
   const uint32_t tmem = *slot_addr;
-  const int total = a.steps * a.L * (2 * a.tri + a.full);
+  const int total = a.steps * a.L * (2 * a.tri + a.full) * kHalves;
   const uint32_t rempty0 = mma::leader_addr<CG>(&rempty[0]);
 
   if (warp == 0) {
@@ -685,12 +690,12 @@ __global__ void __launch_bounds__(kThreads, 1) muon_gemm_kernel(const __grid_con
         const int t = ring[slot];
         mma::arrive_at(rempty0 + 8 * slot);
         if (t < 0) break;
-        const Tile w = tile_of(t, a);
+        const Tile w = tile_of<kHalves>(t, a);
         const int from = w.step & 1;
         const CUtensorMap* ma = w.kind == kGram ? &a.xk[from] : w.kind == kPoly ? &a.ak : &a.bk;
-        const CUtensorMap* mb = w.kind == kGram ? &a.xk[from] : w.kind == kPoly ? &a.ak : &a.xn[from];
+        const CUtensorMap* mb = w.kind == kGram ? &a.xs[from] : w.kind == kPoly ? &a.a2 : &a.xn[from];
         const int mrow = w.m * G::kM + static_cast<int>(rank) * 128;
-        const int ncol = w.n * G::kN + static_cast<int>(rank) * 128;
+        const int ncol = w.n * G::kTile + w.half * G::kN + static_cast<int>(rank) * 128;
         const int num_kb = ((w.kind == kGram ? a.m : a.n) + 63) / 64;
         int known = 0;                       // k-blocks whose operands are there
         for (int kb = 0; kb < num_kb; ++kb) {
@@ -722,7 +727,7 @@ __global__ void __launch_bounds__(kThreads, 1) muon_gemm_kernel(const __grid_con
           // begin with
           if (leader && kb == max(num_kb - kDrawAhead, 0)) mbar_arrive(near_end);
           const uint32_t bar = full0 + 8 * stage;
-          if (leader) mbar_arrive_expect_tx(&full[stage], CG * 2 * kOperand);
+          if (leader) mbar_arrive_expect_tx(&full[stage], CG * 128 * (128 + G::kRowsB));
           mma::load_3d<CG>(s_a + stage * kOperand, ma, bar, kb * 64, mrow, w.l);
           if (w.kind <= kPoly) mma::load_3d<CG>(s_b + stage * kOperand, mb, bar, kb * 64, ncol, w.l);
           else mma::load_4d<CG>(s_b + stage * kOperand, mb, bar, 0, kb * 64, ncol >> 6, w.l);
@@ -742,7 +747,7 @@ __global__ void __launch_bounds__(kThreads, 1) muon_gemm_kernel(const __grid_con
         }
       }
     }
-  } else if (warp == kThreads / 32 - 1) {
+  } else if (warp == G::kThreads / 32 - 1) {
     bool ok = true;
     for (int it = 0; ok; ++it) {
       const int slot = it % kRing;
@@ -771,14 +776,14 @@ __global__ void __launch_bounds__(kThreads, 1) muon_gemm_kernel(const __grid_con
       ok = __shfl_sync(0xffffffffu, ok, 0);
       t = __shfl_sync(0xffffffffu, t, 0);
       if (!ok || t < 0) break;
-      const Tile w = tile_of(t, a);
+      const Tile w = tile_of<kHalves>(t, a);
       const int num_kb = ((w.kind == kGram ? a.m : a.n) + 63) / 64;
       const int chunks = (num_kb + G::kChunk - 1) / G::kChunk;
       const int want = G::kDone * (w.kind == kGram ? w.step : w.step + 1);
       for (int c0 = 0; ok && c0 < chunks; c0 += 16) {
         // lanes 0 to 15 watch the first operand's counters, 16 to 31 the second one's
         const int mine = c0 + (lane & 15), most = min(chunks - c0, 16);
-        const int* at = mine < chunks ? operand_counter<CG>(w, mine, lane >> 4, a) : nullptr;
+        const int* at = mine < chunks ? operand_counter(w, mine, lane >> 4, a) : nullptr;
         bool ready = !at;
         int have = 0;                      // of these chunks, from the first on
         long long t0 = clock64();
@@ -818,7 +823,7 @@ __global__ void __launch_bounds__(kThreads, 1) muon_gemm_kernel(const __grid_con
         const int t = ring[slot];
         mbar_arrive(&rempty[slot]);
         if (t < 0) break;
-        const Tile w = tile_of(t, a);
+        const Tile w = tile_of<kHalves>(t, a);
         const bool k_rows = w.kind > kPoly;        // X's rows are k
         const int num_kb = ((w.kind == kGram ? a.m : a.n) + 63) / 64;
         const uint32_t idesc = k_rows ? mma::idesc_f16_f32(G::kM, G::kN, false, true)
@@ -858,7 +863,7 @@ __global__ void __launch_bounds__(kThreads, 1) muon_gemm_kernel(const __grid_con
     }
   } else {
     const int q = warp & 3, half = (warp - 2) >> 2;
-    constexpr int kCols = G::kN / 2;
+    constexpr int kCols = G::kN * 4 / G::kStore;
     Boxes b = {s_epi + (warp - 2) * kEpiWarp, &fetched[warp - 2], 0};
     const uint32_t tempty0 = mma::leader_addr<CG>(&tempty[0]);
     for (int it = 0;; ++it) {
@@ -876,10 +881,10 @@ __global__ void __launch_bounds__(kThreads, 1) muon_gemm_kernel(const __grid_con
       __syncwarp();
       if (lane == 0) mma::arrive_at(rempty0 + 8 * slot);
       if (t < 0) break;
-      const Tile w = tile_of(t, a);
+      const Tile w = tile_of<kHalves>(t, a);
       const int buf = it & 1;
       const uint32_t tbase = tmem + (static_cast<uint32_t>(q * 32) << 16) + buf * G::kN + half * kCols;
-      const int row0 = w.m * G::kM + static_cast<int>(rank) * 128 + q * 32, n0 = w.n * G::kN + half * kCols;
+      const int row0 = w.m * G::kM + static_cast<int>(rank) * 128 + q * 32, n0 = w.n * G::kTile + w.half * G::kN + half * kCols;
       if (lane == 0 && row0 < a.n && n0 < (w.kind <= kPoly ? a.n : a.m)) {
         // the boxes are free: the tile before waited for its stores (and, Last, all
         // lanes are through with theirs)
@@ -1257,37 +1262,40 @@ bool map_3d(MapEncoder enc, CUtensorMap* m, const T* base, long long cols, long 
                 strides, box, swizzle);
 }
 
-// The same as blocks of 64 columns, two blocks x 64 rows a box: an operand whose rows
+// The same as blocks of 64 columns, `blocks` of them x 64 rows a box: an operand whose rows
 // are k.  Columns past `cols` in the last block come from the rows' padding; they
 // reach only results past the result's last column.
 bool map_k_rows(MapEncoder enc, CUtensorMap* m, const __half* base, long long cols, long long rows, long long L,
-                long long ld) {
+                long long ld, int blocks) {
   const cuuint64_t dims[4] = {64, static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>((cols + 63) / 64),
                               static_cast<cuuint64_t>(L)};
   const cuuint64_t strides[3] = {static_cast<cuuint64_t>(ld) * 2, 128, static_cast<cuuint64_t>(ld) * 2 * rows};
-  const cuuint32_t box[4] = {64, 64, 2, 1};
+  const cuuint32_t box[4] = {64, 64, static_cast<cuuint32_t>(blocks), 1};
   return map_of(enc, m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, base, 4, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-template <int CG>
+template <int CG, int kHalves>
 cudaError_t run_steps(const MuonArgs& a, MapEncoder enc, int num_sms, cudaStream_t s) {
+  using G = Geo<CG, kHalves>;
   GemmArgs g;
   memset(&g, 0, sizeof(g));
   bool ok = true;
   for (int i = 0; i < 2; ++i) {
     ok = ok && map_3d(enc, &g.xk[i], a.x[i].hi, a.m, a.n, a.L, a.ldx, 64, 128) &&
-         map_k_rows(enc, &g.xn[i], a.x[i].hi, a.m, a.n, a.L, a.ldx) &&
+         map_3d(enc, &g.xs[i], a.x[i].hi, a.m, a.n, a.L, a.ldx, 64, G::kRowsB) &&
+         map_k_rows(enc, &g.xn[i], a.x[i].hi, a.m, a.n, a.L, a.ldx, G::kRowsB / 64) &&
          map_3d(enc, &g.xh[i], a.x[i].hi, a.m, a.n, a.L, a.ldx, 64, 32) &&
          map_3d(enc, &g.xl[i], a.x[i].lo, a.m, a.n, a.L, a.ldx, 64, 32, CU_TENSOR_MAP_SWIZZLE_64B);
   }
   ok = ok && map_3d(enc, &g.ak, a.gram, a.n, a.n, a.L, a.lda, 64, 128) &&
+       map_3d(enc, &g.a2, a.gram, a.n, a.n, a.L, a.lda, 64, G::kRowsB) &&
        map_3d(enc, &g.as, a.gram, a.n, a.n, a.L, a.lda, 64, 32) &&
        map_3d(enc, &g.at, a.gram, a.n, a.n, a.L, a.lda, 32, 64, CU_TENSOR_MAP_SWIZZLE_NONE) &&
        map_3d(enc, &g.bk, a.poly, a.n, a.n, a.L, a.lda, 64, 128) &&
        map_3d(enc, &g.bs, a.poly, a.n, a.n, a.L, a.lda, 64, 32) &&
        map_3d(enc, &g.bt, a.poly, a.n, a.n, a.L, a.lda, 32, 64, CU_TENSOR_MAP_SWIZZLE_NONE);
   if (!ok) return cudaErrorInvalidValue;
-  constexpr int T = Geo<CG>::kM;
+  constexpr int T = G::kTile;
   g.n = a.n;
   g.m = a.m;
   g.L = a.L;
@@ -1306,12 +1314,12 @@ cudaError_t run_steps(const MuonArgs& a, MapEncoder enc, int num_sms, cudaStream
   g.done_x = g.done_b + static_cast<long long>(a.L) * g.num_m * g.num_m;
   g.status = a.status;
   g.budget = a.budget;
-  const auto kernel = muon_gemm_kernel<CG>;
-  cudaError_t e = allow_smem<muon_gemm_kernel<CG>>(kSmem);
+  const auto kernel = muon_gemm_kernel<CG, kHalves>;
+  cudaError_t e = allow_smem<muon_gemm_kernel<CG, kHalves>>(kSmem);
   if (e != cudaSuccess) return e;
   // a CTA an SM at most; CTAs wait for one another, so they are launched to run
   // together
-  const long long tiles = static_cast<long long>(g.tri + g.tri + g.full) * a.L * a.steps, most = num_sms / CG;
+  const long long tiles = static_cast<long long>(g.tri + g.tri + g.full) * a.L * a.steps * kHalves, most = num_sms / CG;
   cudaLaunchAttribute attr[2] = {};
   attr[0].id = cudaLaunchAttributeCooperative;
   attr[0].val.cooperative = 1;
@@ -1319,7 +1327,7 @@ cudaError_t run_steps(const MuonArgs& a, MapEncoder enc, int num_sms, cudaStream
   attr[1].val.clusterDim = {CG, 1, 1};
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(CG * (tiles < most ? tiles : most)));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(G::kThreads);
   cfg.dynamicSmemBytes = kSmem;
   cfg.stream = s;
   cfg.attrs = attr;
@@ -1374,11 +1382,15 @@ cudaError_t launch_muon(const MuonArgs& a, int grad_bf16, MapEncoder enc, int nu
   if (a.n <= kSmallRows && a.m <= kSmallCols) return grad_bf16 ? run_small<__nv_bfloat16>(a, s) : run_small<float>(a, s);
   const cudaError_t e = grad_bf16 ? prepare<__nv_bfloat16>(a, num_sms, s) : prepare<float>(a, num_sms, s);
   if (e != cudaSuccess) return e;
-  // 128 x 128 tiles where each SM gets one of X's at most, so that a product takes as
-  // little as its depth allows; else 256 x 256 tiles by pairs, which take in half the
-  // bytes an operation
+  // Products are deep (n or m) and few tiles wide where matrices are small, so the rule
+  // goes by X's tiles of 128 x 128: where each SM gets half of one at most, halves, which
+  // take in 24 KB a k-block instead of 32 ([1003][777] 130 us and 143, [320][320] 87 and
+  // 99); where it gets one, whole ones ([1088][1088] 155 us); else 256 x 256 tiles by
+  // pairs, which take in half the bytes an operation.
   const long long small = static_cast<long long>(a.L) * ((a.n + 127) / 128) * ((a.m + 127) / 128);
-  return small > num_sms ? run_steps<2>(a, enc, num_sms, s) : run_steps<1>(a, enc, num_sms, s);
+  return small > num_sms       ? run_steps<2, 1>(a, enc, num_sms, s)
+         : 2 * small > num_sms ? run_steps<1, 1>(a, enc, num_sms, s)
+                               : run_steps<1, 2>(a, enc, num_sms, s);
 }
 
 }  // namespace eas
