@@ -30,6 +30,7 @@ namespace {
 
 constexpr int kThreads = 512;     // at most
 constexpr int kCand = 512;        // values that wait to be ordered
+constexpr int kOrderAtOnce = 96;  // more are cut down first
 constexpr int kPieces = 8;        // of a thread's part
 constexpr int kTieThreads = 64;   // threads whose maximum is t, and
 constexpr int kTiePieces = 256;   // pieces whose maximum is t that are read again, at most
@@ -294,18 +295,17 @@ __device__ __forceinline__ void block_bits(const uint4& r, uint32_t (&b)[kVec16<
   for (int j = 0; j < kVec16<T>; ++j) b[j] = order_bits(f[j]);
 }
 
-// A t that k of the threads' maxima reach: the k-th largest of them, or one that exactly
-// k reach.  0: fewer than k threads have one.  The bits below kLow are the same in every
-// value of the type and its sign.
-template <typename T, int NT>
-__device__ __forceinline__ uint32_t kth_of_maxima(const uint32_t* best, int nt, int k) {
+// A t that k of up to 32 kPer values reach: the k-th largest of them, or one that exactly
+// k reach.  bits(i): the order bits of this lane's i-th value, 0 for none.  0: fewer than k
+// values.  The bits below kLow are the same in every value of the type and its sign.
+template <typename T, int kPer, typename F>
+__device__ __forceinline__ uint32_t kth_largest(F bits, int k) {
   constexpr int kLow = sizeof(T) == 2 ? 16 : 0;
-  const int lane = threadIdx.x & 31;
-  uint32_t key[NT / 32], most = 0, least = 0xffffffffu;
+  uint32_t key[kPer], most = 0, least = 0xffffffffu;
   int n = 0;
 #pragma unroll
-  for (int i = 0; i < NT / 32; ++i) {
-    key[i] = i * 32 < nt ? best[i * 32 + lane] : 0u;
+  for (int i = 0; i < kPer; ++i) {
+    key[i] = bits(i);
     most = max(most, key[i]);
     if (key[i]) {
       least = min(least, key[i]);
@@ -324,12 +324,13 @@ __device__ __forceinline__ uint32_t kth_of_maxima(const uint32_t* best, int nt, 
     const uint32_t c = t | (1u << bit);
     n = 0;
 #pragma unroll
-    for (int i = 0; i < NT / 32; ++i) n += key[i] >= c;
+    for (int i = 0; i < kPer; ++i) n += key[i] >= c;
     n = __reduce_add_sync(0xffffffffu, n);
     if (n >= k) t = c;
     if (n == k) return t;
   }
-  // a negative value's low bits are ones
+  // a negative value's low bits are ones, NaN's too
+  if (kLow && t >= 0xffff0000u) return 0xffffffffu;
   if (kLow && !(t & 0x80000000u)) t |= (1u << kLow) - 1;
   return t;
 }
@@ -344,7 +345,7 @@ __device__ void k_largest(const Slice<T>& sl, const Maxima<NT>& mx, int nt, int 
   constexpr unsigned kAll = 0xffffffffu;
   const int lane = threadIdx.x & 31;
   const unsigned below = (1u << lane) - 1;
-  const uint32_t t = kth_of_maxima<T, NT>(mx.best, nt, k);
+  const uint32_t t = kth_largest<T, NT / 32>([&](int i) { return i * 32 < nt ? mx.best[i * 32 + lane] : 0u; }, k);
   const int pieces = (groups + span - 1) / span;
 
   // the threads above t (at most k) and, if they are few, those at t; then their pieces.
@@ -384,6 +385,24 @@ __device__ void k_largest(const Slice<T>& sl, const Maxima<NT>& mx, int nt, int 
   unsigned long long floor = static_cast<unsigned long long>(t) << 32 | (t && !take_ties ? 0xffffffffu : 0u);
   auto order = [&] {
     __syncwarp();
+    // Each is compared with all: n^2 / 32 steps.  Many (k close to the number of threads)
+    // are cut down to those that reach the k-th value first: [4096][1000] fp32 with 64
+    // alternatives 291 us without.
+    if (n > kOrderAtOnce) {
+      const uint32_t kth = kth_largest<T, kCand / 32>(
+          [&](int i) { return i * 32 + lane < n ? static_cast<uint32_t>(sc.cand[i * 32 + lane] >> 32) : 0u; }, k);
+      int kept = 0;
+      for (int i = 0; i < n; i += 32) {
+        const unsigned long long key = i + lane < n ? sc.cand[i + lane] : 0ull;
+        const bool keep = i + lane < n && static_cast<uint32_t>(key >> 32) >= kth;
+        const unsigned who = __ballot_sync(kAll, keep);
+        __syncwarp();                              // read before the place is written
+        if (keep) sc.cand[kept + __popc(who & below)] = key;
+        kept += __popc(who);
+      }
+      n = kept;
+      __syncwarp();
+    }
     for (int i = lane; i < n; i += 32) {
       const unsigned long long key = sc.cand[i];
       int place = 0;

@@ -194,6 +194,36 @@ def test_many_rows_of_many_kinds(dtype):
         check_fwd(x[pick], tokens[pick], k, 1.0, mask[pick], [t[pick] for t in got])
 
 
+@pytest.mark.parametrize("N,V,threads", [(160, 16384, 512), (330, 30000, 256)])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_nan_in_nearly_every_threads_part(N, V, threads, dtype):
+    """More threads that hold NaN than a list of ties takes, beside some that hold none."""
+    x = make(1, V, dtype, 4)
+    vec = 8 if dtype == "bf16" else 4
+    part = torch.arange(V, device="cuda") // vec % threads
+    x[0, part != 5] = math.nan
+    x = x.repeat(N, 1)
+    tokens = torch.zeros((N, 1), dtype=torch.int32, device="cuda")
+    for k in (1, 9, 64):
+        got = eas.token_logprobs_fwd(x, tokens, k)
+        for i in (0, N - 1):
+            check_fwd(x[i:i + 1], tokens[i:i + 1], k, 1.0, None, [t[i:i + 1] for t in got])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("V", [64, 100, 515, 1000, 2047, 5000])
+def test_many_alternatives_of_narrow_rows(V, dtype):
+    """k close to the number of threads: many candidates for few places, with ties."""
+    for N in (3, 400):
+        x = make(N, V, dtype, 6)
+        x[1] = (x[1] * 2).round() / 2                  # a dozen values
+        x[2] = -x[2].abs()
+        tokens = make_tokens(N, V, 1)
+        for k in (33, 64):
+            got = eas.token_logprobs_fwd(x, tokens, k)
+            check_fwd(x[:20], tokens[:20], k, 1.0, None, [t[:20] for t in got])
+
+
 @pytest.mark.parametrize("scale", [2.0 ** -30, 1e-3, 1e3, 2.0 ** 20])
 def test_scales(scale):
     for N in (2, 330):
