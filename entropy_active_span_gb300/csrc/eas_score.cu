@@ -337,8 +337,8 @@ __device__ __forceinline__ uint32_t kth_largest(F bits, int k) {
 
 // The k largest of the slice in order, to `out` (0 where it has fewer), by one warp.
 // The walk was that of nt threads (a power of two) in `groups` groups of kGroup vectors,
-// `span` groups to a piece.
-template <typename T, int NT, int kGroup>
+// `span` groups to a piece.  kMany: k may be close to nt, with many values above t.
+template <typename T, int NT, int kGroup, bool kMany>
 __device__ void k_largest(const Slice<T>& sl, const Maxima<NT>& mx, int nt, int groups, int span, int k, Scratch& sc,
                           unsigned long long* out) {
   constexpr int VEC = kVec16<T>;
@@ -385,10 +385,10 @@ __device__ void k_largest(const Slice<T>& sl, const Maxima<NT>& mx, int nt, int 
   unsigned long long floor = static_cast<unsigned long long>(t) << 32 | (t && !take_ties ? 0xffffffffu : 0u);
   auto order = [&] {
     __syncwarp();
-    // Each is compared with all: n^2 / 32 steps.  Many (k close to the number of threads)
-    // are cut down to those that reach the k-th value first: [4096][1000] fp32 with 64
-    // alternatives 291 us without.
-    if (n > kOrderAtOnce) {
+    // Each is compared with all: n^2 / 32 steps.  Many are cut down to those that reach
+    // the k-th value first: [4096][1000] fp32 with 64 alternatives 83 us, 291 without.
+    // (Where k is far below nt it is not worth its code: [4096][32003] 132 us, 141 with.)
+    if (kMany && n > kOrderAtOnce) {
       const uint32_t kth = kth_largest<T, kCand / 32>(
           [&](int i) { return i * 32 + lane < n ? static_cast<uint32_t>(sc.cand[i * 32 + lane] >> 32) : 0u; }, k);
       int kept = 0;
@@ -668,7 +668,7 @@ __global__ void __launch_bounds__(kThreads, 2) score_fwd_kernel(const ScoreFwdAr
   __syncthreads();
   if (tid < 32) {
     st = row_stats(warps, nt / 32, a.c);
-    if (a.k) k_largest<T, kThreads, kGroup>(sl, mx, nt, groups, span, a.k, sc, list);
+    if (a.k) k_largest<T, kThreads, kGroup, true>(sl, mx, nt, groups, span, a.k, sc, list);
   }
   __syncthreads();
   if (split > 1) {
@@ -801,7 +801,7 @@ __global__ void __launch_bounds__(kRowAll, kRowCtas) score_rows_kernel(const Sco
       const Slice<T> sl(base + row * a.ld, a.V, 0, 1);
       const int groups = (sl.nvec + kStep - 1) / kStep;
       barrier_sync(kFull + turn);
-      if (a.k) k_largest<T, kRowThreads, kGroup>(sl, sh.mx[turn], kRowThreads, groups, span_of(groups), a.k, sc, list);
+      if (a.k) k_largest<T, kRowThreads, kGroup, false>(sl, sh.mx[turn], kRowThreads, groups, span_of(groups), a.k, sc, list);
       const Stats st = row_stats(sh.warps[turn], kRowThreads / 32, a.c);
       __syncwarp();
       if (next < a.N) barrier_arrive(kEmpty + turn);
