@@ -348,6 +348,9 @@ struct GemmArgs {
   int n, m, L, steps;
   int num_m, num_n;                         // tiles down and across X
   int tri, full;                            // tiles of A (or B), of X, a matrix
+  int split, depth;                         // parts of a tile of A along k, and k-blocks of one
+  float* parts;                             // [L][tri][8 slices of 32 x 64][split][64][32]
+  int* arrived;                             // [L][tri][8]: parts of a slice that are there
   float coeffs[3 * kMuonSteps];
   __nv_bfloat16* out;
   float scale;
@@ -361,7 +364,7 @@ struct GemmArgs {
 };
 
 struct Tile {
-  int kind, step, l, m, n, half;
+  int kind, step, l, m, n, half, part;
 };
 
 template <int kHalves>
@@ -369,12 +372,19 @@ __device__ __forceinline__ Tile tile_of(int t, const GemmArgs& a) {
   Tile w;
   w.half = t % kHalves;
   t /= kHalves;
-  const int per_step = a.L * (2 * a.tri + a.full);
+  const int gram = a.L * a.tri * a.split, per_step = gram + a.L * (a.tri + a.full);
   w.step = t / per_step;
   t -= w.step * per_step;
-  if (t < 2 * a.L * a.tri) {
-    w.kind = t < a.L * a.tri ? kGram : kPoly;
-    if (w.kind == kPoly) t -= a.L * a.tri;
+  w.part = 0;
+  if (t < gram + a.L * a.tri) {
+    if (t < gram) {
+      w.kind = kGram;
+      w.part = t % a.split;
+      t /= a.split;
+    } else {
+      w.kind = kPoly;
+      t -= gram;
+    }
     w.l = t / a.tri;
     t -= w.l * a.tri;
     // column by column of the upper triangle: n (n + 1) / 2 tiles before column n
@@ -385,7 +395,7 @@ __device__ __forceinline__ Tile tile_of(int t, const GemmArgs& a) {
     w.m = t - n * (n + 1) / 2;
   } else {
     w.kind = w.step + 1 < a.steps ? kApply : kLast;
-    t -= 2 * a.L * a.tri;
+    t -= gram + a.L * a.tri;
     w.l = t / a.full;
     t -= w.l * a.full;
     // bands of rows, column by column: the next step's first tiles need the first
@@ -396,6 +406,12 @@ __device__ __forceinline__ Tile tile_of(int t, const GemmArgs& a) {
     w.m = band * kBand + t - w.n * height;
   }
   return w;
+}
+
+// A tile's k-blocks, from w.part * a.depth on.
+__device__ __forceinline__ int k_blocks(const Tile& w, const GemmArgs& a) {
+  const int all = ((w.kind == kGram ? a.m : a.n) + 63) / 64;
+  return w.kind == kGram ? min(a.depth, all - w.part * a.depth) : all;
 }
 
 __device__ __forceinline__ int acquire(const int* p) {
@@ -475,11 +491,35 @@ __device__ __forceinline__ void fetch(const GemmArgs& a, const Tile& w, const Bo
   }
 }
 
+// The parts of a slice of 32 rows and 64 columns of A: false for all but the last one to
+// come, which gets their sum, in the order of the parts.
+__device__ __forceinline__ bool sum_parts(const GemmArgs& a, const Tile& w, int slice, int lane, float (&v)[64]) {
+  const long long s = (static_cast<long long>(w.l) * a.tri + w.n * (w.n + 1) / 2 + w.m) * kStoreWarps + slice;
+  float* p = a.parts + s * a.split * 2048 + lane;
+#pragma unroll
+  for (int j = 0; j < 64; ++j) __stcg(p + w.part * 2048 + j * 32, v[j]);
+  __threadfence();
+  __syncwarp();
+  int before = 0;
+  if (lane == 0) before = atomicAdd(&a.arrived[s], 1);
+  if (__shfl_sync(0xffffffffu, before, 0) != a.split - 1) return false;
+  __threadfence();
+  if (lane == 0) a.arrived[s] = 0;                 // for the next step, whose parts wait for this tile
+#pragma unroll
+  for (int j = 0; j < 64; ++j) v[j] = __ldcg(p + j * 32);
+#pragma unroll 1
+  for (int i = 1; i < a.split; ++i)
+#pragma unroll
+    for (int j = 0; j < 64; ++j) v[j] += __ldcg(p + i * 2048 + j * 32);
+  return true;
+}
+
 // A warp's 32 rows (from row0 on; this thread's is row0 + lane) and kCols columns
-// (from n0 on) of a tile.  What the first columns (lo: all) add has been fetched.
+// (from n0 on) of a tile.  What the first columns (lo: all) add has been fetched.  mine:
+// whether the tile's counter is this warp's to add to (of a tile in parts, one does).
 template <int kKind, int kCols>
 __device__ __forceinline__ bool epilogue(const GemmArgs& a, const Tile& w, uint32_t tbase, int row0, int n0,
-                                         int lane, Boxes& b, volatile int* abort_flag) {
+                                         int lane, Boxes& b, volatile int* abort_flag, int slice, bool& mine) {
   static_assert(kCols <= 128, "lo has room for two boxes");
   const int width = kKind <= kPoly ? a.n : a.m;
   const int row = row0 + lane;
@@ -509,6 +549,7 @@ __device__ __forceinline__ bool epilogue(const GemmArgs& a, const Tile& w, uint3
     }
     uint8_t* lo_box = box + 4096 + 2048 * c;
     if constexpr (kKind == kGram) {
+      if (a.split > 1 && !(mine = sum_parts(a, w, slice, lane, v))) return true;
 #pragma unroll
       for (int j = 0; j < 64; ++j) v[j] *= kDown;
     } else if constexpr (kKind == kPoly) {
@@ -672,7 +713,7 @@ __global__ void __launch_bounds__(Geo<CG, kHalves>::kThreads, 1) muon_gemm_kerne
   mma::sync_pair<CG>();
   tc_fence_after();
   const uint32_t tmem = *slot_addr;
-  const int total = a.steps * a.L * (2 * a.tri + a.full) * kHalves;
+  const int total = a.steps * a.L * (a.tri * a.split + a.tri + a.full) * kHalves;
   const uint32_t rempty0 = mma::leader_addr<CG>(&rempty[0]);
 
   if (warp == 0) {
@@ -696,7 +737,8 @@ __global__ void __launch_bounds__(Geo<CG, kHalves>::kThreads, 1) muon_gemm_kerne
         const CUtensorMap* mb = w.kind == kGram ? &a.xs[from] : w.kind == kPoly ? &a.a2 : &a.xn[from];
         const int mrow = w.m * G::kM + static_cast<int>(rank) * 128;
         const int ncol = w.n * G::kTile + w.half * G::kN + static_cast<int>(rank) * 128;
-        const int num_kb = ((w.kind == kGram ? a.m : a.n) + 63) / 64;
+        const int num_kb = k_blocks(w, a);
+        const int kb0 = w.part * a.depth;
         int known = 0;                       // k-blocks whose operands are there
         for (int kb = 0; kb < num_kb; ++kb) {
           if (kb == known) {
@@ -728,8 +770,8 @@ __global__ void __launch_bounds__(Geo<CG, kHalves>::kThreads, 1) muon_gemm_kerne
           if (leader && kb == max(num_kb - kDrawAhead, 0)) mbar_arrive(near_end);
           const uint32_t bar = full0 + 8 * stage;
           if (leader) mbar_arrive_expect_tx(&full[stage], CG * 128 * (128 + G::kRowsB));
-          mma::load_3d<CG>(s_a + stage * kOperand, ma, bar, kb * 64, mrow, w.l);
-          if (w.kind <= kPoly) mma::load_3d<CG>(s_b + stage * kOperand, mb, bar, kb * 64, ncol, w.l);
+          mma::load_3d<CG>(s_a + stage * kOperand, ma, bar, (kb0 + kb) * 64, mrow, w.l);
+          if (w.kind <= kPoly) mma::load_3d<CG>(s_b + stage * kOperand, mb, bar, (kb0 + kb) * 64, ncol, w.l);
           else mma::load_4d<CG>(s_b + stage * kOperand, mb, bar, 0, kb * 64, ncol >> 6, w.l);
           if (++stage == kStages) {
             stage = 0;
@@ -777,13 +819,13 @@ __global__ void __launch_bounds__(Geo<CG, kHalves>::kThreads, 1) muon_gemm_kerne
       t = __shfl_sync(0xffffffffu, t, 0);
       if (!ok || t < 0) break;
       const Tile w = tile_of<kHalves>(t, a);
-      const int num_kb = ((w.kind == kGram ? a.m : a.n) + 63) / 64;
+      const int num_kb = k_blocks(w, a);
       const int chunks = (num_kb + G::kChunk - 1) / G::kChunk;
       const int want = G::kDone * (w.kind == kGram ? w.step : w.step + 1);
       for (int c0 = 0; ok && c0 < chunks; c0 += 16) {
         // lanes 0 to 15 watch the first operand's counters, 16 to 31 the second one's
         const int mine = c0 + (lane & 15), most = min(chunks - c0, 16);
-        const int* at = mine < chunks ? operand_counter(w, mine, lane >> 4, a) : nullptr;
+        const int* at = mine < chunks ? operand_counter(w, mine + w.part * (a.depth / G::kChunk), lane >> 4, a) : nullptr;
         bool ready = !at;
         int have = 0;                      // of these chunks, from the first on
         long long t0 = clock64();
@@ -825,7 +867,7 @@ __global__ void __launch_bounds__(Geo<CG, kHalves>::kThreads, 1) muon_gemm_kerne
         if (t < 0) break;
         const Tile w = tile_of<kHalves>(t, a);
         const bool k_rows = w.kind > kPoly;        // X's rows are k
-        const int num_kb = ((w.kind == kGram ? a.m : a.n) + 63) / 64;
+        const int num_kb = k_blocks(w, a);
         const uint32_t idesc = k_rows ? mma::idesc_f16_f32(G::kM, G::kN, false, true)
                                       : mma::idesc_f16_f32(G::kM, G::kN, false, false);
         const uint32_t b_lbo = k_rows ? 8192 : 16, b_step = k_rows ? 2048 : 32;
@@ -897,11 +939,12 @@ __global__ void __launch_bounds__(Geo<CG, kHalves>::kThreads, 1) muon_gemm_kerne
         break;
       }
       tc_fence_after();
-      bool ok;
-      if (w.kind == kGram) ok = epilogue<kGram, kCols>(a, w, tbase, row0, n0, lane, b, abort_flag);
-      else if (w.kind == kPoly) ok = epilogue<kPoly, kCols>(a, w, tbase, row0, n0, lane, b, abort_flag);
-      else if (w.kind == kApply) ok = epilogue<kApply, kCols>(a, w, tbase, row0, n0, lane, b, abort_flag);
-      else ok = epilogue<kLast, kCols>(a, w, tbase, row0, n0, lane, b, abort_flag);
+      bool ok, mine = w.part == 0;
+      const int slice = kHalves * (warp - 2) + w.half;
+      if (w.kind == kGram) ok = epilogue<kGram, kCols>(a, w, tbase, row0, n0, lane, b, abort_flag, slice, mine);
+      else if (w.kind == kPoly) ok = epilogue<kPoly, kCols>(a, w, tbase, row0, n0, lane, b, abort_flag, slice, mine);
+      else if (w.kind == kApply) ok = epilogue<kApply, kCols>(a, w, tbase, row0, n0, lane, b, abort_flag, slice, mine);
+      else ok = epilogue<kLast, kCols>(a, w, tbase, row0, n0, lane, b, abort_flag, slice, mine);
       if (!ok) {
         report(a.status, kStTimeout, kWhereMuon + 9, t);
         break;
@@ -911,7 +954,7 @@ __global__ void __launch_bounds__(Geo<CG, kHalves>::kThreads, 1) muon_gemm_kerne
       __syncwarp();
       if (lane == 0) {
         mma::arrive_at(tempty0 + 8 * buf);
-        if (w.kind != kLast) {
+        if (w.kind != kLast && mine) {
           mma::stores_done();
           fence_async_global();
           const long long l = w.l;
@@ -1304,6 +1347,13 @@ cudaError_t run_steps(const MuonArgs& a, MapEncoder enc, int num_sms, cudaStream
   g.num_n = (a.m + T - 1) / T;
   g.tri = g.num_m * (g.num_m + 1) / 2;
   g.full = g.num_m * g.num_n;
+  g.depth = (g.m + 63) / 64;
+  g.split = 1;
+  if (CG == 1 && a.split > 1) {
+    g.depth = ((g.depth + a.split - 1) / a.split + G::kChunk - 1) / G::kChunk * G::kChunk;
+    g.split = ((g.m + 63) / 64 + g.depth - 1) / g.depth;
+  }
+  g.parts = a.parts;
   memcpy(g.coeffs, a.coeffs, sizeof(float) * 3 * static_cast<size_t>(a.steps));
   g.out = a.out;
   g.scale = a.scale;
@@ -1312,6 +1362,7 @@ cudaError_t run_steps(const MuonArgs& a, MapEncoder enc, int num_sms, cudaStream
   g.done_a = a.sync + 32;
   g.done_b = g.done_a + static_cast<long long>(a.L) * g.num_m * g.num_m;
   g.done_x = g.done_b + static_cast<long long>(a.L) * g.num_m * g.num_m;
+  g.arrived = g.done_x + static_cast<long long>(a.L) * g.full;
   g.status = a.status;
   g.budget = a.budget;
   const auto kernel = muon_gemm_kernel<CG, kHalves>;
@@ -1319,7 +1370,7 @@ cudaError_t run_steps(const MuonArgs& a, MapEncoder enc, int num_sms, cudaStream
   if (e != cudaSuccess) return e;
   // a CTA an SM at most; CTAs wait for one another, so they are launched to run
   // together
-  const long long tiles = static_cast<long long>(g.tri + g.tri + g.full) * a.L * a.steps * kHalves, most = num_sms / CG;
+  const long long tiles = static_cast<long long>(g.tri * g.split + g.tri + g.full) * a.L * a.steps * kHalves, most = num_sms / CG;
   cudaLaunchAttribute attr[2] = {};
   attr[0].id = cudaLaunchAttributeCooperative;
   attr[0].val.cooperative = 1;
@@ -1354,6 +1405,16 @@ cudaError_t prepare(const MuonArgs& a, int num_sms, cudaStream_t s) {
 
 }  // namespace
 
+// Parts of a tile of A along k (where tiles are 128 x 128 or halves of that): a few long
+// products would leave most SMs idle.  A part of k-blocks takes 416 to 555 clocks each, a
+// part's sum 64 KB from L2, twice that: ten k-blocks a part at least, eight parts at most.
+// [129][8000] 136 us, 250 in one part; [200][3000] 115 and 142.
+static long long gram_split(long long L, long long n, long long m) {
+  const long long tn = (n + 127) / 128, tri = tn * (tn + 1) / 2, kb = (m + 63) / 64;
+  const long long most = L > 0 ? 64 / (L * tri) : 0, s = kb / 10 < most ? kb / 10 : most;
+  return s > 8 ? 8 : s < 1 ? 1 : s;
+}
+
 MuonPlan muon_plan(long long L, long long rows, long long cols) {
   MuonPlan p;
   const long long n = rows < cols ? rows : cols, m = rows < cols ? cols : rows, size = n * m;
@@ -1367,14 +1428,17 @@ MuonPlan muon_plan(long long L, long long rows, long long cols) {
   const size_t x = up(static_cast<size_t>(L * n * p.ldx)), q = up(static_cast<size_t>(2 * L * n * p.lda));
   // a drawing counter (a line of its own) and one a tile, of the smaller tiles
   const size_t tn = static_cast<size_t>((n + 127) / 128), tm = static_cast<size_t>((m + 127) / 128);
-  p.sync_words = 32 + static_cast<size_t>(L) * tn * (2 * tn + tm);
+  p.split = gram_split(L, n, m);
+  const size_t slices = static_cast<size_t>(L) * (tn * (tn + 1) / 2) * kStoreWarps;
+  p.sync_words = 32 + static_cast<size_t>(L) * tn * (2 * tn + tm) + slices;
   p.sync = up(sizeof(DevStatus));
   p.partial = p.sync + up(4 * p.sync_words);
   p.x[0] = p.partial + up(static_cast<size_t>(8 * L * p.chunks));
   for (int i = 1; i < 4; ++i) p.x[i] = p.x[i - 1] + (i % 2 ? 2 : 1) * x;     // hi, lo, hi, lo
   p.gram = p.x[3] + x;
   p.poly = p.gram + q;
-  p.total = p.poly + q;
+  p.parts = p.poly + q;
+  p.total = p.parts + (p.split > 1 ? slices * static_cast<size_t>(p.split) * 8192 : 0);
   return p;
 }
 

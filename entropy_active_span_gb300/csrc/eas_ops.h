@@ -147,9 +147,11 @@ struct MuonPlan {         // sizes of the workspace, in bytes from its start
   size_t partial;         // double [L][chunks]
   size_t x[4];            // X's two pairs: hi (fp16), lo (e5m2), hi, lo
   size_t gram, poly;
+  size_t parts;           // float, of the tiles of A that are computed in parts
   size_t total;
   long long ldx, lda;     // row pitches in elements
   long long chunk, chunks;
+  long long split;        // parts of a tile of A
 };
 MuonPlan muon_plan(long long L, long long rows, long long cols);
 struct MuonPair {
@@ -175,6 +177,8 @@ struct MuonArgs {
   MuonPair x[2];
   __half* gram;           // A
   __half* poly;           // B
+  float* parts;           // of A's tiles
+  long long split;
   long long ldx, lda;
   int* sync;              // counters of the products, zero at their start
   long long sync_words;

@@ -94,6 +94,19 @@ def test_momentum(L, n, m, nesterov, mom, dtype):
     assert torch.equal(again, out) and torch.equal(buf, other)
 
 
+@pytest.mark.parametrize("shape", [(1, 129, 8000), (1, 8000, 129), (1, 200, 3001), (5, 100, 5000), (1, 64, 1279), (1, 64, 1280),
+                                   (1, 700, 2049), (2, 300, 2500), (1, 1, 6000), (1, 1920, 255), (1, 513, 1281)])
+def test_few_long_products(shape):
+    """A's tiles in parts along k: as good as in one, and the same again in the same workspace."""
+    g = torch.randn(shape, generator=torch.Generator().manual_seed(5)).cuda()
+    ws = eas.workspace(eas.orthogonalize_workspace_size(*shape), g.device)
+    ws.fill_(0xff)
+    first = eas.orthogonalize(g, ws=ws)
+    check_all(first, f64(g))
+    for _ in range(5):
+        assert torch.equal(eas.orthogonalize(g, ws=ws), first)
+
+
 def test_steps_coefficients_scale():
     g = gradient(1, 200, 300, "fp32", 1, "normal")[0]
     for steps in (1, 2, 7):
