@@ -1450,9 +1450,10 @@ cudaError_t launch_muon(const MuonArgs& a, int grad_bf16, MapEncoder enc, int nu
   // goes by X's tiles of 128 x 128: where each SM gets half of one at most, halves, which
   // take in 24 KB a k-block instead of 32 ([1003][777] 130 us and 143, [320][320] 87 and
   // 99); where it gets one, whole ones ([1088][1088] 155 us); else 256 x 256 tiles by
-  // pairs, which take in half the bytes an operation.
+  // pairs, which take in half the bytes an operation, but would be half empty at 128 rows
+  // or fewer (12 x [128][4096] 157 us, 230 by pairs; [128][40000] 257 and 975).
   const long long small = static_cast<long long>(a.L) * ((a.n + 127) / 128) * ((a.m + 127) / 128);
-  return small > num_sms       ? run_steps<2, 1>(a, enc, num_sms, s)
+  return small > num_sms && a.n > 128 ? run_steps<2, 1>(a, enc, num_sms, s)
          : 2 * small > num_sms ? run_steps<1, 1>(a, enc, num_sms, s)
                                : run_steps<1, 2>(a, enc, num_sms, s);
 }

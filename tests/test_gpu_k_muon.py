@@ -94,8 +94,8 @@ def test_momentum(L, n, m, nesterov, mom, dtype):
     assert torch.equal(again, out) and torch.equal(buf, other)
 
 
-@pytest.mark.parametrize("shape", [(1, 129, 8000), (1, 8000, 129), (1, 200, 3001), (5, 100, 5000), (1, 64, 1279), (1, 64, 1280),
-                                   (1, 700, 2049), (2, 300, 2500), (1, 1, 6000), (1, 1920, 255), (1, 513, 1281)])
+@pytest.mark.parametrize("shape", [(1, 129, 8000), (1, 8000, 129), (1, 200, 3001), (1, 64, 1279), (1, 64, 1280),
+                                   (1, 700, 2049), (2, 300, 2500), (5, 100, 5000), (30, 128, 900), (1, 20000, 128), (1, 1, 6000), (1, 1920, 255), (1, 513, 1281)])
 def test_few_long_products(shape):
     """A's tiles in parts along k: as good as in one, and the same again in the same workspace."""
     g = torch.randn(shape, generator=torch.Generator().manual_seed(5)).cuda()
