@@ -1447,13 +1447,17 @@ cudaError_t launch_muon(const MuonArgs& a, int grad_bf16, MapEncoder enc, int nu
   const cudaError_t e = grad_bf16 ? prepare<__nv_bfloat16>(a, num_sms, s) : prepare<float>(a, num_sms, s);
   if (e != cudaSuccess) return e;
   // Products are deep (n or m) and few tiles wide where matrices are small, so the rule
-  // goes by X's tiles of 128 x 128: where each SM gets half of one at most, halves, which
+  // goes by X's tiles of 128 x 128.  Where each SM gets half of one at most, halves, which
   // take in 24 KB a k-block instead of 32 ([1003][777] 130 us and 143, [320][320] 87 and
-  // 99); where it gets one, whole ones ([1088][1088] 155 us); else 256 x 256 tiles by
-  // pairs, which take in half the bytes an operation, but would be half empty at 128 rows
-  // or fewer (12 x [128][4096] 157 us, 230 by pairs; [128][40000] 257 and 975).
+  // 99).  Where it gets few, whole ones, X X^T of few tiles in parts ([2048][2048] 259 us
+  // and 268 by pairs, [640][8192] 226 and 335).  Else 256 x 256 tiles by pairs, which take
+  // in half the bytes an operation ([2560][2560], 2.6 tiles an SM, 343 us and 400).  That
+  // matters less the less deep the products are (2 x [384][4096], 155 us and 208;
+  // 3 x [300][8000], 3.7 an SM, 232 and 327; 8 x [320][4096], 5 an SM, 275 and 269), and
+  // at 128 rows or fewer pairs would be half empty (12 x [128][4096] 157 us and 230).
   const long long small = static_cast<long long>(a.L) * ((a.n + 127) / 128) * ((a.m + 127) / 128);
-  return small > num_sms && a.n > 128 ? run_steps<2, 1>(a, enc, num_sms, s)
+  const bool single = a.n <= 128 || 4 * small <= (a.n <= 384 ? 16LL : 9LL) * num_sms;
+  return !single               ? run_steps<2, 1>(a, enc, num_sms, s)
          : 2 * small > num_sms ? run_steps<1, 1>(a, enc, num_sms, s)
                                : run_steps<1, 2>(a, enc, num_sms, s);
 }

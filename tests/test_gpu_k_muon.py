@@ -64,7 +64,8 @@ def test_orthogonalize(n, m, dtype):
 
 # stacks: small ones, and large enough for 256 x 256 tiles (odd ends, both ways round)
 @pytest.mark.parametrize("L,n,m", [(3, 40, 70), (5, 130, 90), (12, 128, 128), (16, 520, 1100), (20, 700, 513),
-                                   (40, 300, 257), (1, 3400, 3333)])
+                                   (40, 300, 257), (1, 3400, 3333), (2, 640, 4097),
+                                   (30, 256, 512), (12, 200, 2000), (1, 1700, 1650)])
 def test_stacks(L, n, m):
     g = gradient(L, n, m, "bf16", L)
     out = eas.orthogonalize(g)
