@@ -1407,11 +1407,12 @@ cudaError_t prepare(const MuonArgs& a, int num_sms, cudaStream_t s) {
 
 // Parts of a tile of A along k (where tiles are 128 x 128 or halves of that): a few long
 // products would leave most SMs idle.  A part of k-blocks takes 416 to 555 clocks each, a
-// part's sum 64 KB from L2, twice that: ten k-blocks a part at least, eight parts at most.
+// part's sum 64 KB from L2, twice that: ten k-blocks a part at least, eight parts at most,
+// and all of them at once ([640][8192] 220 us, 228 with four parts instead of five).
 // [129][8000] 136 us, 250 in one part; [200][3000] 115 and 142.
 static long long gram_split(long long L, long long n, long long m) {
   const long long tn = (n + 127) / 128, tri = tn * (tn + 1) / 2, kb = (m + 63) / 64;
-  const long long most = L > 0 ? 64 / (L * tri) : 0, s = kb / 10 < most ? kb / 10 : most;
+  const long long most = L > 0 ? 76 / (L * tri) : 0, s = kb / 10 < most ? kb / 10 : most;
   return s > 8 ? 8 : s < 1 ? 1 : s;
 }
 
