@@ -548,7 +548,8 @@ eas_status eas_token_logprobs_bwd(const float* g_logprob, const float* g_entropy
  *   eps      >= 1e-30 (a zero matrix gives zeros)
  *   out      [L][rows][cols] bf16
  *   ws       eas_orthogonalize_workspace_size(L, rows, cols) bytes, about
- *            6 + 4 n / m bytes an element for n <= m; holds the status word
+ *            6 + 4 n / m bytes an element for n <= m and up to 5 MB; holds the status
+ *            word
  * rows and cols are at most EAS_MAX_MUON_SIDE, L at most 65535.
  */
 #define EAS_MAX_MUON_SIDE 65536

@@ -108,6 +108,26 @@ def test_few_long_products(shape):
         assert torch.equal(eas.orthogonalize(g, ws=ws), first)
 
 
+def test_graphs_share_a_workspace():
+    """Two captured calls over one workspace, replayed in turn: parts and counters of the one
+    are nothing to the other."""
+    shapes = [(1, 129, 8000), (2, 300, 2500)]
+    gs = [torch.randn(s, generator=torch.Generator().manual_seed(i)).cuda() for i, s in enumerate(shapes)]
+    refs = [eas.orthogonalize(g) for g in gs]
+    ws = eas.workspace(max(eas.orthogonalize_workspace_size(*s) for s in shapes), "cuda:0")
+    outs = [torch.empty_like(r) for r in refs]
+    graphs = []
+    for g, o in zip(gs, outs):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            eas.orthogonalize(g, ws=ws, out=o)
+    for i in (0, 1, 1, 0, 0, 1):
+        outs[i].zero_()
+        graphs[i].replay()
+        torch.cuda.synchronize()
+        assert torch.equal(outs[i], refs[i])
+
+
 def test_steps_coefficients_scale():
     g = gradient(1, 200, 300, "fp32", 1, "normal")[0]
     for steps in (1, 2, 7):
