@@ -116,8 +116,7 @@ eas_status eas_rmsnorm_fwd(const void* x, const void* residual, const void* weig
                            void* sum_out, void* y, uint8_t* y_e4m3, float* y_scale, void* stream) {
   eas_status st = check_rows(R, H, dtype);
   if (st != EAS_OK) return st;
-  // below, the factor of a matrix of that norm would leave fp32
-  if (!(eps >= 1e-30f) || !std::isfinite(eps)) return fail(EAS_ERR_INVALID_ARG, "eps must be 1e-30 or more");
+  if (!(eps > 0.f) || !std::isfinite(eps)) return fail(EAS_ERR_INVALID_ARG, "eps must be positive");
   if (!weight || (R > 0 && !x)) return fail(EAS_ERR_INVALID_ARG, "null pointer");
   if ((y_e4m3 == nullptr) != (y_scale == nullptr))
     return fail(EAS_ERR_INVALID_ARG, "y_e4m3 and y_scale come together");
@@ -152,8 +151,7 @@ eas_status eas_rmsnorm_bwd(const void* dy, const void* sum, const void* weight, 
                            void* dx, float* dweight, void* ws, size_t ws_bytes, void* stream) {
   eas_status st = check_rows(R, H, dtype);
   if (st != EAS_OK) return st;
-  // below, the factor of a matrix of that norm would leave fp32
-  if (!(eps >= 1e-30f) || !std::isfinite(eps)) return fail(EAS_ERR_INVALID_ARG, "eps must be 1e-30 or more");
+  if (!(eps > 0.f) || !std::isfinite(eps)) return fail(EAS_ERR_INVALID_ARG, "eps must be positive");
   if (!weight || !dweight || !ws || (R > 0 && (!dy || !sum || !dx)))
     return fail(EAS_ERR_INVALID_ARG, "null pointer");
   if (!aligned(dy, 16) || !aligned(sum, 16) || !aligned(weight, 16) || !aligned(ds, 16) ||
