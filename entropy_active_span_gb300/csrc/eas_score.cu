@@ -71,9 +71,10 @@ __device__ __forceinline__ uint4 load_block(const T* row, int col) {
   return __ldg(reinterpret_cast<const uint4*>(row + col));
 }
 
-// A vector that adds nothing to sums whose largest value is above kFillerMost, if c is
-// below kFillerScale (-1e30 everywhere): what a thread takes where it has none left.
-constexpr float kFillerMost = -1e25f, kFillerScale = 1e7f;
+// A vector that adds nothing to sums whose largest value is above kFillerMost, if c lies
+// between kFillerLeast and kFillerScale (-1e30 everywhere, an exponent of -1e3 to -1e37):
+// what a thread takes where it has none left.
+constexpr float kFillerMost = -1e25f, kFillerLeast = 1e-27f, kFillerScale = 1e7f;
 template <typename T>
 __device__ __forceinline__ uint4 filler() {
   const uint32_t w = sizeof(T) == 2 ? 0xf14af14au : 0xf149f2cau;
@@ -255,7 +256,7 @@ struct Walk {
   // The same of a group of which only the first n vectors may be there (all: they are).
   template <typename T, int N, typename F>
   __device__ __forceinline__ float add_some(const uint4 (&r)[N], bool all, float c, F again, int n) {
-    if (all || (c < kFillerScale && group_max<T>(r) > kFillerMost)) return add<T>(r, c, again);
+    if (all || (c > kFillerLeast && c < kFillerScale && group_max<T>(r) > kFillerMost)) return add<T>(r, c, again);
     float most = -INFINITY;
 #pragma unroll 1
     for (int i = 0; i < N && i < n; ++i) {
