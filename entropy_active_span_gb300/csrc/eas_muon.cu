@@ -5,15 +5,18 @@
 //   each step  A = X X^T,  B = b A + c A A,  X = a X + B X;  out = scale X.
 //
 // The products run on the tensor cores with fp16 operands and fp32 accumulators.
-// X is kept in 14 bits: hi in fp16, and what that leaves out, lo, in e5m2 (times 2^11).
+// X is kept in 22 bits: hi in fp16, and what that leaves out, lo, in fp16 too (times 2^11).
 // hi is multiplied; B holds a on its diagonal, so B hi + a lo is the next X.  What decides
-// the precision is X's own rounding: an error in a direction of small singular values
-// grows with them by a each step, beside large ones that do not grow.  On gradients of low
-// rank with noise, X in one fp16 ends 5e-3 off, in bf16 4e-2, with lo 5e-4 (512 to 1024
-// rows, five steps; Gaussian ones 1.4e-3; the output's rounding to bf16 is 1.7e-3).  The
-// roundings of A, B and of hi in the products stay where they are, each 2^-11 of its own
-// product.  Everything is stored times 2^12, so that fp16's range covers entries from
-// 2^-36 to 16.
+// the precision is X's own rounding: an error in directions that the gradient does not have
+// grows by a each step, beside singular values near 1 that do not grow: 485 times in five of
+// the usual steps, 20 000 times in eight.  A gradient of rank 1 in five steps ends 1.5e-1 off
+// with hi alone, 7e-3 with lo in eight bits (e5m2), 2.6e-3 with these; rank 8 in seven steps
+// 5e-1, 2.3e-2 and 2.5e-3 (256 x 512; the output's rounding to bf16 is 1.7e-3 of it).  lo in
+// eight bits would save 2 to 4 % of the time at 1024 rows and more.  The roundings of A, B
+// and of hi in the products stay where they are, each 2^-11 of its own product: they turn
+// singular vectors, which does not grow.  fp32 sums leave 2^-23 of X a step for every 16 terms,
+// in squares, and that does: about 3e-8 sqrt(n) prod |a|.  Everything is stored times 2^12, so
+// that fp16's range covers entries from 2^-36 to 16.
 //
 // A and A A are symmetric: only tiles on and above the diagonal are computed, and
 // stored twice, the second time transposed.  A step takes 3 n^2 m + n^3 operations.
@@ -21,7 +24,6 @@
 #include <type_traits>
 
 #include <cuda_fp16.h>
-#include <cuda_fp8.h>
 
 #include "eas_launch.cuh"
 #include "eas_mma.cuh"
@@ -185,10 +187,8 @@ __device__ __forceinline__ uint32_t hi_bits(float a, float b) {
 __device__ __forceinline__ float2 hi_values(uint32_t w) { return __half22float2(*reinterpret_cast<const __half2*>(&w)); }
 __device__ __forceinline__ uint32_t lo_bits(float a, float b, uint32_t hi) {
   const float2 h = hi_values(hi);
-  return __nv_cvt_float2_to_fp8x2(make_float2((a - h.x) * kLoUp, (b - h.y) * kLoUp), __NV_SATFINITE, __NV_E5M2);
+  return hi_bits((a - h.x) * kLoUp, (b - h.y) * kLoUp);
 }
-// Two lo (the lower 16 bits of w), times 2^11: an e5m2 is the upper half of an fp16.
-__device__ __forceinline__ float2 lo_values(uint32_t w) { return hi_values(__byte_perm(w, 0u, 0x1404)); }
 
 __device__ __forceinline__ void write_pair(const MuonPair& x, long long o, const float (&v)[8], float f) {
   uint32_t hi[4], lo[4];
@@ -199,7 +199,7 @@ __device__ __forceinline__ void write_pair(const MuonPair& x, long long o, const
     lo[j] = lo_bits(p, q, hi[j]);
   }
   *reinterpret_cast<uint4*>(x.hi + o) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-  *reinterpret_cast<uint2*>(x.lo + o) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
+  *reinterpret_cast<uint4*>(x.lo + o) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
 }
 
 // 2^12 / (norm + eps) from the sum of squares.
@@ -450,28 +450,24 @@ __device__ __forceinline__ void load64(uint32_t taddr, float (&v)[64]) {
 
 __device__ __forceinline__ uint32_t word_of(const uint4& r, int i) { return i == 0 ? r.x : i == 1 ? r.y : i == 2 ? r.z : r.w; }
 
-// The row of a [32][64] fp16 box in the 128-byte swizzled layout.
-__device__ __forceinline__ void get_box(const uint8_t* box, int lane, uint4 (&r)[8]) {
+// 16-byte block j of a row in a [..][64] fp16 box in the 128-byte swizzled layout.
+__device__ __forceinline__ uint4* swizzled(uint8_t* box, int row, int j) {
+  return reinterpret_cast<uint4*>(box + row * 128 + ((j ^ (row & 7)) << 4));
+}
+__device__ __forceinline__ void get_box(uint8_t* box, int lane, uint4 (&r)[8]) {
 #pragma unroll
-  for (int j = 0; j < 8; ++j)
-    r[j] = *reinterpret_cast<const uint4*>(box + lane * 128 + ((j ^ (lane & 7)) << 4));
+  for (int j = 0; j < 8; ++j) r[j] = *swizzled(box, lane, j);
 }
 __device__ __forceinline__ void put_box(uint8_t* box, int lane, const uint32_t (&w)[32]) {
 #pragma unroll
   for (int j = 0; j < 8; ++j)
-    *reinterpret_cast<uint4*>(box + lane * 128 + ((j ^ (lane & 7)) << 4)) =
-        make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+    *swizzled(box, lane, j) = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
 }
 
-// The same of a [32][64] e5m2 box in the 64-byte swizzled layout: 16-byte block j of the
-// row.
-__device__ __forceinline__ uint4* lo_block(uint8_t* box, int lane, int j) {
-  return reinterpret_cast<uint4*>(box + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4));
-}
-
-// What a storing warp keeps: two boxes of 4 KB (the first: A, or the values to be stored;
-// the second: their transpose, or lo of the tile's columns, 64 by 64), their load barrier
-// and its phase.
+// What a storing warp keeps: two boxes of 4 KB, their load barrier and its phase.  The first
+// takes A and then A or B to be stored, the second their transpose.  Of X the second takes
+// lo of the first 64 columns, then hi to be stored; the first lo of the other 64, then
+// lo to be stored.
 struct Boxes {
   uint8_t* box;
   uint64_t* bar;
@@ -487,9 +483,9 @@ __device__ __forceinline__ void fetch(const GemmArgs& a, const Tile& w, const Bo
     mma::load_3d<1>(b.box, &a.as, smem_u32(b.bar), col, row0, w.l);
   } else if constexpr (kKind >= kApply) {
     const int n = min((a.m - col + 63) / 64, cols / 64);
-    mbar_arrive_expect_tx(b.bar, 2048 * n);
+    mbar_arrive_expect_tx(b.bar, 4096 * n);
     for (int c = 0; c < n; ++c)
-      mma::load_3d<1>(b.box + 4096 + 2048 * c, &a.xl[w.step & 1], smem_u32(b.bar), col + 64 * c, row0, w.l);
+      mma::load_3d<1>(b.box + 4096 * (1 - c), &a.xl[w.step & 1], smem_u32(b.bar), col + 64 * c, row0, w.l);
   }
 }
 
@@ -522,21 +518,21 @@ __device__ __forceinline__ bool sum_parts(const GemmArgs& a, const Tile& w, int 
 template <int kKind, int kCols>
 __device__ __forceinline__ bool epilogue(const GemmArgs& a, const Tile& w, uint32_t tbase, int row0, int n0,
                                          int lane, Boxes& b, volatile int* abort_flag, int slice, bool& mine) {
-  static_assert(kCols <= 128, "lo has room for two boxes");
+  static_assert(kCols <= 128, "a box for lo of 64 columns each");
   const int width = kKind <= kPoly ? a.n : a.m;
   const int row = row0 + lane;
   const bool mirror = kKind <= kPoly && w.m != w.n;
   const int to = (w.step & 1) ^ 1;
   const float* abc = a.coeffs + 3 * w.step;
-  const CUtensorMap* s0 = kKind == kGram ? &a.as : kKind == kPoly ? &a.bs : &a.xh[to];
-  const CUtensorMap* s1 = kKind == kGram ? &a.at : kKind == kPoly ? &a.bt : &a.xl[to];
   uint8_t* box = b.box;
-#pragma unroll 1
+  uint4 lo[8];                                     // this row's of 64 columns
+  constexpr int kUnroll = kKind >= kApply ? 2 : 1; // lo stays in registers
+#pragma unroll kUnroll
   for (int c = 0; c < kCols / 64; ++c) {
     const int col = n0 + c * 64;
     if (col >= width || row0 >= a.n) break;        // the same for the warp
     if (c) {
-      // the first box (Gram, Poly: both) has been read before it is filled again
+      // the boxes have been read before they are filled again
       __syncwarp();
       if (lane == 0) {
         if constexpr (kKind != kLast) mma::stores_read();
@@ -549,7 +545,6 @@ __device__ __forceinline__ bool epilogue(const GemmArgs& a, const Tile& w, uint3
       if (!mma::warp_wait(b.bar, b.phase, abort_flag, a.budget)) return false;
       b.phase ^= 1u;
     }
-    uint8_t* lo_box = box + 4096 + 2048 * c;
     if constexpr (kKind == kGram) {
       if (a.split > 1 && !(mine = sum_parts(a, w, slice, lane, v))) return true;
 #pragma unroll
@@ -574,17 +569,20 @@ __device__ __forceinline__ bool epilogue(const GemmArgs& a, const Tile& w, uint3
       // B hi + a lo
       const float f = abc[0] * kLoDown;
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const uint4 r = *lo_block(lo_box, lane, q);
+      for (int j = 0; j < 8; ++j) {
+        const uint4 r = kCols > 64 && c ? lo[j] : *swizzled(box + 4096, lane, j);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float2 x = lo_values(word_of(r, j / 2) >> (j % 2 * 16));
-          float* o = v + 16 * q + 2 * j;
+        for (int p = 0; p < 4; ++p) {
+          const float2 x = hi_values(word_of(r, p));
+          float* o = v + 8 * j + 2 * p;
           o[0] = fmaf(o[0], kDown, f * x.x);
           o[1] = fmaf(o[1], kDown, f * x.y);
         }
       }
     }
+    // Last: the lanes write across the boxes' rows
+    if constexpr (kKind == kLast && kCols > 64)
+      if (c == 0) get_box(box, lane, lo);
     __syncwarp();                                  // lane 0 has waited for the box; lo and A have been read
     if constexpr (kKind == kLast) {
       const float up = a.scale * kDown;
@@ -618,37 +616,50 @@ __device__ __forceinline__ bool epilogue(const GemmArgs& a, const Tile& w, uint3
         }
       }
     } else {
-      uint32_t hi[32];
-#pragma unroll
-      for (int j = 0; j < 32; ++j) hi[j] = hi_bits(v[2 * j], v[2 * j + 1]);
-      put_box(box, lane, hi);
       if constexpr (kKind == kApply) {
+        uint4 rest[8];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          uint32_t lo[4];
+        for (int j = 0; j < 8; ++j) {
+          uint32_t h[4], l[4];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int i = 8 * q + 2 * j;
-            lo[j] = lo_bits(v[2 * i], v[2 * i + 1], hi[i]) | lo_bits(v[2 * i + 2], v[2 * i + 3], hi[i + 1]) << 16;
+          for (int p = 0; p < 4; ++p) {
+            const float x = v[8 * j + 2 * p], y = v[8 * j + 2 * p + 1];
+            h[p] = hi_bits(x, y);
+            l[p] = lo_bits(x, y, h[p]);
           }
-          *lo_block(lo_box, lane, q) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+          *swizzled(box + 4096, lane, j) = make_uint4(h[0], h[1], h[2], h[3]);
+          rest[j] = make_uint4(l[0], l[1], l[2], l[3]);
         }
-      } else if (mirror) {
-        // [64][32]: the columns as rows
-        __half* t = reinterpret_cast<__half*>(box + 4096);
+        // the other columns' lo waits in registers: its box is needed
+        if (kCols > 64 && c == 0) get_box(box, lane, lo);
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
-          const __half2 h = *reinterpret_cast<const __half2*>(&hi[j]);
-          t[(2 * j) * 32 + lane] = __low2half(h);
-          t[(2 * j + 1) * 32 + lane] = __high2half(h);
+        for (int j = 0; j < 8; ++j) *swizzled(box, lane, j) = rest[j];
+      } else {
+        uint32_t hi[32];
+#pragma unroll
+        for (int j = 0; j < 32; ++j) hi[j] = hi_bits(v[2 * j], v[2 * j + 1]);
+        put_box(box, lane, hi);
+        if (mirror) {
+          // [64][32]: the columns as rows
+          __half* t = reinterpret_cast<__half*>(box + 4096);
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            const __half2 h = *reinterpret_cast<const __half2*>(&hi[j]);
+            t[(2 * j) * 32 + lane] = __low2half(h);
+            t[(2 * j + 1) * 32 + lane] = __high2half(h);
+          }
         }
       }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
-        mma::store_3d(s0, box, col, row0, w.l);
-        if constexpr (kKind == kApply) mma::store_3d(s1, lo_box, col, row0, w.l);
-        else if (mirror) mma::store_3d(s1, box + 4096, row0, col, w.l);
+        if constexpr (kKind == kApply) {
+          mma::store_3d(&a.xh[to], box + 4096, col, row0, w.l);
+          mma::store_3d(&a.xl[to], box, col, row0, w.l);
+        } else {
+          mma::store_3d(kKind == kGram ? &a.as : &a.bs, box, col, row0, w.l);
+          if (mirror) mma::store_3d(kKind == kGram ? &a.at : &a.bt, box + 4096, row0, col, w.l);
+        }
         mma::store_commit();
       }
     }
@@ -981,19 +992,25 @@ __global__ void __launch_bounds__(Geo<CG, kHalves>::kThreads, 1) muon_gemm_kerne
 // Up to 128 rows and 512 columns of X: a CTA does a matrix from its gradient to its
 // update.  X's hi lies in shared memory as blocks of 64 columns, [128 rows][128 bytes],
 // swizzled: the layout of an operand whose rows are the result's (X X^T) and, read the
-// other way, of one whose rows are k (B X).  A and then B take two more such blocks, and
-// lo a row-major array.  No product waits for memory: 12 x [128][128] in fp32 take 78 us
-// over the counters above, 27 here.
+// other way, of one whose rows are k (B X).  A and then B take two more such blocks, and lo
+// as many as fit (16 KB a block of 64 columns too): all of them up to 384 columns, five of
+// seven and four of eight beyond; the others' lo lies in the workspace, and comes from L2.
+// No product waits for memory: 12 x [128][128] in fp32 take 78 us over the counters above,
+// 24 here; 12 x [128][448] 55 and [128][512] 61 (53 and 59 with lo in eight
+// bits, all of it in shared memory).
 
 constexpr int kSmallRows = 128, kSmallCols = 512, kSmallThreads = 512;
-constexpr int small_bytes(int m) { return (m + 63) / 64 * (16384 + 8192) + 32768 + 1024 + 256; }
+constexpr int kBlock = 16384;
+__host__ __device__ constexpr int small_blocks(int m) { return (m + 63) / 64; }
+__host__ __device__ constexpr int small_lo(int blocks) { return blocks < 12 - blocks ? blocks : 12 - blocks; }
+constexpr int small_bytes(int blocks) { return (blocks + small_lo(blocks) + 2) * kBlock + 1024 + 256; }
+constexpr bool is_small(long long n, long long m) { return n <= kSmallRows && m <= kSmallCols; }
 
-// 16-byte block j of row r in a block of 64 columns.
-__device__ __forceinline__ uint4* swizzled(uint8_t* block, int r, int j) {
-  return reinterpret_cast<uint4*>(block + r * 128 + ((j ^ (r & 7)) << 4));
+// Eight columns of row r in a block of lo, [8][128 rows] of eight values.
+__device__ __forceinline__ uint4* small_lo_at(uint8_t* lo, int r, int j) {
+  return reinterpret_cast<uint4*>(lo + (j * 128 + r) * 16);
 }
-// Eight columns (8 j0 on) of a row of X to their block of 64 and to lo's, which is
-// [8][128 rows] of eight values.
+// Eight columns (8 j0 on) of a row of X to their block of 64 and to lo's.
 __device__ __forceinline__ void put_x(uint8_t* hi, uint8_t* lo, int r, int j0, const float (&v)[8]) {
   uint32_t h[4], l[4];
 #pragma unroll
@@ -1002,7 +1019,7 @@ __device__ __forceinline__ void put_x(uint8_t* hi, uint8_t* lo, int r, int j0, c
     l[j] = lo_bits(v[2 * j], v[2 * j + 1], h[j]);
   }
   *swizzled(hi, r, j0) = make_uint4(h[0], h[1], h[2], h[3]);
-  *reinterpret_cast<uint2*>(lo + (j0 * 128 + r) * 8) = make_uint2(l[0] | l[1] << 16, l[2] | l[3] << 16);
+  *small_lo_at(lo, r, j0) = make_uint4(l[0], l[1], l[2], l[3]);
 }
 
 template <typename G, typename M, bool kMom>
@@ -1010,16 +1027,18 @@ __global__ void __launch_bounds__(kSmallThreads) muon_small_kernel(const __grid_
   extern __shared__ uint8_t smem_raw[];
   uint8_t* s_x = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                             ~static_cast<uintptr_t>(1023));
-  const int blocks = (a.m + 63) / 64;
-  uint8_t* s_a = s_x + blocks * 16384;
-  uint8_t* s_lo = s_a + 32768;
-  uint64_t* bar = reinterpret_cast<uint64_t*>(s_lo + blocks * 8192);
+  const int blocks = small_blocks(a.m), near = small_lo(blocks);      // near: lo's in shared memory
+  uint8_t* s_a = s_x + blocks * kBlock;
+  uint8_t* s_lo = s_a + 2 * kBlock;
+  uint64_t* bar = reinterpret_cast<uint64_t*>(s_lo + near * kBlock);
   uint32_t* slot = reinterpret_cast<uint32_t*>(bar + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(slot + 1);
   float* factor = reinterpret_cast<float*>(slot + 2);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const long long l = blockIdx.x, base = l * a.rows * a.cols;
   const uint32_t cols = blocks <= 2 ? 128 : blocks <= 4 ? 256 : 512;
+  uint8_t* far = a.far_lo + l * (blocks - near) * kBlock;
+  auto lo_of = [&](int c) { return c < near ? s_lo + c * kBlock : far + (c - near) * kBlock; };
   if (tid == 0) {
     mbar_init(bar, 1);
     *abort_flag = 0;
@@ -1126,7 +1145,7 @@ __global__ void __launch_bounds__(kSmallThreads) muon_small_kernel(const __grid_
       }
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[k][j] *= f;
-      put_x(s_x + (j0 >> 3) * 16384, s_lo + (j0 >> 3) * 8192, r, j0 & 7, v[k]);
+      put_x(s_x + (j0 >> 3) * kBlock, lo_of(j0 >> 3), r, j0 & 7, v[k]);
     }
   }
 
@@ -1213,20 +1232,22 @@ __global__ void __launch_bounds__(kSmallThreads) muon_small_kernel(const __grid_
     for (int u = quarter; u < 2 * blocks; u += 4) {
       tmem_ld32(trow + 32 * u, v);
       const int c = u >> 1;
+      uint8_t* lo_c = lo_of(c);
+      uint4 r[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) r[i] = *small_lo_at(lo_c, row, (u & 1) * 4 + i);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int j = (u & 1) * 4 + i;
-        const uint2 r = *reinterpret_cast<const uint2*>(s_lo + c * 8192 + (j * 128 + row) * 8);
-        const uint32_t w[4] = {r.x, r.x >> 16, r.y, r.y >> 16};
         float x[8];
 #pragma unroll
         for (int p = 0; p < 4; ++p) {
-          const float2 lo = lo_values(w[p]);
+          const float2 lo = hi_values(word_of(r[i], p));
           x[2 * p] = fmaf(v[8 * i + 2 * p], kDown, fl * lo.x);
           x[2 * p + 1] = fmaf(v[8 * i + 2 * p + 1], kDown, fl * lo.y);
         }
         if (!last) {
-          put_x(s_x + c * 16384, s_lo + c * 8192, row, j, x);
+          put_x(s_x + c * kBlock, lo_c, row, j, x);
         } else if (a.tall) {
 #pragma unroll
           for (int p = 0; p < 8; ++p)
@@ -1273,11 +1294,12 @@ __global__ void __launch_bounds__(kSmallThreads) muon_small_kernel(const __grid_
 
 template <typename G, typename M, bool kMom>
 cudaError_t run_small(const MuonArgs& args, cudaStream_t s) {
-  const cudaError_t e = allow_smem<muon_small_kernel<G, M, kMom>>(small_bytes(kSmallCols));
+  static_assert(small_bytes(6) == small_bytes(small_blocks(kSmallCols)) && small_bytes(6) == small_bytes(7), "the most");
+  const cudaError_t e = allow_smem<muon_small_kernel<G, M, kMom>>(small_bytes(6));
   if (e != cudaSuccess) return e;
   MuonArgs a = args;
   memcpy(a.small_coeffs, args.coeffs, sizeof(float) * 3 * static_cast<size_t>(a.steps));
-  muon_small_kernel<G, M, kMom><<<static_cast<unsigned>(a.L), kSmallThreads, small_bytes(a.m), s>>>(a);
+  muon_small_kernel<G, M, kMom><<<static_cast<unsigned>(a.L), kSmallThreads, small_bytes(small_blocks(a.m)), s>>>(a);
   return cudaGetLastError();
 }
 template <typename G>
@@ -1297,14 +1319,12 @@ bool map_of(MapEncoder enc, CUtensorMap* m, CUtensorMapDataType type, const void
 }
 
 // [L][rows][cols] with row pitch ld, in boxes of bc columns x br rows.
-template <typename T>
-bool map_3d(MapEncoder enc, CUtensorMap* m, const T* base, long long cols, long long rows, long long L, long long ld,
+bool map_3d(MapEncoder enc, CUtensorMap* m, const __half* base, long long cols, long long rows, long long L, long long ld,
             int bc, int br, CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(L)};
-  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld) * sizeof(T), static_cast<cuuint64_t>(ld) * sizeof(T) * rows};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld) * 2, static_cast<cuuint64_t>(ld) * 2 * rows};
   const cuuint32_t box[3] = {static_cast<cuuint32_t>(bc), static_cast<cuuint32_t>(br), 1};
-  return map_of(enc, m, sizeof(T) == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, base, 3, dims,
-                strides, box, swizzle);
+  return map_of(enc, m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, base, 3, dims, strides, box, swizzle);
 }
 
 // The same as blocks of 64 columns, `blocks` of them x 64 rows a box: an operand whose rows
@@ -1330,7 +1350,7 @@ cudaError_t run_steps(const MuonArgs& a, MapEncoder enc, int num_sms, cudaStream
          map_3d(enc, &g.xs[i], a.x[i].hi, a.m, a.n, a.L, a.ldx, 64, G::kRowsB) &&
          map_k_rows(enc, &g.xn[i], a.x[i].hi, a.m, a.n, a.L, a.ldx, G::kRowsB / 64) &&
          map_3d(enc, &g.xh[i], a.x[i].hi, a.m, a.n, a.L, a.ldx, 64, 32) &&
-         map_3d(enc, &g.xl[i], a.x[i].lo, a.m, a.n, a.L, a.ldx, 64, 32, CU_TENSOR_MAP_SWIZZLE_64B);
+         map_3d(enc, &g.xl[i], a.x[i].lo, a.m, a.n, a.L, a.ldx, 64, 32);
   }
   ok = ok && map_3d(enc, &g.ak, a.gram, a.n, a.n, a.L, a.lda, 64, 128) &&
        map_3d(enc, &g.a2, a.gram, a.n, a.n, a.L, a.lda, 64, G::kRowsB) &&
@@ -1428,7 +1448,7 @@ MuonPlan muon_plan(long long L, long long rows, long long cols) {
   p.chunk = (p.chunk + 7) / 8 * 8;
   p.chunks = (size + p.chunk - 1) / p.chunk;
   auto up = [](size_t x) { return (x + 1023) / 1024 * 1024; };
-  const size_t x = up(static_cast<size_t>(L * n * p.ldx)), q = up(static_cast<size_t>(2 * L * n * p.lda));
+  const size_t x = up(static_cast<size_t>(2 * L * n * p.ldx)), q = up(static_cast<size_t>(2 * L * n * p.lda));
   // a drawing counter (a line of its own) and one a tile, of the smaller tiles
   const size_t tn = static_cast<size_t>((n + 127) / 128), tm = static_cast<size_t>((m + 127) / 128);
   p.split = gram_split(L, n, m);
@@ -1437,16 +1457,18 @@ MuonPlan muon_plan(long long L, long long rows, long long cols) {
   p.sync = up(sizeof(DevStatus));
   p.partial = p.sync + up(4 * p.sync_words);
   p.x[0] = p.partial + up(static_cast<size_t>(8 * L * p.chunks));
-  for (int i = 1; i < 4; ++i) p.x[i] = p.x[i - 1] + (i % 2 ? 2 : 1) * x;     // hi, lo, hi, lo
+  for (int i = 1; i < 4; ++i) p.x[i] = p.x[i - 1] + x;
   p.gram = p.x[3] + x;
   p.poly = p.gram + q;
   p.parts = p.poly + q;
-  p.total = p.parts + (p.split > 1 ? slices * static_cast<size_t>(p.split) * 8192 : 0);
+  p.far_lo = p.parts + (p.split > 1 ? slices * static_cast<size_t>(p.split) * 8192 : 0);
+  const long long blocks = (m + 63) / 64;
+  p.total = p.far_lo + (is_small(n, m) ? static_cast<size_t>(L * (blocks - small_lo(static_cast<int>(blocks))) * kBlock) : 0);
   return p;
 }
 
 cudaError_t launch_muon(const MuonArgs& a, int grad_bf16, MapEncoder enc, int num_sms, cudaStream_t s) {
-  if (a.n <= kSmallRows && a.m <= kSmallCols) return grad_bf16 ? run_small<__nv_bfloat16>(a, s) : run_small<float>(a, s);
+  if (is_small(a.n, a.m)) return grad_bf16 ? run_small<__nv_bfloat16>(a, s) : run_small<float>(a, s);
   const cudaError_t e = grad_bf16 ? prepare<__nv_bfloat16>(a, num_sms, s) : prepare<float>(a, num_sms, s);
   if (e != cudaSuccess) return e;
   // Products are deep (n or m) and few tiles wide where matrices are small, so the rule

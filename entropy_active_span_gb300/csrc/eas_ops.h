@@ -145,9 +145,10 @@ constexpr int kMuonSteps = 32;    // EAS_MAX_MUON_STEPS
 struct MuonPlan {         // sizes of the workspace, in bytes from its start
   size_t sync, sync_words;
   size_t partial;         // double [L][chunks]
-  size_t x[4];            // X's two pairs: hi (fp16), lo (e5m2), hi, lo
+  size_t x[4];            // X's two pairs: hi, lo, hi, lo (fp16)
   size_t gram, poly;
   size_t parts;           // float, of the tiles of A that are computed in parts
+  size_t far_lo;          // of small matrices: lo that shared memory has no room for
   size_t total;
   long long ldx, lda;     // row pitches in elements
   long long chunk, chunks;
@@ -155,8 +156,7 @@ struct MuonPlan {         // sizes of the workspace, in bytes from its start
 };
 MuonPlan muon_plan(long long L, long long rows, long long cols);
 struct MuonPair {
-  __half* hi;
-  uint8_t* lo;
+  __half *hi, *lo;
 };
 struct MuonArgs {
   const void* grad;       // [L][rows][cols]
@@ -178,6 +178,7 @@ struct MuonArgs {
   __half* gram;           // A
   __half* poly;           // B
   float* parts;           // of A's tiles
+  uint8_t* far_lo;        // of small matrices
   long long split;
   long long ldx, lda;
   int* sync;              // counters of the products, zero at their start

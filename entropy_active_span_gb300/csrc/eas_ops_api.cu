@@ -454,10 +454,11 @@ eas_status eas_orthogonalize(const void* grad, eas_dtype grad_dtype, const void*
   a.partial = at<double>(ws, p.partial);
   a.chunk = static_cast<int>(p.chunk);
   a.chunks = static_cast<int>(p.chunks);
-  for (int i = 0; i < 2; ++i) a.x[i] = {at<__half>(ws, p.x[2 * i]), at<uint8_t>(ws, p.x[2 * i + 1])};
+  for (int i = 0; i < 2; ++i) a.x[i] = {at<__half>(ws, p.x[2 * i]), at<__half>(ws, p.x[2 * i + 1])};
   a.gram = at<__half>(ws, p.gram);
   a.poly = at<__half>(ws, p.poly);
   a.parts = at<float>(ws, p.parts);
+  a.far_lo = at<uint8_t>(ws, p.far_lo);
   a.split = p.split;
   a.ldx = p.ldx;
   a.lda = p.lda;

@@ -532,11 +532,17 @@ eas_status eas_token_logprobs_bwd(const float* g_logprob, const float* g_entropy
  *   (u = g without a momentum);  X = u / (|u| + eps), the 2-norm over the matrix;
  *   for each (a, b, c) of coeffs:  Q = X X^T,  X = a X + (b Q + c Q Q) X;
  *   out = bf16(scale X).
- * Products take fp16 operands (X itself is kept in 14 bits) and fp32 sums: out is
- * within about 2e-3 of its norm, its rounding to bf16 alone being 1.7e-3.  Singular
- * values have to stay below 4 through all steps, and |a| + |b| s^2 + |c| s^4 below 16
- * (with the usual coefficients they stay below 1.3).  Results repeat to the bit.  Where
- * a matrix holds NaN or Inf, or its norm is not finite, its out is NaN.
+ * Products take fp16 operands (X itself is kept in 22 bits) and fp32 sums.  With the
+ * usual coefficients and n = min(rows, cols) of 64 or more, out is within 3.3e-3 of its
+ * 2-norm after five steps, 1.7e-3 of which is its rounding to bf16, and within 5e-3 after
+ * ten; with fewer rows, whose errors do not average out, within 1e-2 after five and several
+ * times that after ten.  Coefficients whose terms cancel more carry 2^-12 of each term of
+ * a step.  Where the matrix has (nearly) no part in some directions, the sums' roundings
+ * there grow with the steps: 4e-8 sqrt(n) times the product of all |a| comes on top,
+ * 1e-3 at n = 4096 after five usual steps, 5e-2 after eight.
+ * Singular values have to stay below 4 through all steps, and |a| + |b| s^2 + |c| s^4
+ * below 16 (with the usual coefficients they stay below 1.3).  Results repeat to the bit.
+ * Where a matrix holds NaN or Inf, or its norm is not finite, its out is NaN.
  *
  *   grad     [L][rows][cols] bf16 or fp32 (grad_dtype), contiguous, like the others
  *   momentum, new_momentum : [L][rows][cols] bf16 or fp32 (momentum_dtype) in and
@@ -548,8 +554,8 @@ eas_status eas_token_logprobs_bwd(const float* g_logprob, const float* g_entropy
  *   eps      >= 1e-30 (a zero matrix gives zeros)
  *   out      [L][rows][cols] bf16
  *   ws       eas_orthogonalize_workspace_size(L, rows, cols) bytes, about
- *            6 + 4 n / m bytes an element for n <= m and up to 5 MB; holds the status
- *            word
+ *            8 + 4 n / m bytes an element for n <= m, both sides rounded up to 64 where
+ *            they are a row's length, and up to 5 MB; holds the status word
  * rows and cols are at most EAS_MAX_MUON_SIDE, L at most 65535.
  */
 #define EAS_MAX_MUON_SIDE 65536
