@@ -18,18 +18,23 @@ using namespace eas;
 namespace {
 
 // A buffer of a call.  `shared`: a written one may replace, whole, a read one that
-// is also marked so.
+// is also marked so.  pitch: it is rows of `row` bytes, that far apart (0: all of it).
 struct Buf {
   const void* p;
   size_t n;
   bool shared = false;
+  size_t row = 0, pitch = 0;
 };
 
-// Whether no written buffer shares a byte with another buffer (null shares none).
+// Whether no written buffer shares a byte with another buffer (null shares none; the bytes
+// between rows count as theirs, except beside other rows of the same pitch).
 bool disjoint(std::initializer_list<Buf> written, std::initializer_list<Buf> read) {
   auto overlap = [](const Buf& a, const Buf& b) {
     const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
-    return x && y && a.n && b.n && x < y + b.n && y < x + a.n;
+    if (!(x && y && a.n && b.n && x < y + b.n && y < x + a.n)) return false;
+    if (a.pitch == 0 || a.pitch != b.pitch) return true;
+    const size_t at = y > x ? (y - x) % a.pitch : (a.pitch - (x - y) % a.pitch) % a.pitch;   // b's rows, from a's on
+    return at < a.row || at + b.row > a.pitch;
   };
   for (const Buf* w = written.begin(); w != written.end(); ++w) {
     for (const Buf* v = w + 1; v != written.end(); ++v)
@@ -371,8 +376,9 @@ eas_status eas_token_logprobs_bwd(const float* g_logprob, const float* g_entropy
     return fail(EAS_ERR_INVALID_ARG, "tensors must be aligned to their elements and ws to 16 bytes");
   if (ws && ws_bytes < sizeof(DevStatus)) return fail(EAS_ERR_WORKSPACE, "workspace too small");
   const size_t n = static_cast<size_t>(N), mb = 4 * n * static_cast<size_t>(M);
-  if (!disjoint({{dlogits, extent(N, V, ld_dlogits, e), true}, {ws, sizeof(DevStatus)}},
-                {{logits, extent(N, V, ld, e), true}, {tokens, mb}, {mask, n}, {g_logprob, mb},
+  const size_t row = static_cast<size_t>(V) * e;
+  if (!disjoint({{dlogits, extent(N, V, ld_dlogits, e), true, row, static_cast<size_t>(ld_dlogits) * e}, {ws, sizeof(DevStatus)}},
+                {{logits, extent(N, V, ld, e), true, row, static_cast<size_t>(ld) * e}, {tokens, mb}, {mask, n}, {g_logprob, mb},
                  {g_entropy, 4 * n}, {lse, 4 * n}, {entropy, 4 * n}}))
     return overlap_error();
   DevInfo di;

@@ -363,7 +363,8 @@ eas_status eas_lmhead_fwd_noalloc(const void* hidden, const void* weight,
 /*
  * In the calls from here to eas_orthogonalize no output and no workspace may
  * share a byte with another buffer of the call, except where an argument says
- * that it may replace another (EAS_ERR_INVALID_ARG).
+ * that it may replace another (EAS_ERR_INVALID_ARG).  The bytes between rows that lie
+ * apart count as the rows', except where an argument says otherwise.
  */
 
 /* --------------------------------------------- norm before the LM head */
@@ -513,8 +514,9 @@ eas_status eas_token_logprobs_fwd(const void* logits, int64_t ld, const int32_t*
  *   lse, entropy : the forward's; p is taken from lse
  *   g_logprob [N, M], g_entropy [N] fp32; g_entropy may be NULL (zero)
  *   dlogits  [N] rows of V values, ld_dlogits apart, in dtype; may be logits itself
- *            (same pitch).  Inactive rows get zeros, whatever logits and the
- *            gradients hold there.  Elements between the rows are left alone.
+ *            (same pitch), or rows of the same pitch between logits' rows.  Inactive
+ *            rows get zeros, whatever logits and the gradients hold there.  Elements
+ *            between the rows are left alone.
  */
 eas_status eas_token_logprobs_bwd(const float* g_logprob, const float* g_entropy,
                                   const void* logits, int64_t ld, const int32_t* tokens,
