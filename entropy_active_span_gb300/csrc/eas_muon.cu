@@ -1439,15 +1439,21 @@ static long long gram_split(long long L, long long n, long long m) {
 }
 
 MuonPlan muon_plan(long long L, long long rows, long long cols) {
-  MuonPlan p;
+  MuonPlan p = {};
   const long long n = rows < cols ? rows : cols, m = rows < cols ? cols : rows, size = n * m;
+  auto up = [](size_t x) { return (x + 1023) / 1024 * 1024; };
+  if (is_small(n, m)) {
+    const int blocks = small_blocks(static_cast<int>(m));
+    p.far_lo = up(sizeof(DevStatus));
+    p.total = p.far_lo + static_cast<size_t>(L * (blocks - small_lo(blocks)) * kBlock);
+    return p;
+  }
   p.ldx = (m + 63) / 64 * 64;
   p.lda = (n + 63) / 64 * 64;
   p.chunk = (size + kMostChunks - 1) / kMostChunks;
   if (p.chunk < kChunk) p.chunk = kChunk;
   p.chunk = (p.chunk + 7) / 8 * 8;
   p.chunks = (size + p.chunk - 1) / p.chunk;
-  auto up = [](size_t x) { return (x + 1023) / 1024 * 1024; };
   const size_t x = up(static_cast<size_t>(2 * L * n * p.ldx)), q = up(static_cast<size_t>(2 * L * n * p.lda));
   // a drawing counter (a line of its own) and one a tile, of the smaller tiles
   const size_t tn = static_cast<size_t>((n + 127) / 128), tm = static_cast<size_t>((m + 127) / 128);
@@ -1461,9 +1467,7 @@ MuonPlan muon_plan(long long L, long long rows, long long cols) {
   p.gram = p.x[3] + x;
   p.poly = p.gram + q;
   p.parts = p.poly + q;
-  p.far_lo = p.parts + (p.split > 1 ? slices * static_cast<size_t>(p.split) * 8192 : 0);
-  const long long blocks = (m + 63) / 64;
-  p.total = p.far_lo + (is_small(n, m) ? static_cast<size_t>(L * (blocks - small_lo(static_cast<int>(blocks))) * kBlock) : 0);
+  p.total = p.parts + (p.split > 1 ? slices * static_cast<size_t>(p.split) * 8192 : 0);
   return p;
 }
 

@@ -142,13 +142,13 @@ cudaError_t launch_score_bwd(const ScoreBwdArgs& a, int is_bf16, int num_sms, cu
 
 // ---- orthogonalised update (eas_muon.cu) ----
 constexpr int kMuonSteps = 32;    // EAS_MAX_MUON_STEPS
-struct MuonPlan {         // sizes of the workspace, in bytes from its start
-  size_t sync, sync_words;
+struct MuonPlan {         // places in the workspace, in bytes from its start
+  size_t far_lo;          // of small matrices, all they take: lo that shared memory has no room for
+  size_t sync, sync_words;   // from here on: of larger ones
   size_t partial;         // double [L][chunks]
   size_t x[4];            // X's two pairs: hi, lo, hi, lo (fp16)
   size_t gram, poly;
   size_t parts;           // float, of the tiles of A that are computed in parts
-  size_t far_lo;          // of small matrices: lo that shared memory has no room for
   size_t total;
   long long ldx, lda;     // row pitches in elements
   long long chunk, chunks;

@@ -556,8 +556,9 @@ eas_status eas_token_logprobs_bwd(const float* g_logprob, const float* g_entropy
  *   eps      >= 1e-30 (a zero matrix gives zeros)
  *   out      [L][rows][cols] bf16
  *   ws       eas_orthogonalize_workspace_size(L, rows, cols) bytes, about
- *            8 + 4 n / m bytes an element for n <= m, both sides rounded up to 64 where
- *            they are a row's length, and up to 5 MB; holds the status word
+ *            8 n m' + 4 n n' bytes a matrix, n <= m, and up to 5 MB and 2 % of that;
+ *            n' and m' are n and m rounded up to 64.  Matrices of n <= 128 and m <= 512
+ *            take 64 KB each at most, none up to m = 384.  Holds the status word
  * rows and cols are at most EAS_MAX_MUON_SIDE, L at most 65535.
  */
 #define EAS_MAX_MUON_SIDE 65536
