@@ -5,6 +5,7 @@
 //   y = c x - fp32(c m),  s = sum 2^y,  u = sum 2^y y,
 //   lse = ln2 (fp32(c m) + log2 s),  logp(t) = ln2 (y_t - log2 s),
 //   H = ln2 (log2 s - u / s),
+// (where c m is so large that its rounding would count, y = c (x - m) and c m itself below),
 // m being close to the largest x: a value is read once, each thread keeps (m, s, u) of
 // what it has seen and moves m when a group of its values reaches 2^4 beyond it (a
 // larger step would cost digits of y).
@@ -105,15 +106,21 @@ struct Stats {
 // not 0 * -inf.
 constexpr float kLeast = -160.f;
 
-// c x - fp32(c m); where c m leaves fp32, c (x - m).
+// Whether c m is far from 0: its rounding, part of every exponent below it, would be 2 or
+// more, from 2^31 on beyond what 2^y takes.  NaN and infinities are far.
+constexpr float kFar = 0x1p26f;
+__device__ __forceinline__ bool is_far(float cm) { return !(fabsf(cm) <= kFar); }
+
+// The exponent of x below m: c x - fp32(c m), or c (x - m).
 __device__ __forceinline__ float exponent(float x, float m, float c) {
   const float cm = __fmul_rn(m, c);
-  return fabsf(cm) < INFINITY ? fmaf(x, c, -cm) : (x - m) * c;
+  return is_far(cm) ? (x - m) * c : fmaf(x, c, -cm);
 }
 // What to add to an exponent below m to have one below n >= m.
 __device__ __forceinline__ float shift(float m, float n, float c) {
-  const float d = __fmul_rn(m, c) - __fmul_rn(n, c);
-  return d <= 0.f ? d : (m - n) * c;
+  const float cm = __fmul_rn(m, c), cn = __fmul_rn(n, c);
+  if (is_far(cn)) return is_far(cm) ? (m - n) * c : -fmaf(n, c, -cm);
+  return is_far(cm) ? fmaf(m, c, -cn) : cm - cn;
 }
 
 // Two statistics of one row.  s = 0: no value but -inf.  A NaN or +inf makes s NaN.
@@ -175,13 +182,13 @@ __device__ __forceinline__ float group_max(const uint4 (&r)[N]) {
 struct Sums {
   float s0, s1, u0, u1;
 
-  // kCareful: some of the values are -inf or so low that y is not finite; wild: c m is not.
+  // kCareful: some of the values are -inf or so low that y is not finite, or c m is far.
   template <bool kCareful>
-  __device__ __forceinline__ void add(float x0, float x1, float m, float cm, float c, bool wild) {
+  __device__ __forceinline__ void add(float x0, float x1, float m, float cm, float c, bool far) {
     float y0 = fmaf(x0, c, -cm), y1 = fmaf(x1, c, -cm);
     if constexpr (kCareful) {
-      y0 = fmaxf(wild ? (x0 - m) * c : y0, kLeast);
-      y1 = fmaxf(wild ? (x1 - m) * c : y1, kLeast);
+      y0 = fmaxf(far ? (x0 - m) * c : y0, kLeast);
+      y1 = fmaxf(far ? (x1 - m) * c : y1, kLeast);
     }
     const float e0 = ex2_approx(y0), e1 = ex2_approx(y1);
     s0 += e0;
@@ -191,16 +198,16 @@ struct Sums {
   }
   template <typename T, bool kCareful, int N>
   __device__ __forceinline__ void add_group(const uint4 (&r)[N], float m, float cm, float c) {
-    const bool wild = kCareful && isinf(cm);
+    const bool far = kCareful && is_far(cm);
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const uint32_t w[4] = {r[i].x, r[i].y, r[i].z, r[i].w};
       if constexpr (sizeof(T) == 2) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) add<kCareful>(bf16_lo(w[j]), bf16_hi(w[j]), m, cm, c, wild);
+        for (int j = 0; j < 4; ++j) add<kCareful>(bf16_lo(w[j]), bf16_hi(w[j]), m, cm, c, far);
       } else {
-        add<kCareful>(__uint_as_float(w[0]), __uint_as_float(w[1]), m, cm, c, wild);
-        add<kCareful>(__uint_as_float(w[2]), __uint_as_float(w[3]), m, cm, c, wild);
+        add<kCareful>(__uint_as_float(w[0]), __uint_as_float(w[1]), m, cm, c, far);
+        add<kCareful>(__uint_as_float(w[2]), __uint_as_float(w[3]), m, cm, c, far);
       }
     }
   }
@@ -210,9 +217,9 @@ struct Sums {
 // the code short (it fits the instruction cache); else it takes them from registers.
 template <bool kAgain>
 struct Walk {
-  bool low = false;                  // a group with values for the careful path has come
+  bool low = false;                  // a group with values for the careful path has come, or c m is far
   float best = -INFINITY;            // the largest value
-  float m = -INFINITY, cm = 0.f;     // reference of the sums
+  float m = -INFINITY, cm = NAN;     // reference of the sums; NaN: no value yet, or far
   Sums sum = {0.f, 0.f, 0.f, 0.f};
 
   // Returns the group's largest value.  again(i): the group's i-th vector once more.
@@ -220,8 +227,8 @@ struct Walk {
   __device__ __forceinline__ float add(const uint4 (&r)[N], float c, F again) {
     const float most = group_max<T>(r);
     best = max_nan(best, most);
-    if (!(fmaf(most, c, -cm) <= 4.f) || m == -INFINITY) {
-      if (most == -INFINITY) return most;              // nothing but -inf so far
+    if (!(fmaf(most, c, -cm) <= 4.f)) {
+      if (most == -INFINITY) return most;              // adds nothing
       const float to = max_nan(m, most);
       if (m != -INFINITY) {
         const float d = fmaxf(shift(m, to, c), kLeast), f = ex2_approx(d);
@@ -231,7 +238,12 @@ struct Walk {
         sum.s1 *= f;
       }
       m = to;
+      low = low && cm == cm;         // far from here no longer
       cm = __fmul_rn(m, c);
+      if (is_far(cm)) {
+        cm = NAN;
+        low = true;
+      }
       if (!(to < INFINITY)) sum.s0 = NAN;
     }
     if (!low) {
@@ -574,7 +586,7 @@ struct Pieces {
 // a rounding below y.
 __device__ __forceinline__ float log_prob(float x, const Stats& st, float ls, const ScoreFwdArgs& a) {
   const float y = exponent(x, st.m, a.c);
-  const float lp = isinf(y) ? fmaf(x - st.m, a.scale, -kLn2 * ls)   // c x may leave fp32 where scale x does not
+  const float lp = isinf(y) ? fmaf(x, a.scale, -(st.m * a.scale)) - kLn2 * ls   // y may leave fp32 where z does not
                             : kLn2 * (y - ls);
   return lp > 0.f ? 0.f : lp;
 }
@@ -599,7 +611,7 @@ __device__ __forceinline__ void write_row(const ScoreFwdArgs& a, long long row, 
   }
   if (tid == 0) {
     const float cm = __fmul_rn(st.m, a.c);
-    a.lse[row] = fabsf(cm) < INFINITY ? kLn2 * (cm + ls) : fmaf(kLn2, ls, st.m * a.scale);
+    a.lse[row] = is_far(cm) ? fmaf(kLn2, ls, st.m * a.scale) : kLn2 * (cm + ls);
     const float h = kLn2 * (ls - st.u / st.s);
     a.entropy[row] = h < 0.f ? 0.f : h;
   }
