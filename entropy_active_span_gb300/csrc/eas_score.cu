@@ -18,7 +18,8 @@
 // there is ordered.  Order is by (value, then lower column), kept in 64 bits:
 // monotonic value bits above the complement of the column.
 //
-// Backward, with G = sum of a row's g_j and p = 2^(c x - log2 e lse):
+// Backward, with G = sum of a row's g_j and p = exp(z - lse), 1 at most (z - lse carries the
+// rounding of an lse far from 0):
 //   dx_v = scale (sum_j g_j [v == t_j] - p_v (G + g_H (z_v - lse + H))).
 #include "eas_device.cuh"
 #include "eas_launch.cuh"
@@ -149,10 +150,16 @@ __device__ __forceinline__ void add_value(Stats& st, float x, float c) {
   st = join(st, one, c);
 }
 
-// The larger of two values, NaN if one is.
+// The larger, or smaller, of two values, NaN if one is.
 __device__ __forceinline__ float max_nan(float a, float b) {
   float r;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
   return r;
 }
 
@@ -942,7 +949,7 @@ __global__ void __launch_bounds__(kThreads) score_bwd_kernel(const ScoreBwdArgs 
     c1 = -a.scale * gh;
   }
   auto value = [&](float xv) {
-    const float d = max_nan(fmaf(xv, a.scale, -lse), kLeast);
+    const float d = max_nan(min_nan(fmaf(xv, a.scale, -lse), 0.f), kLeast);
     return ex2_approx(d * kLog2e) * fmaf(c1, d, c0);
   };
   // the values at the given tokens, before dx (which may be x) is written
