@@ -3,7 +3,8 @@
 //
 // With c = scale log2 e, a row's statistics are kept in base 2:
 //   y = c x - fp32(c m),  s = sum 2^y,  u = sum 2^y y,
-//   lse = ln2 (fp32(c m) + log2 s),  logp(t) = ln2 (y_t - log2 s),
+//   lse = scale m + ln2 (log2 s - (c m - fp32(c m))),
+//   logp(t) = ln2 (y_t - log2 s),
 //   H = ln2 (log2 s - u / s),
 // (where c m is so large that its rounding would count, y = c (x - m) and c m itself below),
 // m being close to the largest x: a value is read once, each thread keeps (m, s, u) of
@@ -618,7 +619,10 @@ __device__ __forceinline__ void write_row(const ScoreFwdArgs& a, long long row, 
   }
   if (tid == 0) {
     const float cm = __fmul_rn(st.m, a.c);
-    a.lse[row] = is_far(cm) ? fmaf(kLn2, ls, st.m * a.scale) : kLn2 * (cm + ls);
+    // z_m, and what the sums leave out of c m: lse, which the gradient starts from, is within
+    // a step of its type however large it is
+    const float rest = is_far(cm) ? 0.f : fmaf(st.m, a.c, -cm);
+    a.lse[row] = fmaf(st.m, a.scale, kLn2 * (ls - rest));
     const float h = kLn2 * (ls - st.u / st.s);
     a.entropy[row] = h < 0.f ? 0.f : h;
   }
