@@ -534,14 +534,16 @@ eas_status eas_token_logprobs_bwd(const float* g_logprob, const float* g_entropy
  *   (u = g without a momentum);  X = u / (|u| + eps), the 2-norm over the matrix;
  *   for each (a, b, c) of coeffs:  Q = X X^T,  X = a X + (b Q + c Q Q) X;
  *   out = bf16(scale X).
- * Products take fp16 operands (X itself is kept in 22 bits) and fp32 sums.  With the
- * usual coefficients and n = min(rows, cols) of 64 or more, out is within 3.3e-3 of its
- * 2-norm after five steps, 1.7e-3 of which is its rounding to bf16, and within 5e-3 after
- * ten; with fewer rows, whose errors do not average out, within 1e-2 after five and several
- * times that after ten.  Coefficients whose terms cancel more carry 2^-12 of each term of
- * a step.  Where the matrix has (nearly) no part in some directions, the sums' roundings
- * there grow with the steps: 4e-8 sqrt(n) times the product of all |a| comes on top,
- * 1e-3 at n = 4096 after five usual steps, 5e-2 after eight.
+ * Products take fp16 operands (X itself is kept in 22 bits) and fp32 sums.  With five of
+ * the usual steps and n = min(rows, cols) of 64 or more, out is 1.7e-3 to 3e-3 of its
+ * 2-norm off, 1.7e-3 of which is its rounding to bf16; at worst, with a rank of two or
+ * three, 6e-3, and 1.2e-2 after seven steps.  With fewer rows or a few singular values alone
+ * errors do not average out, and each step carries them further: at worst 1.1e-2 from 8
+ * rows on and 2e-2 below after five steps, 4e-2 after seven, 1.5e-1 after ten.  Other
+ * coefficients carry 2^-12 of each of their terms a step.
+ * Where the matrix has (nearly) no part in some directions, the sums' roundings there
+ * grow with the steps: 4e-8 sqrt(n) times the product of all |a| comes on top, 1.2e-3 at
+ * n = 4096 after five usual steps, 5e-2 after eight.
  * Singular values have to stay below 4 through all steps, and |a| + |b| s^2 + |c| s^4
  * below 16 (with the usual coefficients they stay below 1.3).  Results repeat to the bit.
  * Where a matrix holds NaN or Inf, or its norm is not finite, its out is NaN.

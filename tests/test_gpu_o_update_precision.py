@@ -91,3 +91,21 @@ def test_a_triple_for_each_step(shape, rank):
     """The first ones steep; singular values stay below 2."""
     each = [(7.0, -18.0, 12.5), (4.0, -2.9, 0.55), (3.8, -2.8, 0.54), (3.2, -2.4, 0.48), (2.2, -1.6, 0.4), (1.7, -1.1, 0.35)]
     check(of_rank(shape, rank, 5), each)
+
+
+@pytest.mark.parametrize("n,m", [(1, 2), (2, 2), (2, 16), (3, 5), (5, 3), (4, 4), (8, 8), (64, 8), (16, 30), (31, 33)])
+@pytest.mark.parametrize("rank", [1, 2, 64])
+def test_few_rows(n, m, rank):
+    """Single singular values: what the roundings of a step leave, about 1e-3 of one (four of
+    2^-12 on terms of a few times the result), the next step can carry 1.7 times further (the
+    most that p' is up to the largest p, 1.13): 1e-3 (1 + 1.7 + ... + 1.7^4) = 1.9e-2, and
+    the output's rounding."""
+    g = of_rank((2000, n, m), rank, 3).cuda()
+    out = eas.orthogonalize(g).double()
+    x = g.double()
+    x = x / (x.flatten(1).norm(dim=1)[:, None, None] + 1e-7)
+    for a, b, c in (ABC,) * 5:
+        q = x @ x.mT
+        x = a * x + (b * q + c * q @ q) @ x
+    off = (out - x).flatten(1).norm(dim=1) / x.flatten(1).norm(dim=1)
+    assert float(off.max()) <= 2.1e-2 and float(off.mean()) <= 5e-3
