@@ -894,7 +894,8 @@ def fused_token_logprobs(logits, tokens=None, top_k: int = 0, scale: float = 1.0
 
 
 # Coefficients (a, b, c) of a Newton-Schulz step that raise small singular values fast
-# and bring all of them near 1 in about five steps.
+# and bring all of them near 1 in about five steps: those of Keller Jordan's description
+# of the Muon optimiser (2024).
 NEWTON_SCHULZ = (3.4445, -4.7750, 2.0315)
 
 

@@ -1430,11 +1430,14 @@ cudaError_t prepare(const MuonArgs& a, int num_sms, cudaStream_t s) {
 // Parts of a tile of A along k (where tiles are 128 x 128 or halves of that): a few long
 // products would leave most SMs idle.  A part of k-blocks takes 416 to 555 clocks each, a
 // part's sum 64 KB from L2, twice that: ten k-blocks a part at least, eight parts at most,
-// and all of them at once ([640][8192] 220 us, 228 with four parts instead of five).
-// [129][8000] 136 us, 250 in one part; [200][3000] 115 and 142.
+// and all of them at once as halves on a GB300's 152 SMs ([640][8192] 220 us, 228 with four
+// parts instead of five).  It goes by that number and not by the device's, since it decides
+// the workspace's size, which is asked for without a device; with fewer SMs the parts
+// take turns.  [129][8000] 131 us, 249 in one part; [200][3000] 109 and 139.
+constexpr long long kSplitTiles = 152 / 2;
 static long long gram_split(long long L, long long n, long long m) {
   const long long tn = (n + 127) / 128, tri = tn * (tn + 1) / 2, kb = (m + 63) / 64;
-  const long long most = L > 0 ? 76 / (L * tri) : 0, s = kb / 10 < most ? kb / 10 : most;
+  const long long most = L > 0 ? kSplitTiles / (L * tri) : 0, s = kb / 10 < most ? kb / 10 : most;
   return s > 8 ? 8 : s < 1 ? 1 : s;
 }
 
@@ -1477,13 +1480,13 @@ cudaError_t launch_muon(const MuonArgs& a, int grad_bf16, MapEncoder enc, int nu
   if (e != cudaSuccess) return e;
   // Products are deep (n or m) and few tiles wide where matrices are small, so the rule
   // goes by X's tiles of 128 x 128.  Where each SM gets half of one at most, halves, which
-  // take in 24 KB a k-block instead of 32 ([1003][777] 130 us and 143, [320][320] 87 and
-  // 99).  Where it gets few, whole ones, X X^T of few tiles in parts ([2048][2048] 259 us
-  // and 268 by pairs, [640][8192] 226 and 335).  Else 256 x 256 tiles by pairs, which take
-  // in half the bytes an operation ([2560][2560], 2.6 tiles an SM, 343 us and 400).  That
-  // matters less the less deep the products are (2 x [384][4096], 155 us and 208;
-  // 3 x [300][8000], 3.7 an SM, 232 and 327; 8 x [320][4096], 5 an SM, 275 and 269), and
-  // at 128 rows or fewer pairs would be half empty (12 x [128][4096] 157 us and 230).
+  // take in 24 KB a k-block instead of 32 ([1003][777] 128 us and 139, [320][320] 81 and
+  // 95).  Where it gets few, whole ones, X X^T of few tiles in parts ([2048][2048] 258 us
+  // and 274 by pairs, [640][8192] 221 and 336).  Else 256 x 256 tiles by pairs, which take
+  // in half the bytes an operation ([2560][2560], 2.6 tiles an SM, 349 us and 401).  That
+  // matters less the less deep the products are (2 x [384][4096], 152 us and 207;
+  // 3 x [300][8000], 3.7 an SM, 220 and 331; 8 x [320][4096], 5 an SM, 274 and 273), and
+  // at 128 rows or fewer pairs would be half empty (12 x [128][4096] 157 us and 234).
   const long long small = static_cast<long long>(a.L) * ((a.n + 127) / 128) * ((a.m + 127) / 128);
   const bool single = a.n <= 128 || 4 * small <= (a.n <= 384 ? 16LL : 9LL) * num_sms;
   return !single               ? run_steps<2, 1>(a, enc, num_sms, s)

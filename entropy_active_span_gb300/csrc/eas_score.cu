@@ -739,8 +739,8 @@ __global__ void __launch_bounds__(kThreads, 2) score_fwd_kernel(const ScoreFwdAr
 // Two CTAs an SM take rows in turn.  Eight warps walk: a thread's next vectors come by
 // cp.async into its own places of a ring in shared memory, on into the CTA's next row.
 // Three other warps, each for every third row, find the k largest and write a row's
-// outputs while the walk goes on.  [16384][128256] bf16 behind a 62 % mask: 391 us, 94 to
-// 99 % of the copy rate; 674 with a CTA a row that does one after the other.
+// outputs while the walk goes on.  [16384][128256] bf16 behind a 62 % mask: 399 us, 97 %
+// of the copy rate; 674 with a CTA a row that does one after the other.
 
 constexpr int kRowThreads = 256;                  // that walk
 constexpr int kSelect = 3;                        // warps that find the k largest
@@ -912,7 +912,10 @@ __global__ void __launch_bounds__(kRowAll, kRowCtas) score_rows_kernel(const Sco
 // ----------------------------------------------------------------- backward
 
 // Bound by its bytes: one read (of active rows) and one write, a few vectors a thread on
-// their way.  [16384][128256] bf16 behind a 62 % mask 990 us, the copy rate.
+// their way.  [16384][128256] bf16 behind a 62 % mask 999 us, the copy rate.
+// Where logits and their gradient lie differently to 16 bytes the stores are single elements:
+// [4096][32003] bf16 out of rows of 32064 to dense ones 306 us, 91 between rows of one pitch
+// (fp32 162 and 159).
 // blockIdx.x = row * split + part of the row.
 template <typename T>
 __global__ void __launch_bounds__(kThreads) score_bwd_kernel(const ScoreBwdArgs a) {

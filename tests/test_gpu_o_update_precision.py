@@ -109,3 +109,17 @@ def test_few_rows(n, m, rank):
         x = a * x + (b * q + c * q @ q) @ x
     off = (out - x).flatten(1).norm(dim=1) / x.flatten(1).norm(dim=1)
     assert float(off.max()) <= 2.1e-2 and float(off.mean()) <= 5e-3
+
+
+@pytest.mark.parametrize("shape", [(3, 100, 500), (2, 449, 128), (5, 128, 385), (4, 60, 384), (2, 128, 512)])
+def test_workspace_of_small_matrices(shape):
+    """lo beyond shared memory: inside its workspace, whatever that held, and the same again."""
+    from test_gpu_9_guard import Guarded
+    gd = Guarded(torch.device("cuda", 0))
+    g = of_rank(shape, 8, 1).cuda()
+    ws = gd.bytes(eas.orthogonalize_workspace_size(*shape))
+    ws.fill_(0xff)
+    out = gd.view(shape, torch.bfloat16)
+    eas.orthogonalize(g, ws=ws, out=out)
+    assert eas.read_device_status(ws) == 0 and torch.equal(out, eas.orthogonalize(g))
+    gd.check()
